@@ -12,6 +12,12 @@
  *   ssm_step         one-token recurrent decode step, state updated in place
  *   ssm_step_ex      the decode step with the options of ssm_scan_fwd_ex
  *   ssm_ssd_step     the same for the Mamba-2 form (scalar decay per head, (N, P) state)
+ *   ssm_linattn_fwd  linear attention with a decay per head, queries and keys per head
+ *                    or head group (prefill; padded batches)
+ *   ssm_linattn_bwd  its gradient
+ *   ssm_linattn_step its one-token decode step, optionally with the group norm and gate
+ *   ssm_group_norm_fwd, ssm_group_norm_bwd
+ *                    group norm, channels last, with activation and/or silu(z) gate
  *
  * The operation (selective SSM of Gu & Dao, "Mamba: Linear-Time Sequence
  * Modeling with Selective State Spaces", 2023, and the SSD form of Dao & Gu,
@@ -400,6 +406,155 @@ int ssm_ssd_step(int B, int H, int P, int N, ssm_dtype_t io,
                  float* state, const void* x, const void* delta, const float* A,
                  const void* Bm, const void* Cm, const float* Dskip, const void* z,
                  void* y, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * ssm_linattn_fwd -- linear attention with a decay for each head (prefill).
+ *
+ * The SSD recurrence with a constant decay per head and queries and keys of
+ * their own per head (or per group of heads, as B and C groups): per (b, h), with
+ * lam = exp(log_decay[h]) and g = h / (H / G), from S = h0[b, h] (or zeros), for
+ * t = 0 .. len_b - 1:
+ *   S[i, j]   = lam * S[i, j] + k[b,t,g,i] * v[b,t,h,j]
+ *   o[b,t,h,j] = scale * sum_i q[b,t,g,i] * S[i, j]
+ *   h_final[b, h] = S after step len_b - 1.
+ * Rows t >= len_b are padding: their q, k, v are not used and their o is 0.
+ *
+ *   q, k      : [B, L, G, K]  io dtype; G divides H
+ *   v, o      : [B, L, H, V]  io dtype
+ *   log_decay : [H]           fp32, <= 0 (0: no decay; -infinity: the current
+ *                             token only)
+ *   scale     : factor of o (usually 1 / sqrt(K))
+ *   seqlens   : [B] int32 or NULL (every length L); a value outside [0, L] is
+ *               taken as the nearest of the two
+ *   h0        : [B, H, K, V]  fp32 or NULL (zeros)
+ *   h_final   : [B, H, K, V]  fp32 out, or NULL
+ *   norm      : NULL, or the group norm and gate that follow: o becomes
+ *               ((o - mean) rstd weight + bias) silu(z) with the statistics of each
+ *               head's V values of a token, exactly what ssm_group_norm_fwd gives
+ *               on the stored o viewed as [B L, 1, H V] with H groups (padding
+ *               rows: what that gives for a row of zeros)
+ *   workspace : at least ssm_linattn_workspace_size(B, L, H, G, K, V, io) bytes
+ * Arithmetic: products of io values are exact in fp32 accumulators; the state and
+ * the decayed score matrix, formed in fp32, enter the matrix cores as pairs of
+ * bf16 numbers (about 17 significant bits) when io = SSM_BF16, as fp32 when
+ * io = SSM_F32.
+ * Supported: K, V in {64, 128}; B, H <= 65535; B * H <= 2^24. Every pointer must be
+ * 16-byte aligned; h_final must not be h0. Errors as for ssm_scan_fwd.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+    const float* weight; /* [H * V] fp32 or NULL (ones) */
+    const float* bias;   /* [H * V] fp32 or NULL (zeros) */
+    const void* z;       /* gate, the shape and dtype of o, or NULL (no gate) */
+    float eps;           /* > 0, added to the variance */
+} ssm_linattn_norm_t;
+
+size_t ssm_linattn_workspace_size(int B, int L, int H, int G, int K, int V, ssm_dtype_t io);
+
+int ssm_linattn_fwd(int B, int L, int H, int G, int K, int V, ssm_dtype_t io,
+                    const void* q, const void* k, const void* v, const float* log_decay,
+                    float scale, const int* seqlens, const float* h0,
+                    const ssm_linattn_norm_t* norm,
+                    void* o, float* h_final,
+                    void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * ssm_linattn_bwd -- gradient of ssm_linattn_fwd (without norm).
+ *
+ * For the loss  l = sum(dout * o) + sum(dh_final * h_final)  every output is dl/d(the
+ * input of the same name), with n = len_b, T = dh_final:
+ *   dq_i = scale (sum_{j<=i} lam^(i-j) (dout_i . v_j) k_j + lam^(i+1) h0 dout_i)
+ *   dk_j = scale  sum_{i>=j} lam^(i-j) (dout_i . v_j) q_i + lam^(n-1-j) T v_j
+ *   dv_j = scale  sum_{i>=j} lam^(i-j) (q_i . k_j) dout_i + lam^(n-1-j) T^t k_j
+ *   dh0  = lam^n T + scale sum_i lam^(i+1) q_i (x) dout_i
+ * dq and dk of a head group are the sums over its heads (fp32, in head order,
+ * rounded once). The decay is a constant of the model and has no gradient here.
+ *
+ *   inputs   : q, k, v, log_decay, scale, seqlens, h0 exactly as given to ssm_linattn_fwd
+ *   dout     : [B, L, H, V]  io dtype (rows t >= len_b are not used)
+ *   dh_final : [B, H, K, V]  fp32 or NULL (zeros)
+ *   dq, dk   : [B, L, G, K]  io dtype out (0 at padding)
+ *   dv       : [B, L, H, V]  io dtype out (0 at padding)
+ *   dh0      : [B, H, K, V]  fp32 out, or NULL (not written); must not be dh_final
+ *   workspace: at least ssm_linattn_bwd_workspace_size(B, L, H, G, K, V, io) bytes
+ * States are recomputed, not read from a forward call; reductions run in a fixed
+ * order. Supported sizes, alignment and errors as for ssm_linattn_fwd.
+ * ------------------------------------------------------------------------- */
+size_t ssm_linattn_bwd_workspace_size(int B, int L, int H, int G, int K, int V, ssm_dtype_t io);
+
+int ssm_linattn_bwd(int B, int L, int H, int G, int K, int V, ssm_dtype_t io,
+                    const void* q, const void* k, const void* v, const float* log_decay,
+                    float scale, const int* seqlens, const float* h0,
+                    const void* dout, const float* dh_final,
+                    void* dq, void* dk, void* dv, float* dh0,
+                    void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * ssm_linattn_step -- one-token decode step of ssm_linattn_fwd, state in place.
+ *
+ *   state : [B, H, K, V]  fp32, updated in place
+ *   q, k  : [B, G, K]     io dtype;  v, o : [B, H, V]  io dtype
+ *   norm  : as for ssm_linattn_fwd (z: [B, H, V]); here the norm takes o before it
+ *           is rounded to the io dtype
+ * Supported: K, V in {64, 128}; B * H <= 2^24. Every pointer must be 16-byte
+ * aligned. Errors as for ssm_step.
+ * ------------------------------------------------------------------------- */
+int ssm_linattn_step(int B, int H, int G, int K, int V, ssm_dtype_t io,
+                     float* state, const void* q, const void* k, const void* v,
+                     const float* log_decay, float scale, const ssm_linattn_norm_t* norm,
+                     void* o, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * ssm_group_norm_fwd -- group norm over channels-last data, with an activation
+ * and / or a gate: the output stage of linear attention (S = 1, G = heads, gate z),
+ * and the norm of the convolutional blocks around a scan (S positions, SiLU).
+ *
+ * Group g holds the channels c with c / (C / G) = g. Per sample m and group g,
+ * over the S * (C / G) values of that sample and group:
+ *   mean[m, g], var (biased), rstd[m, g] = 1 / sqrt(var + eps)
+ *   u = (x[m,s,c] - mean) * rstd * weight[c] + bias[c]
+ *   y[m,s,c] = act(u) * silu(z[m,s,c])
+ *
+ *   x, z, y      : [M, S, C]  io dtype (z may be NULL: no gate); y may be x
+ *   weight, bias : [C]        fp32, each may be NULL (ones, zeros)
+ *   mean, rstd   : [M, G]     fp32 out, both given or both NULL
+ *   act          : SSM_ACT_NONE or SSM_ACT_SILU
+ *   eps          : > 0
+ *   workspace    : at least ssm_group_norm_workspace_size(M, S, C, G, io) bytes
+ * Statistics are fp32, from squared distances to a mean (no difference of large
+ * sums). Supported: C >= 1 a multiple of G, C <= 65536; M >= 0 and S >= 1 (M = 0 does
+ * nothing); M * S * C <= 2^40, M * S < 2^31. Every pointer must be 16-byte
+ * aligned. Errors as for ssm_scan_fwd.
+ * ------------------------------------------------------------------------- */
+typedef enum { SSM_ACT_NONE = 0, SSM_ACT_SILU = 1, SSM_ACT_INT_RANGE_ = 0x7fffffff } ssm_act_t;
+
+size_t ssm_group_norm_workspace_size(int M, int S, int C, int G, ssm_dtype_t io);
+
+int ssm_group_norm_fwd(int M, int S, int C, int G, ssm_dtype_t io, ssm_act_t act,
+                       const void* x, const float* weight, const float* bias, const void* z, float eps,
+                       void* y, float* mean, float* rstd,
+                       void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * ssm_group_norm_bwd -- gradient of ssm_group_norm_fwd.
+ *
+ *   x, weight, bias, z, act : as given to ssm_group_norm_fwd; mean, rstd: its outputs
+ *   dy            : [M, S, C]  io dtype
+ *   dx            : [M, S, C]  io dtype out
+ *   dweight, dbias: [C]        fp32 out, each may be NULL (not written); given or not
+ *                              whether weight and bias are
+ *   dz            : [M, S, C]  io dtype out; given exactly when z is
+ *   workspace     : at least ssm_group_norm_bwd_workspace_size(M, S, C, G, io) bytes
+ * Outputs must not alias inputs or each other. Sums over samples and positions run
+ * in a fixed order. M = 0 writes dweight = dbias = 0. Sizes and errors as for
+ * ssm_group_norm_fwd.
+ * ------------------------------------------------------------------------- */
+size_t ssm_group_norm_bwd_workspace_size(int M, int S, int C, int G, ssm_dtype_t io);
+
+int ssm_group_norm_bwd(int M, int S, int C, int G, ssm_dtype_t io, ssm_act_t act,
+                       const void* x, const float* weight, const float* bias, const void* z,
+                       const float* mean, const float* rstd, const void* dy,
+                       void* dx, float* dweight, float* dbias, void* dz,
+                       void* workspace, size_t workspace_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------
  * Diagnostics for benchmarks (not part of the method; asynchronous on `stream`,

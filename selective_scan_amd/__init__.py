@@ -14,6 +14,15 @@ from .ops import (  # noqa: F401
     ssm_diag_copy,
     ssm_diag_stream_scale,
     ssm_diag_valu_rate,
+    ssm_group_norm_bwd,
+    ssm_group_norm_bwd_workspace_size,
+    ssm_group_norm_fwd,
+    ssm_group_norm_workspace_size,
+    ssm_linattn_bwd,
+    ssm_linattn_bwd_workspace_size,
+    ssm_linattn_fwd,
+    ssm_linattn_step,
+    ssm_linattn_workspace_size,
     ssm_scan3_fwd,
     ssm_scan3_workspace_size,
     ssm_step3,

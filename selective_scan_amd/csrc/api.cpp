@@ -11,7 +11,9 @@
 #include <string>
 
 #include "extras.h"
+#include "group_norm.h"
 #include "launch.h"
+#include "linattn.h"
 #include "scan3.h"
 #include "step3.h"
 
@@ -409,6 +411,205 @@ int ssm_ssd_step(int B, int H, int P, int N, ssm_dtype_t io,
         if (!aligned16(p)) return fail(SSM_ERR_INVALID_ARG, fn, "every pointer must be 16-byte aligned");
     ssm::SsdStepArgs a{B, H, P, N, io == SSM_BF16, state, x, delta, A, Bm, Cm, Dskip, z, y};
     return hip_status(ssm::launch_ssd_step(a, static_cast<hipStream_t>(stream)), fn);
+}
+
+// ------------------------------------------------------------------ linear attention
+}  // extern "C"
+
+namespace {
+
+// Sizes shared by the linear attention entry points; SSM_OK or the failure.
+int linattn_dims(const char* fn, int B, int L, int H, int G, int K, int V, int io) {
+    if (B < 1 || L < 0 || H < 1 || G < 1 || K < 1 || V < 1)
+        return fail(SSM_ERR_INVALID_ARG, fn, "B, H, G, K, V must be >= 1 and L >= 0");
+    if (io != SSM_F32 && io != SSM_BF16) return fail(SSM_ERR_INVALID_ARG, fn, "io must be SSM_F32 or SSM_BF16");
+    if (H % G != 0) return fail(SSM_ERR_INVALID_ARG, fn, "G must divide H");
+    if (!ssm::linattn_supported_dim(K) || !ssm::linattn_supported_dim(V))
+        return fail(SSM_ERR_UNSUPPORTED, fn, "K and V must be 64 or 128");
+    if (B > 65535 || H > 65535) return fail(SSM_ERR_UNSUPPORTED, fn, "B and H must be <= 65535");
+    if ((long long)B * H > (1LL << 24)) return fail(SSM_ERR_UNSUPPORTED, fn, "B * H must be <= 2^24");
+    if (!product_ok({B, L, H, std::max(K, V)}, 1LL << 40) || !product_ok({B, H, K, V}, 1LL << 40))
+        return fail(SSM_ERR_INVALID_ARG, fn, "tensor sizes overflow");
+    return SSM_OK;
+}
+
+bool linattn_dims_ok(int B, int L, int H, int G, int K, int V, int io) {
+    return B >= 1 && L >= 0 && H >= 1 && G >= 1 && H % G == 0 && B <= 65535 && H <= 65535 &&
+           (long long)B * H <= (1LL << 24) && (io == SSM_F32 || io == SSM_BF16) && ssm::linattn_supported_dim(K) &&
+           ssm::linattn_supported_dim(V) && product_ok({B, L, H, std::max(K, V)}, 1LL << 40) &&
+           product_ok({B, H, K, V}, 1LL << 40);
+}
+
+int linattn_norm_args(const char* fn, const ssm_linattn_norm_t* n, ssm::LinattnNorm* out) {
+    *out = ssm::LinattnNorm{false, nullptr, nullptr, nullptr, 0.0f};
+    if (!n) return SSM_OK;
+    if (!(n->eps > 0.0f)) return fail(SSM_ERR_INVALID_ARG, fn, "norm eps must be > 0");
+    if (!aligned16(n->weight) || !aligned16(n->bias) || !aligned16(n->z))
+        return fail(SSM_ERR_INVALID_ARG, fn, "every pointer must be 16-byte aligned");
+    *out = ssm::LinattnNorm{true, n->weight, n->bias, n->z, n->eps};
+    return SSM_OK;
+}
+
+// Sizes of the group norm; SSM_OK or the failure.
+int group_norm_dims(const char* fn, int M, int S, int C, int G, int io, int act) {
+    if (M < 0 || S < 1 || C < 1 || G < 1)
+        return fail(SSM_ERR_INVALID_ARG, fn, "M must be >= 0 and S, C, G >= 1");
+    if (io != SSM_F32 && io != SSM_BF16) return fail(SSM_ERR_INVALID_ARG, fn, "io must be SSM_F32 or SSM_BF16");
+    if (act != SSM_ACT_NONE && act != SSM_ACT_SILU)
+        return fail(SSM_ERR_INVALID_ARG, fn, "act must be SSM_ACT_NONE or SSM_ACT_SILU");
+    if (C % G != 0) return fail(SSM_ERR_INVALID_ARG, fn, "G must divide C");
+    if (C > 65536) return fail(SSM_ERR_UNSUPPORTED, fn, "C must be <= 65536");
+    if (!product_ok({M, S}, 0x7fffffffLL)) return fail(SSM_ERR_UNSUPPORTED, fn, "M * S must be < 2^31");
+    if (!product_ok({M, S, C}, 1LL << 40)) return fail(SSM_ERR_INVALID_ARG, fn, "tensor sizes overflow");
+    return SSM_OK;
+}
+
+bool group_norm_dims_ok(int M, int S, int C, int G, int io) {
+    return M >= 0 && S >= 1 && C >= 1 && C <= 65536 && G >= 1 && C % G == 0 && (io == SSM_F32 || io == SSM_BF16) &&
+           product_ok({M, S}, 0x7fffffffLL) && product_ok({M, S, C}, 1LL << 40);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t ssm_linattn_workspace_size(int B, int L, int H, int G, int K, int V, ssm_dtype_t io) {
+    if (!linattn_dims_ok(B, L, H, G, K, V, io)) return 0;
+    return ssm::linattn_workspace_bytes(B, L, H, G, K, V, io == SSM_BF16);
+}
+
+int ssm_linattn_fwd(int B, int L, int H, int G, int K, int V, ssm_dtype_t io,
+                    const void* q, const void* k, const void* v, const float* log_decay,
+                    float scale, const int* seqlens, const float* h0,
+                    const ssm_linattn_norm_t* norm,
+                    void* o, float* h_final,
+                    void* workspace, size_t workspace_bytes, void* stream) {
+    const char* fn = "ssm_linattn_fwd";
+    int s = linattn_dims(fn, B, L, H, G, K, V, io);
+    if (s != SSM_OK) return s;
+    if (!log_decay) return fail(SSM_ERR_INVALID_ARG, fn, "log_decay is NULL");
+    if (L > 0 && (!q || !k || !v || !o)) return fail(SSM_ERR_INVALID_ARG, fn, "q, k, v and o are required");
+    const void* ptrs[] = {q, k, v, log_decay, seqlens, h0, o, h_final, workspace};
+    for (const void* p : ptrs)
+        if (!aligned16(p)) return fail(SSM_ERR_INVALID_ARG, fn, "every pointer must be 16-byte aligned");
+    if (h0 && h0 == h_final) return fail(SSM_ERR_INVALID_ARG, fn, "h_final must not be h0");
+    ssm::LinattnNorm nm;
+    if ((s = linattn_norm_args(fn, norm, &nm)) != SSM_OK) return s;
+    if (nm.on && ((long long)H * V > 65536 || !product_ok({B, L}, 0x7fffffffLL)))
+        return fail(SSM_ERR_UNSUPPORTED, fn, "norm: H * V must be <= 65536 and B * L < 2^31");
+    const size_t need = ssm::linattn_workspace_bytes(B, L, H, G, K, V, io == SSM_BF16);
+    if (need > 0 && (workspace == nullptr || workspace_bytes < need))
+        return fail(SSM_ERR_WORKSPACE, fn, "workspace missing or smaller than ssm_linattn_workspace_size()");
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    ssm::LinattnArgs a{B, L, H, G, K, V, io == SSM_BF16, q, k, v, log_decay, scale, seqlens, h0, o, h_final, workspace};
+    const hipError_t e = ssm::launch_linattn_fwd(a, st);
+    if (e != hipSuccess || !nm.on || L == 0) return hip_status(e, fn);
+    // one position per sample: needs no workspace
+    ssm::GroupNormArgs n{B * L, 1, H * V, H, io == SSM_BF16, SSM_ACT_NONE, o, nm.weight, nm.bias, nm.z, nm.eps,
+                         o, nullptr, nullptr, nullptr};
+    return hip_status(ssm::launch_group_norm_fwd(n, st), fn);
+}
+
+size_t ssm_linattn_bwd_workspace_size(int B, int L, int H, int G, int K, int V, ssm_dtype_t io) {
+    if (!linattn_dims_ok(B, L, H, G, K, V, io)) return 0;
+    return ssm::linattn_bwd_workspace_bytes(B, L, H, G, K, V, io == SSM_BF16);
+}
+
+int ssm_linattn_bwd(int B, int L, int H, int G, int K, int V, ssm_dtype_t io,
+                    const void* q, const void* k, const void* v, const float* log_decay,
+                    float scale, const int* seqlens, const float* h0,
+                    const void* dout, const float* dh_final,
+                    void* dq, void* dk, void* dv, float* dh0,
+                    void* workspace, size_t workspace_bytes, void* stream) {
+    const char* fn = "ssm_linattn_bwd";
+    const int s = linattn_dims(fn, B, L, H, G, K, V, io);
+    if (s != SSM_OK) return s;
+    if (!log_decay) return fail(SSM_ERR_INVALID_ARG, fn, "log_decay is NULL");
+    if (L > 0 && (!q || !k || !v || !dout || !dq || !dk || !dv))
+        return fail(SSM_ERR_INVALID_ARG, fn, "q, k, v, dout, dq, dk and dv are required");
+    const void* ptrs[] = {q, k, v, log_decay, seqlens, h0, dout, dh_final, dq, dk, dv, dh0, workspace};
+    for (const void* p : ptrs)
+        if (!aligned16(p)) return fail(SSM_ERR_INVALID_ARG, fn, "every pointer must be 16-byte aligned");
+    if (dh0 && dh0 == dh_final) return fail(SSM_ERR_INVALID_ARG, fn, "dh0 must not be dh_final");
+    const size_t need = ssm::linattn_bwd_workspace_bytes(B, L, H, G, K, V, io == SSM_BF16);
+    if (need > 0 && (workspace == nullptr || workspace_bytes < need))
+        return fail(SSM_ERR_WORKSPACE, fn, "workspace missing or smaller than ssm_linattn_bwd_workspace_size()");
+    ssm::LinattnBwdArgs a{B, L, H, G, K, V, io == SSM_BF16, q, k, v, log_decay, scale, seqlens, h0, dout, dh_final,
+                          dq, dk, dv, dh0, workspace};
+    return hip_status(ssm::launch_linattn_bwd(a, static_cast<hipStream_t>(stream)), fn);
+}
+
+int ssm_linattn_step(int B, int H, int G, int K, int V, ssm_dtype_t io,
+                     float* state, const void* q, const void* k, const void* v,
+                     const float* log_decay, float scale, const ssm_linattn_norm_t* norm,
+                     void* o, void* stream) {
+    const char* fn = "ssm_linattn_step";
+    int s = linattn_dims(fn, B, 1, H, G, K, V, io);
+    if (s != SSM_OK) return s;
+    if (!state || !q || !k || !v || !log_decay || !o)
+        return fail(SSM_ERR_INVALID_ARG, fn, "state, q, k, v, log_decay and o are required");
+    const void* ptrs[] = {state, q, k, v, log_decay, o};
+    for (const void* p : ptrs)
+        if (!aligned16(p)) return fail(SSM_ERR_INVALID_ARG, fn, "every pointer must be 16-byte aligned");
+    ssm::LinattnNorm nm;
+    if ((s = linattn_norm_args(fn, norm, &nm)) != SSM_OK) return s;
+    ssm::LinattnStepArgs a{B, H, G, K, V, io == SSM_BF16, state, q, k, v, log_decay, scale, nm, o};
+    return hip_status(ssm::launch_linattn_step(a, static_cast<hipStream_t>(stream)), fn);
+}
+
+// ------------------------------------------------------------------ group norm
+size_t ssm_group_norm_workspace_size(int M, int S, int C, int G, ssm_dtype_t io) {
+    if (!group_norm_dims_ok(M, S, C, G, io)) return 0;
+    return ssm::group_norm_workspace_bytes(M, S, C, G, io == SSM_BF16);
+}
+
+int ssm_group_norm_fwd(int M, int S, int C, int G, ssm_dtype_t io, ssm_act_t act,
+                       const void* x, const float* weight, const float* bias, const void* z, float eps,
+                       void* y, float* mean, float* rstd,
+                       void* workspace, size_t workspace_bytes, void* stream) {
+    const char* fn = "ssm_group_norm_fwd";
+    const int s = group_norm_dims(fn, M, S, C, G, io, act);
+    if (s != SSM_OK) return s;
+    if (!(eps > 0.0f)) return fail(SSM_ERR_INVALID_ARG, fn, "eps must be > 0");
+    if (M > 0 && (!x || !y)) return fail(SSM_ERR_INVALID_ARG, fn, "x and y are required");
+    if ((mean == nullptr) != (rstd == nullptr))
+        return fail(SSM_ERR_INVALID_ARG, fn, "mean and rstd must be given together");
+    const void* ptrs[] = {x, weight, bias, z, y, mean, rstd, workspace};
+    for (const void* p : ptrs)
+        if (!aligned16(p)) return fail(SSM_ERR_INVALID_ARG, fn, "every pointer must be 16-byte aligned");
+    const size_t need = ssm::group_norm_workspace_bytes(M, S, C, G, io == SSM_BF16);
+    if (need > 0 && (workspace == nullptr || workspace_bytes < need))
+        return fail(SSM_ERR_WORKSPACE, fn, "workspace missing or smaller than ssm_group_norm_workspace_size()");
+    ssm::GroupNormArgs a{M, S, C, G, io == SSM_BF16, act, x, weight, bias, z, eps, y, mean, rstd, workspace};
+    return hip_status(ssm::launch_group_norm_fwd(a, static_cast<hipStream_t>(stream)), fn);
+}
+
+size_t ssm_group_norm_bwd_workspace_size(int M, int S, int C, int G, ssm_dtype_t io) {
+    if (!group_norm_dims_ok(M, S, C, G, io)) return 0;
+    return ssm::group_norm_bwd_workspace_bytes(M, S, C, G, io == SSM_BF16);
+}
+
+int ssm_group_norm_bwd(int M, int S, int C, int G, ssm_dtype_t io, ssm_act_t act,
+                       const void* x, const float* weight, const float* bias, const void* z,
+                       const float* mean, const float* rstd, const void* dy,
+                       void* dx, float* dweight, float* dbias, void* dz,
+                       void* workspace, size_t workspace_bytes, void* stream) {
+    const char* fn = "ssm_group_norm_bwd";
+    const int s = group_norm_dims(fn, M, S, C, G, io, act);
+    if (s != SSM_OK) return s;
+    if (M > 0 && (!x || !mean || !rstd || !dy || !dx))
+        return fail(SSM_ERR_INVALID_ARG, fn, "x, mean, rstd, dy and dx are required");
+    if (M > 0 && (z == nullptr) != (dz == nullptr))
+        return fail(SSM_ERR_INVALID_ARG, fn, "dz must be given exactly when z is");
+    const void* ptrs[] = {x, weight, bias, z, mean, rstd, dy, dx, dweight, dbias, dz, workspace};
+    for (const void* p : ptrs)
+        if (!aligned16(p)) return fail(SSM_ERR_INVALID_ARG, fn, "every pointer must be 16-byte aligned");
+    const size_t need = ssm::group_norm_bwd_workspace_bytes(M, S, C, G, io == SSM_BF16);
+    if (need > 0 && (workspace == nullptr || workspace_bytes < need))
+        return fail(SSM_ERR_WORKSPACE, fn, "workspace missing or smaller than ssm_group_norm_bwd_workspace_size()");
+    ssm::GroupNormBwdArgs a{M, S, C, G, io == SSM_BF16, act, x, weight, bias, z, mean, rstd, dy, dx, dweight, dbias,
+                            dz, workspace};
+    return hip_status(ssm::launch_group_norm_bwd(a, static_cast<hipStream_t>(stream)), fn);
 }
 
 // ------------------------------------------------------------------ diagnostics

@@ -63,6 +63,21 @@ def lib():
     L.ssm_ssd_step.restype = i
     L.ssm_step3.argtypes = [i, i, i, i] + [fp] + [vp] * 12 + [vp]
     L.ssm_step3.restype = i
+    f = ctypes.c_float
+    L.ssm_linattn_workspace_size.argtypes, L.ssm_linattn_workspace_size.restype = [i] * 7, sz
+    L.ssm_linattn_fwd.argtypes = [i] * 7 + [vp] * 4 + [f] + [vp] * 5 + [vp, sz, vp]
+    L.ssm_linattn_fwd.restype = i
+    L.ssm_linattn_bwd_workspace_size.argtypes, L.ssm_linattn_bwd_workspace_size.restype = [i] * 7, sz
+    L.ssm_linattn_bwd.argtypes = [i] * 7 + [vp] * 4 + [f] + [vp] * 8 + [vp, sz, vp]
+    L.ssm_linattn_bwd.restype = i
+    L.ssm_linattn_step.argtypes = [i] * 6 + [vp] * 5 + [f] + [vp] * 3
+    L.ssm_linattn_step.restype = i
+    L.ssm_group_norm_workspace_size.argtypes, L.ssm_group_norm_workspace_size.restype = [i] * 5, sz
+    L.ssm_group_norm_fwd.argtypes = [i] * 6 + [vp] * 4 + [f] + [vp] * 3 + [vp, sz, vp]
+    L.ssm_group_norm_fwd.restype = i
+    L.ssm_group_norm_bwd_workspace_size.argtypes, L.ssm_group_norm_bwd_workspace_size.restype = [i] * 5, sz
+    L.ssm_group_norm_bwd.argtypes = [i] * 6 + [vp] * 11 + [vp, sz, vp]
+    L.ssm_group_norm_bwd.restype = i
     L.ssm_diag_valu_rate.argtypes, L.ssm_diag_valu_rate.restype = [i, i, i, vp, vp], i
     L.ssm_diag_stream_scale.argtypes, L.ssm_diag_stream_scale.restype = [vp, sz, ctypes.c_float, vp], i
     L.ssm_diag_copy.argtypes, L.ssm_diag_copy.restype = [vp, vp, sz, vp], i
@@ -420,6 +435,247 @@ def ssm_step3(state, x, delta, lam, Are, theta, Bm, Cm, D=None, z=None, x_prev=N
     if st != SSM_OK:
         _raise("ssm_step3", st)
     return y
+
+
+# ------------------------------------------------------------------ linear attention
+class _LinattnNorm(ctypes.Structure):
+    """ssm_linattn_norm_t"""
+    _fields_ = [("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("z", ctypes.c_void_p),
+                ("eps", ctypes.c_float)]
+
+
+def _device_of(t):
+    """Makes the tensors' device current for the launch where it is not."""
+    return (contextlib.nullcontext() if not t.is_cuda or torch.cuda.current_device() == t.device.index
+            else torch.cuda.device(t.device))
+
+
+def _norm_arg(eps, weight, bias, z, HV, shape, io, dev):
+    """The norm argument of the linear attention calls (None without norm_eps)."""
+    if eps is None:
+        if weight is not None or bias is not None or z is not None:
+            raise ValueError("norm_weight, norm_bias and z need norm_eps")
+        return None
+    _check(weight, "norm_weight", (HV,), torch.float32, dev, required=False)
+    _check(bias, "norm_bias", (HV,), torch.float32, dev, required=False)
+    _check(z, "z", shape, io, dev, required=False)
+    return ctypes.byref(_LinattnNorm(_ptr(weight), _ptr(bias), _ptr(z), float(eps)))
+
+
+def ssm_linattn_workspace_size(B, L, H, G, K, V, io=SSM_BF16):
+    return int(lib().ssm_linattn_workspace_size(B, L, H, G, K, V, io))
+
+
+def ssm_linattn_fwd(q, k, v, log_decay, *, scale=None, seqlens=None, h0=None, norm_eps=None, norm_weight=None,
+                    norm_bias=None, z=None, o=None, h_final=None, workspace=None, stream=None,
+                    want_final_state=True):
+    """Linear attention with a decay per head. q, k: [B, L, G, K]; v: [B, L, H, V] (bf16 or
+    fp32; G divides H); log_decay: [H] fp32, <= 0; scale: K ** -0.5 by default; seqlens: [B]
+    int32, rows past a length are padding (o is 0 there); h0: [B, H, K, V] fp32. With
+    ``norm_eps`` o goes through the per-head group norm (norm_weight, norm_bias: [H * V]
+    fp32) and the gate silu(z). Returns (o [B, L, H, V], h_final [B, H, K, V])."""
+    B, L, G, K = q.shape
+    H, V = v.shape[2], v.shape[3]
+    dev, io = q.device, q.dtype
+    code = _io_code(q)
+    _check(q, "q", (B, L, G, K), io, dev)
+    _check(k, "k", (B, L, G, K), io, dev)
+    _check(v, "v", (B, L, H, V), io, dev)
+    _check(log_decay, "log_decay", (H,), torch.float32, dev)
+    _check(seqlens, "seqlens", (B,), torch.int32, dev, required=False)
+    _check(h0, "h0", (B, H, K, V), torch.float32, dev, required=False)
+    norm = _norm_arg(norm_eps, norm_weight, norm_bias, z, H * V, (B, L, H, V), io, dev)
+    need = ssm_linattn_workspace_size(B, L, H, G, K, V, code)
+    with _on(stream):
+        if o is None:
+            o = torch.empty((B, L, H, V), dtype=io, device=dev)
+        if want_final_state and h_final is None:
+            h_final = torch.empty((B, H, K, V), dtype=torch.float32, device=dev)
+        if workspace is None and need > 0:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    _check(o, "o", (B, L, H, V), io, dev)
+    _check(h_final, "h_final", (B, H, K, V), torch.float32, dev, required=False)
+    wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    with _device_of(q):
+        st = lib().ssm_linattn_fwd(B, L, H, G, K, V, code, _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay),
+                                   K ** -0.5 if scale is None else float(scale), _ptr(seqlens), _ptr(h0), norm,
+                                   _ptr(o), _ptr(h_final), _ptr(workspace), wbytes, _stream(dev, stream))
+    if st != SSM_OK:
+        _raise("ssm_linattn_fwd", st)
+    return o, h_final
+
+
+def ssm_linattn_bwd_workspace_size(B, L, H, G, K, V, io=SSM_BF16):
+    return int(lib().ssm_linattn_bwd_workspace_size(B, L, H, G, K, V, io))
+
+
+def ssm_linattn_bwd(q, k, v, log_decay, dout, *, scale=None, seqlens=None, h0=None, dh_final=None, want_dh0=True,
+                    out=None, workspace=None, stream=None):
+    """Gradient of ``ssm_linattn_fwd`` (without norm) for l = sum(dout * o) + sum(dh_final *
+    h_final). Inputs as for ``ssm_linattn_fwd``; dout: [B, L, H, V]; dh_final: [B, H, K, V]
+    fp32 or None. Returns a dict with dq, dk [B, L, G, K], dv [B, L, H, V] (0 at padding) and
+    dh0 [B, H, K, V] fp32 (None unless want_dh0). ``out`` may supply any of these tensors."""
+    B, L, G, K = q.shape
+    H, V = v.shape[2], v.shape[3]
+    dev, io = q.device, q.dtype
+    code = _io_code(q)
+    _check(q, "q", (B, L, G, K), io, dev)
+    _check(k, "k", (B, L, G, K), io, dev)
+    _check(v, "v", (B, L, H, V), io, dev)
+    _check(log_decay, "log_decay", (H,), torch.float32, dev)
+    _check(dout, "dout", (B, L, H, V), io, dev)
+    _check(seqlens, "seqlens", (B,), torch.int32, dev, required=False)
+    _check(h0, "h0", (B, H, K, V), torch.float32, dev, required=False)
+    _check(dh_final, "dh_final", (B, H, K, V), torch.float32, dev, required=False)
+    shapes = dict(dq=((B, L, G, K), io), dk=((B, L, G, K), io), dv=((B, L, H, V), io),
+                  dh0=((B, H, K, V), torch.float32))
+    g = dict(out or {})
+    need = ssm_linattn_bwd_workspace_size(B, L, H, G, K, V, code)
+    with _on(stream):
+        for n, (shp, dt) in shapes.items():
+            if n == "dh0" and not want_dh0:
+                g[n] = None
+                continue
+            if g.get(n) is None:
+                g[n] = torch.empty(shp, dtype=dt, device=dev)
+            else:
+                _check(g[n], n, shp, dt, dev)
+        if workspace is None and need > 0:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    with _device_of(q):
+        st = lib().ssm_linattn_bwd(B, L, H, G, K, V, code, _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay),
+                                   K ** -0.5 if scale is None else float(scale), _ptr(seqlens), _ptr(h0),
+                                   _ptr(dout), _ptr(dh_final), *(_ptr(g[n]) for n in ("dq", "dk", "dv", "dh0")),
+                                   _ptr(workspace), wbytes, _stream(dev, stream))
+    if st != SSM_OK:
+        _raise("ssm_linattn_bwd", st)
+    return g
+
+
+def ssm_linattn_step(state, q, k, v, log_decay, *, scale=None, norm_eps=None, norm_weight=None, norm_bias=None,
+                     z=None, o=None, stream=None):
+    """One decode step of ``ssm_linattn_fwd``. state: [B, H, K, V] fp32 (updated in place);
+    q, k: [B, G, K]; v, z: [B, H, V]; log_decay: [H]; norm arguments as there. Returns o
+    [B, H, V]."""
+    B, H, K, V = state.shape
+    G = q.shape[1]
+    dev, io = q.device, q.dtype
+    code = _io_code(q)
+    _check(state, "state", (B, H, K, V), torch.float32, dev)
+    _check(q, "q", (B, G, K), io, dev)
+    _check(k, "k", (B, G, K), io, dev)
+    _check(v, "v", (B, H, V), io, dev)
+    _check(log_decay, "log_decay", (H,), torch.float32, dev)
+    norm = _norm_arg(norm_eps, norm_weight, norm_bias, z, H * V, (B, H, V), io, dev)
+    if o is None:
+        with _on(stream):
+            o = torch.empty((B, H, V), dtype=io, device=dev)
+    else:
+        _check(o, "o", (B, H, V), io, dev)
+    with _device_of(q):
+        st = lib().ssm_linattn_step(B, H, G, K, V, code, _ptr(state), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay),
+                                    K ** -0.5 if scale is None else float(scale), norm, _ptr(o),
+                                    _stream(dev, stream))
+    if st != SSM_OK:
+        _raise("ssm_linattn_step", st)
+    return o
+
+
+# ------------------------------------------------------------------ group norm
+SSM_ACT = {"none": 0, "silu": 1}
+
+
+def _norm_dims(x):
+    """(M, S, C) of x [M, C] (one position per sample) or [M, S, C]."""
+    if x.dim() not in (2, 3):
+        raise ValueError(f"x must be [M, C] or [M, S, C], got shape {tuple(x.shape)}")
+    return (x.shape[0], 1, x.shape[1]) if x.dim() == 2 else tuple(x.shape)
+
+
+def ssm_group_norm_workspace_size(M, S, C, G, io=SSM_BF16):
+    return int(lib().ssm_group_norm_workspace_size(M, S, C, G, io))
+
+
+def ssm_group_norm_fwd(x, groups, weight=None, bias=None, z=None, *, eps=1e-5, act="none", y=None, mean=None,
+                       rstd=None, workspace=None, stream=None):
+    """Group norm, channels last: y = act((x - mean) rstd weight + bias) [silu(z)]. x, z: [M, S, C]
+    (statistics over the S positions and a group's C / groups channels) or [M, C] (S = 1), bf16
+    or fp32; weight, bias: [C] fp32; act: "none" | "silu"; y may be x. Returns (y, mean, rstd),
+    mean and rstd [M, groups] fp32."""
+    M, S, C = _norm_dims(x)
+    dev, io, G = x.device, x.dtype, int(groups)
+    code = _io_code(x)
+    _check(x, "x", x.shape, io, dev)
+    _check(weight, "weight", (C,), torch.float32, dev, required=False)
+    _check(bias, "bias", (C,), torch.float32, dev, required=False)
+    _check(z, "z", x.shape, io, dev, required=False)
+    need = ssm_group_norm_workspace_size(M, S, C, G, code)
+    with _on(stream):
+        if y is None:
+            y = torch.empty(x.shape, dtype=io, device=dev)
+        if mean is None:
+            mean = torch.empty((M, G), dtype=torch.float32, device=dev)
+        if rstd is None:
+            rstd = torch.empty((M, G), dtype=torch.float32, device=dev)
+        if workspace is None and need > 0:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    _check(y, "y", x.shape, io, dev)
+    _check(mean, "mean", (M, G), torch.float32, dev)
+    _check(rstd, "rstd", (M, G), torch.float32, dev)
+    wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    with _device_of(x):
+        st = lib().ssm_group_norm_fwd(M, S, C, G, code, SSM_ACT[act], _ptr(x), _ptr(weight), _ptr(bias), _ptr(z),
+                                      float(eps), _ptr(y), _ptr(mean), _ptr(rstd), _ptr(workspace), wbytes,
+                                      _stream(dev, stream))
+    if st != SSM_OK:
+        _raise("ssm_group_norm_fwd", st)
+    return y, mean, rstd
+
+
+def ssm_group_norm_bwd_workspace_size(M, S, C, G, io=SSM_BF16):
+    return int(lib().ssm_group_norm_bwd_workspace_size(M, S, C, G, io))
+
+
+def ssm_group_norm_bwd(x, groups, mean, rstd, dy, weight=None, bias=None, z=None, *, act="none", want_affine=True,
+                       out=None, workspace=None, stream=None):
+    """Gradient of ``ssm_group_norm_fwd`` for l = sum(dy * y), from its inputs and its mean and
+    rstd. Returns a dict with dx, dweight, dbias [C] fp32 (None unless want_affine), dz (None
+    without z). ``out`` may supply any of these tensors."""
+    M, S, C = _norm_dims(x)
+    dev, io, G = x.device, x.dtype, int(groups)
+    code = _io_code(x)
+    _check(x, "x", x.shape, io, dev)
+    _check(mean, "mean", (M, G), torch.float32, dev)
+    _check(rstd, "rstd", (M, G), torch.float32, dev)
+    _check(dy, "dy", x.shape, io, dev)
+    _check(weight, "weight", (C,), torch.float32, dev, required=False)
+    _check(bias, "bias", (C,), torch.float32, dev, required=False)
+    _check(z, "z", x.shape, io, dev, required=False)
+    shapes = dict(dx=(x.shape, io), dweight=((C,), torch.float32), dbias=((C,), torch.float32), dz=(x.shape, io))
+    wanted = dict(dweight=want_affine, dbias=want_affine, dz=z is not None)
+    g = dict(out or {})
+    need = ssm_group_norm_bwd_workspace_size(M, S, C, G, code)
+    with _on(stream):
+        for n, (shp, dt) in shapes.items():
+            if not wanted.get(n, True):
+                g[n] = None
+                continue
+            if g.get(n) is None:
+                g[n] = torch.empty(shp, dtype=dt, device=dev)
+            else:
+                _check(g[n], n, shp, dt, dev)
+        if workspace is None and need > 0:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    with _device_of(x):
+        st = lib().ssm_group_norm_bwd(M, S, C, G, code, SSM_ACT[act], _ptr(x), _ptr(weight), _ptr(bias), _ptr(z),
+                                      _ptr(mean), _ptr(rstd), _ptr(dy),
+                                      *(_ptr(g[n]) for n in ("dx", "dweight", "dbias", "dz")),
+                                      _ptr(workspace), wbytes, _stream(dev, stream))
+    if st != SSM_OK:
+        _raise("ssm_group_norm_bwd", st)
+    return g
 
 
 # ------------------------------------------------------------------ diagnostics

@@ -1,0 +1,235 @@
+"""Group norm, channels last, on the GPU against its 64-bit definition: forward and
+gradient over types, group widths from 1 channel up, odd sizes, one position to
+thousands, gate and activation."""
+import pytest
+import torch
+
+import linattn_ref as ref
+import selective_scan_amd as ssa
+from gpu_util import DEV
+
+pytestmark = pytest.mark.gpu
+
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+def make(M, S, C, G, dtype, seed, offset=1.0, affine=True, gate=False):
+    g = torch.Generator().manual_seed(seed)
+    r = lambda *s: torch.randn(s, generator=g)  # noqa: E731
+    spread = torch.exp(0.5 * r(1, 1, G, 1))
+    x = (r(M, S, G, C // G) * spread + offset * r(1, 1, G, 1)).reshape(M, S, C)
+    return dict(x=x.to(dtype), w=r(C) if affine else None, b=r(C) if affine else None,
+                z=r(M, S, C).to(dtype) if gate else None, dy=r(M, S, C).to(dtype))
+
+
+def check(t, G, act, eps=1e-5, what=""):
+    M, S, C = t["x"].shape
+    n = S * (C // G)
+    dt = t["x"].dtype
+    d = {k: (v.to(DEV) if v is not None else None) for k, v in t.items()}
+    y, mean, rstd = ssa.ssm_group_norm_fwd(d["x"], G, d["w"], d["b"], d["z"], eps=eps, act=act)
+    torch.cuda.synchronize()
+    ry, rm, rr = ref.norm_fwd(t["x"], G, t["w"], t["b"], t["z"], eps=eps, act=act)
+    # sums of n terms: s relative to the sum of absolute values
+    s = ref.sum_error(n)
+    one = lambda v: v.reshape(M, S, G, C // G)  # noqa: E731
+    flat = lambda v: v.expand(M, S, G, C // G).reshape(M, S, C)  # noqa: E731
+    xabs = one(t["x"].double().abs()).mean(dim=(1, 3))
+    ref.close(mean, rm, xabs, s, what + " mean")
+    # the variance from squared distances to a mean that is s xabs off: relative s + (s xabs rstd)^2
+    ref.close(rstd, rr, rr, 4 * s + (s * xabs * rr).max().item() ** 2, what + " rstd")
+    xhat = flat((one(t["x"].double()) - rm[:, None, :, None]) * rr[:, None, :, None])
+    off = flat((s * xabs * rr)[:, None, :, None]) + 2.0 ** -22 * flat(
+        (one(t["x"].double()).abs() + rm.abs()[:, None, :, None]) * rr[:, None, :, None]) + 4 * s * xhat.abs()  # in xhat
+    wa = torch.ones(C).double() if t["w"] is None else t["w"].double().abs()
+    ba = torch.zeros(C).double() if t["b"] is None else t["b"].double().abs()
+    u = xhat * (1 if t["w"] is None else t["w"].double()) + (0 if t["b"] is None else t["b"].double())
+    du = wa * off + 2.0 ** -22 * (wa * xhat.abs() + ba)                                        # in u
+    sg = (u.abs() + 8) * 2.0 ** -23                                                         # relative, sigmoid(u)
+    va = 1.1 * du + u.abs() * sg if act == "silu" else du                                  # |silu'| <= 1.1
+    val = (u * ref.sigmoid(u)).abs() if act == "silu" else u.abs()
+    if t["z"] is not None:
+        z = t["z"].double()
+        gz, sz = (z * ref.sigmoid(z)).abs(), (z.abs() + 8) * 2.0 ** -23
+        ve = va * gz * (1 + sz) + val * gz * sz
+    else:
+        gz, sz, ve = torch.ones_like(val), torch.zeros_like(val), va
+    ref.close(y, ry, ve + 2.0 ** -23 * ry.abs(), 1.0, what + " y", store=dt)
+
+    # the gradient takes the statistics it is given: those of the reference, in 32 bits
+    m32, r32 = rm.float(), rr.float()
+    g = ssa.ssm_group_norm_bwd(d["x"], G, m32.to(DEV), r32.to(DEV), d["dy"], d["w"], d["b"], d["z"], act=act)
+    torch.cuda.synchronize()
+    r = ref.norm_bwd(t["x"], G, m32, r32, t["dy"], t["w"], t["b"], t["z"], act=act)
+    xh = flat((one(t["x"].double()) - m32.double()[:, None, :, None]) * r32.double()[:, None, :, None])
+    oh = 2.0 ** -22 * flat((one(t["x"].double()).abs() + m32.double().abs()[:, None, :, None])
+                           * r32.double()[:, None, :, None])                               # error of xhat
+    ou = wa * oh + 2.0 ** -22 * (wa * xh.abs() + ba)                                          # error of u
+    dy = t["dy"].double().abs()
+    slope, oslope = (1.1, 0.5 * ou + 4 * (u.abs() + 8) * 2.0 ** -23) if act == "silu" else (1.0, 0.0)  # |silu''| <= 0.5
+    if t["z"] is not None:
+        # silu'(z) = s (1 + z (1 - s)): its parts are at most 1 + |z| s (1 - s) <= 1.3
+        vo = 1.1 * ou + u.abs() * (u.abs() + 8) * 2.0 ** -23 if act == "silu" else ou
+        ref.close(g["dz"], r["dz"], dy * (vo * 1.1 + val * 1.3 * 4 * sz), 1.0, what + " dz", store=dt)
+    else:
+        assert g["dz"] is None
+    e = dy * gz * (oslope + slope * (sz + 2.0 ** -21))                                         # error of du
+    big = dy * gz * slope
+    rows = M * S
+    sr = ref.sum_error(rows)
+    ref.close(g["dbias"], r["dbias"], (e + sr * big).sum(dim=(0, 1)), 1.0, what + " dbias", store=F32)
+    ref.close(g["dweight"], r["dweight"], (e * xh.abs() + big * (oh + (sr + 2.0 ** -22) * xh.abs())).sum(dim=(0, 1)), 1.0,
+              what + " dweight", store=F32)
+    en, bn = e * wa + 2.0 ** -23 * big * wa, big * wa
+    mean_ = lambda v: flat(one(v).mean(dim=(1, 3), keepdim=True))  # noqa: E731
+    dxe = (en + mean_(en + s * bn) + oh * mean_(bn * xh.abs())
+           + xh.abs() * mean_(en * xh.abs() + bn * (oh + s * xh.abs()))
+           + 2.0 ** -21 * (bn + mean_(bn) + xh.abs() * mean_(bn * xh.abs())))
+    ref.close(g["dx"], r["dx"], flat(r32.double()[:, None, :, None]) * dxe, 1.0, what + " dx", store=dt)
+    return y, mean, rstd, g
+
+
+SHAPES = [
+    # M, S, C, G
+    (1, 1, 1, 1), (3, 1, 7, 7), (2, 1, 24, 3), (5, 1, 512, 8), (33, 1, 1536, 24), (4, 1, 2048, 16), (2, 1, 4100, 1),
+    (3, 1, 640, 2), (7, 1, 1000, 8), (2, 1, 65536, 2),
+    (1, 2, 8, 2), (2, 5, 40, 4), (2, 64, 320, 32), (1, 1025, 320, 32), (3, 333, 96, 3), (2, 17, 33, 11), (1, 700, 64, 64),
+    (2, 4096, 64, 8), (1, 3, 5000, 5), (1, 9000, 6, 2), (40, 12, 128, 4), (1, 50, 65536, 64),
+]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("act,gate", [("none", True), ("silu", False)], ids=["gate", "silu"])
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "x".join(map(str, s)))
+def test_forward_and_gradient(shape, act, gate, dtype):
+    check(make(*shape, dtype, seed=sum(shape), gate=gate), shape[3], act, what=str(shape))
+
+
+@pytest.mark.parametrize("act", ["none", "silu"])
+@pytest.mark.parametrize("gate", [False, True])
+@pytest.mark.parametrize("affine", [False, True])
+def test_every_combination(act, gate, affine):
+    for shape in ((9, 1, 256, 4), (2, 130, 48, 6)):
+        check(make(*shape, BF16, seed=3, gate=gate, affine=affine), shape[3], act, what=f"{shape} {act} {gate} {affine}")
+
+
+@pytest.mark.parametrize("shape", [(4, 1, 512, 8), (2, 600, 64, 8)], ids=str)
+def test_a_large_common_offset(shape):
+    """Values 300 times their spread: a difference of large sums would lose the variance."""
+    t = make(*shape, F32, seed=5)
+    t["x"] = t["x"] + 300.0
+    check(t, shape[3], "none")
+
+
+@pytest.mark.parametrize("shape", [(3, 1, 128, 4), (2, 40, 24, 4)], ids=str)
+def test_constant_groups(shape):
+    """No spread at all: xhat is 0, y the bias, and nothing divides by zero."""
+    t = make(*shape, F32, seed=7)
+    t["x"] = torch.full(shape[:3], 2.5)
+    y, mean, rstd = ssa.ssm_group_norm_fwd(t["x"].to(DEV), shape[3], t["w"].to(DEV), t["b"].to(DEV))
+    assert torch.equal(y.cpu(), t["b"].expand(shape[:3])) and (mean == 2.5).all()
+    assert torch.allclose(rstd.cpu(), torch.full_like(rstd.cpu(), 1e-5 ** -0.5), rtol=1e-6)
+
+
+@pytest.mark.parametrize("shape", [(5, 1, 256, 4), (2, 30, 48, 4)], ids=str)
+def test_a_group_with_nan_or_infinity_leaves_the_others(shape):
+    M, S, C, G = shape
+    t = make(*shape, BF16, seed=9, gate=True)
+    good, _, _ = ssa.ssm_group_norm_fwd(t["x"].to(DEV), G, t["w"].to(DEV), t["b"].to(DEV), t["z"].to(DEV))
+    cg = C // G
+    t["x"][0, 0, 0] = float("nan")
+    t["x"][1, S - 1, C - 1] = float("inf")
+    y, _, _ = ssa.ssm_group_norm_fwd(t["x"].to(DEV), G, t["w"].to(DEV), t["b"].to(DEV), t["z"].to(DEV))
+    assert torch.isnan(y[0, :, :cg]).all() and torch.isnan(y[1, :, C - cg:]).all()
+    y[0, :, :cg] = good[0, :, :cg]
+    y[1, :, C - cg:] = good[1, :, C - cg:]
+    assert torch.equal(y, good)
+
+
+def test_far_gates_and_activations():
+    """silu far out: 0 on the left, the value itself on the right, no NaN."""
+    x = torch.randn(2, 1, 64, generator=torch.Generator().manual_seed(1))
+    z = torch.tensor([-1e30, -200.0, -90.0, 0.0, 90.0, 200.0, 1e30, -0.0] * 8).expand(2, 1, 64).contiguous()
+    t = dict(x=x, w=None, b=torch.full((64,), 1.0), z=z, dy=torch.ones(2, 1, 64))
+    y, mean, rstd = ssa.ssm_group_norm_fwd(x.to(DEV), 4, None, t["b"].to(DEV), z.to(DEV))
+    g = ssa.ssm_group_norm_bwd(x.to(DEV), 4, mean, rstd, t["dy"].to(DEV), None, t["b"].to(DEV), z.to(DEV))
+    assert torch.isfinite(y).all() and all(torch.isfinite(g[n]).all() for n in ("dx", "dz", "dweight", "dbias"))
+    w = torch.full((64,), 200.0)
+    y, mean, rstd = ssa.ssm_group_norm_fwd(x.to(DEV), 4, w.to(DEV), None, act="silu")
+    g = ssa.ssm_group_norm_bwd(x.to(DEV), 4, mean, rstd, t["dy"].to(DEV), w.to(DEV), act="silu")
+    assert torch.isfinite(y).all() and all(torch.isfinite(g[n]).all() for n in ("dx", "dweight", "dbias"))
+
+
+@pytest.mark.parametrize("shape", [(6, 1, 512, 8), (2, 300, 96, 6)], ids=str)
+def test_in_place_and_the_same_bits_twice(shape):
+    M, S, C, G = shape
+    t = {k: (v.to(DEV) if v is not None else None) for k, v in make(*shape, BF16, seed=11, gate=True).items()}
+    y, mean, rstd = ssa.ssm_group_norm_fwd(t["x"], G, t["w"], t["b"], t["z"])
+    y2, _, _ = ssa.ssm_group_norm_fwd(t["x"], G, t["w"], t["b"], t["z"])
+    x = t["x"].clone()
+    ssa.ssm_group_norm_fwd(x, G, t["w"], t["b"], t["z"], y=x)
+    assert torch.equal(y, y2) and torch.equal(y, x)
+    a, b = (ssa.ssm_group_norm_bwd(t["x"], G, mean, rstd, t["dy"], t["w"], t["b"], t["z"]) for _ in range(2))
+    assert all(torch.equal(a[n], b[n]) for n in a)
+    c = ssa.ssm_group_norm_bwd(t["x"], G, mean, rstd, t["dy"], t["w"], t["b"], t["z"], want_affine=False)
+    assert c["dweight"] is None and torch.equal(c["dx"], a["dx"]) and torch.equal(c["dz"], a["dz"])
+
+
+def test_gradient_against_differences_of_the_forward():
+    """Central differences of the 64-bit sum of the GPU's forward, step 2^-6 (error of the difference: the
+    step squared times the third derivative, and the rounding of y over the step)."""
+    for shape, act, gate in (((4, 1, 64, 4), "none", True), ((2, 20, 24, 4), "silu", False)):
+        M, S, C, G = shape
+        t = {k: (v.to(DEV) if v is not None else None) for k, v in make(*shape, F32, seed=13, gate=gate).items()}
+        _, mean, rstd = ssa.ssm_group_norm_fwd(t["x"], G, t["w"], t["b"], t["z"], act=act)
+        g = ssa.ssm_group_norm_bwd(t["x"], G, mean, rstd, t["dy"], t["w"], t["b"], t["z"], act=act)
+
+        def loss(**kw):
+            u = {**t, **kw}
+            y, _, _ = ssa.ssm_group_norm_fwd(u["x"], G, u["w"], u["b"], u["z"], act=act)
+            return float((y.double() * t["dy"].double()).sum())
+
+        gen = torch.Generator().manual_seed(15)
+        for name, grad in (("x", "dx"), ("w", "dweight"), ("b", "dbias"), ("z", "dz")):
+            if t[name] is None:
+                continue
+            step = torch.randn(t[name].shape, generator=gen).to(DEV)
+            h = 2.0 ** -6
+            diff = (loss(**{name: t[name] + h * step}) - loss(**{name: t[name] - h * step})) / (2 * h)
+            wide = (loss(**{name: t[name] + 2 * h * step}) - loss(**{name: t[name] - 2 * h * step})) / (4 * h)
+            got = float((g[grad].double() * step.double()).sum())
+            # the two widths differ by three times the narrow one's truncation error; rounding of y: 2^-20 of
+            # sum |dy y| over the step
+            y, _, _ = ssa.ssm_group_norm_fwd(t["x"], G, t["w"], t["b"], t["z"], act=act)
+            tol = abs(wide - diff) + 2.0 ** -20 / h * float((y.double() * t["dy"].double()).abs().sum()) + 1e-6
+            assert abs(diff - got) <= tol, (name, diff, got, tol)
+
+
+def test_no_samples():
+    x = torch.empty((0, 5, 24), device=DEV)
+    y, mean, rstd = ssa.ssm_group_norm_fwd(x, 4)
+    assert y.shape == x.shape and mean.shape == (0, 4)
+    g = ssa.ssm_group_norm_bwd(x, 4, mean, rstd, x)
+    torch.cuda.synchronize()
+    assert not g["dweight"].any() and not g["dbias"].any()
+
+
+def test_nothing_is_written_outside_the_outputs():
+    for M, S, C, G in ((3, 1, 72, 9), (2, 33, 20, 4), (1, 1, 1000, 8)):
+        t = {k: (v.to(DEV) if v is not None else None) for k, v in make(M, S, C, G, BF16, seed=17, gate=True).items()}
+
+        def framed(shape, dtype):
+            n = 1
+            for s in shape:
+                n *= s
+            buf = torch.full((n + 2048,), 7.0, dtype=dtype, device=DEV)
+            return buf, buf[1024:1024 + n].view(shape)
+
+        bufs, v = zip(*(framed(s, d) for s, d in (((M, S, C), BF16), ((M, G), F32), ((M, G), F32), ((M, S, C), BF16),
+                                                  ((C,), F32), ((C,), F32), ((M, S, C), BF16))))
+        ssa.ssm_group_norm_fwd(t["x"], G, t["w"], t["b"], t["z"], y=v[0], mean=v[1], rstd=v[2])
+        ssa.ssm_group_norm_bwd(t["x"], G, v[1], v[2], t["dy"], t["w"], t["b"], t["z"],
+                               out=dict(dx=v[3], dweight=v[4], dbias=v[5], dz=v[6]))
+        torch.cuda.synchronize()
+        for buf in bufs:
+            assert (buf[:1024] == 7).all() and (buf[-1024:] == 7).all()
