@@ -9,12 +9,63 @@
 //   dv: backwards on (k, q, dout), from T; what leaves at the front is dh0
 // Backwards in time the decay follows the read-out instead of preceding the update
 // (R_t = P_{t+1} + x2_t (x) x3_t, out_t = x1_t . R_t, P_t = lam R_t, P_n = T).
+//
+// By chunks of 64 steps (rows i, j of a chunk of n <= 64 steps; S the state entering it):
+//   forwards   out_i = lam^(i+1) x1_i S + sum_{j <= i} lam^(i-j) (x1_i . x2_j) x3_j
+//              S    <- lam^n S + sum_j lam^(n-1-j) x2_j (x) x3_j
+//   backwards  out_i = lam^(n-1-i) x1_i S + sum_{j >= i} lam^(j-i) (x1_i . x2_j) x3_j
+//              S    <- lam^n S + sum_j lam^(j+1) x2_j (x) x3_j
+// Every power has an exponent >= 0, so none can overflow.
+//
+// Kernels. A sequence is cut into super-chunks (runs of chunks), one workgroup per
+// (batch, head, super-chunk):
+//   mix_chunks<AGG>   every super-chunk but the last in the run's direction: its state
+//                     from a zero start
+//   mix_carry         per state element, over the super-chunks: the state entering each
+//   mix_chunks        the outputs, from that state
+// One wave owns 32 columns of the state (all KD rows, fp32, in its accumulators) and
+// the same columns of the output. The state never leaves the registers: an
+// accumulator tile of v_mfma_f32_32x32x16_bf16 holds column c = lane % 32 and, per half
+// wave hf, rows 8 (r / 4) + 4 hf + r % 4, while an operand wants eight consecutive
+// contraction indices per lane. Feeding the operand that makes the tile's rows in the
+// order pi(m) = m with bits 2 and 3 exchanged turns registers 0-7 and 8-15 into rows
+// 8 hf .. 8 hf + 7 and 16 + 8 hf .. 16 + 8 hf + 7, exactly two operands. The same holds
+// for the scores x2_j . x1_i (rows j) that multiply x3, and, with the columns of the
+// state in the order pi, for the output tile, whose lanes then hold eight consecutive
+// columns of one row: 16-byte stores.
+// Operands stored in bf16 enter exactly; those formed in fp32 (state, decayed scores,
+// weighted x3) enter as hi = bf16(x) and lo = bf16(x - hi), two products, about 17
+// significant bits (one bf16 rounding would cost 1e-3 of the result). With fp32
+// storage every product is v_mfma_f32_32x32x2_f32.
 #include "common.h"
 #include "launch.h"
 #include "linattn.h"
 
+#include <algorithm>
+
 namespace ssm {
 namespace {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef short i16x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+// LDS-typed pointers keep the address arithmetic in 32 bits
+typedef __attribute__((address_space(3))) char lds_t;
+typedef __attribute__((address_space(3))) float lds_f32;
+typedef __attribute__((address_space(3))) f32x4 lds_f32x4;
+typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
+typedef __attribute__((address_space(3))) bf16x8 lds_bf16x8;
+typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
+
+constexpr int kC = 64;  // steps per chunk
+#ifndef SSM_LINATTN_BLOCKS
+#define SSM_LINATTN_BLOCKS 512
+#endif
+constexpr int kTargetBlocks = SSM_LINATTN_BLOCKS;
 
 // One run of the operator: x1, x2 [B, L, ., KD], x3 [B, L, ., VD], out [B, L, H, VD].
 struct Mix {
@@ -27,17 +78,28 @@ struct Mix {
     const int* seqlens;
     float out_scale;      // factor of every output
     float kv_scale;       // factor of x2 (x) x3
-    const float* init;    // [B, H, KD, VD], transposed ([B, H, VD, KD]) if init_t; or NULL
-    int init_t;
+    const float* init;    // [B, H, KD, VD], transposed ([B, H, VD, KD]) if trans; or NULL
+    float* slots;         // [B, H, NS - 1, KD, VD] (or transposed): entering states
+    int trans;
     void* out;            // io dtype, or fp32 if out_f32
     int out_f32;
     float* final_state;   // [B, H, KD, VD] or NULL
 };
 
-template <bool BF16>
-__device__ __forceinline__ float ld1(const void* p, size_t i) {
-    if constexpr (BF16) return bf16_to_f32(static_cast<const uint16_t*>(p)[i]);
-    else return static_cast<const float*>(p)[i];
+struct Geom {
+    int NC;   // chunks per sequence
+    int cps;  // chunks per super-chunk
+    int NS;   // super-chunks per sequence
+};
+
+Geom geom(int B, int L, int H) {
+    Geom g;
+    g.NC = std::max(1, (L + kC - 1) / kC);
+    const long bh = (long)B * H;
+    const long want = std::max<long>(1, std::min<long>((kTargetBlocks + bh - 1) / bh, g.NC));
+    g.cps = (int)((g.NC + want - 1) / want);
+    g.NS = (g.NC + g.cps - 1) / g.cps;
+    return g;
 }
 
 template <bool BF16>
@@ -50,56 +112,386 @@ __device__ __forceinline__ int seq_len(const int* seqlens, int b, int L) {
     return seqlens ? max(0, min(seqlens[b], L)) : L;
 }
 
-// One workgroup per (batch, head), one lane per column of the state, the recurrence
-// step by step; rows of x1 and x2 pass through LDS kT steps at a time.
-template <int KD, int VD, bool BF16, bool REV>
-__global__ void __launch_bounds__(VD) mix_kernel(Mix a) {
-    constexpr int kT = 16;
-    __shared__ float s1[kT][KD], s2[kT][KD];
-    const int bh = blockIdx.x, b = bh / a.H, h = bh % a.H, j = threadIdx.x;
-    const int G = a.H / a.r;
-    const int h1 = a.g1 ? h / a.r : h, n1 = a.g1 ? G : a.H;
-    const int h2 = a.g2 ? h / a.r : h, n2 = a.g2 ? G : a.H;
-    const int h3 = a.g3 ? h / a.r : h, n3 = a.g3 ? G : a.H;
-    const int len = seq_len(a.seqlens, b, a.L);
-    const Decay decay(a.log_decay[h]);
-    float S[KD];
+// log_decay, kept finite so that 0 steps of it are 0 (exp(-1e4) is 0 as well)
+__device__ __forceinline__ float log_decay_of(const float* p, int h) {
+    const float a = p[h];
+    return a < -1e4f ? -1e4f : a;
+}
+
+__device__ __forceinline__ int pi(int m) { return (m & 0x13) | ((m & 4) << 1) | ((m & 8) >> 1); }
+
+// Operands of a 32 x 32 x 16 product: lane l holds row (or column) l % 32 and the eight
+// contraction indices 8 (l / 32) + e.
+template <bool BF16> struct Types;
+template <> struct Types<true> {
+    typedef bf16x8 Op;
+    struct Formed { bf16x8 hi, lo; };
+    static constexpr int es = 2, pad = 8;
+    static __device__ __forceinline__ f32x16 mma(Op a, Op b, f32x16 c) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+    }
+    static __device__ __forceinline__ f32x16 mma(const Formed& a, Op b, f32x16 c) { return mma(a.lo, b, mma(a.hi, b, c)); }
+    static __device__ __forceinline__ f32x16 mma(Op a, const Formed& b, f32x16 c) { return mma(a, b.lo, mma(a, b.hi, c)); }
+    static __device__ __forceinline__ Formed form(f32x8 v) {
+        Formed f;
 #pragma unroll
-    for (int i = 0; i < KD; ++i)
-        S[i] = !a.init ? 0.0f
-               : a.init_t ? a.init[((size_t)bh * VD + j) * KD + i] : a.init[((size_t)bh * KD + i) * VD + j];
-    for (int c0 = 0; c0 < a.L; c0 += kT) {
-        const int n = min(kT, a.L - c0);
-        __syncthreads();
-        for (int e = j; e < n * KD; e += VD) {
-            const int u = e / KD, i = e % KD, t = REV ? a.L - 1 - (c0 + u) : c0 + u;
-            const size_t row = (size_t)b * a.L + t;
-            s1[u][i] = t < len ? ld1<BF16>(a.x1, (row * n1 + h1) * KD + i) : 0.0f;
-            s2[u][i] = t < len ? ld1<BF16>(a.x2, (row * n2 + h2) * KD + i) * a.kv_scale : 0.0f;
+        for (int e = 0; e < 8; ++e) {
+            f.hi[e] = (__bf16)v[e];
+            f.lo[e] = (__bf16)(v[e] - (float)f.hi[e]);
         }
-        __syncthreads();
-        for (int u = 0; u < n; ++u) {
-            const int t = REV ? a.L - 1 - (c0 + u) : c0 + u;
-            const size_t row = (size_t)b * a.L + t;
-            float y = 0.0f;
-            if (t < len) {
-                const float w = ld1<BF16>(a.x3, (row * n3 + h3) * VD + j);
+        return f;
+    }
+    static __device__ __forceinline__ f32x8 widen(Op a) {
+        f32x8 v;
 #pragma unroll
-                for (int i = 0; i < KD; ++i) {
-                    if constexpr (!REV) S[i] = decay(S[i]);
-                    S[i] = __builtin_fmaf(s2[u][i], w, S[i]);
-                    y = __builtin_fmaf(s1[u][i], S[i], y);
-                    if constexpr (REV) S[i] = decay(S[i]);
-                }
-            }
-            const size_t at = (row * a.H + h) * VD + j;
-            if (a.out_f32) static_cast<float*>(a.out)[at] = y * a.out_scale;
-            else st1<BF16>(a.out, at, y * a.out_scale);
+        for (int e = 0; e < 8; ++e) v[e] = (float)a[e];
+        return v;
+    }
+    // elements c0 .. c0 + 7 of row `row` of an LDS tile with rows of `rs` bytes
+    static __device__ __forceinline__ Op row8(const lds_t* t, int rs, int row, int c0) {
+        return *reinterpret_cast<const lds_bf16x8*>(t + row * rs + c0 * 2);
+    }
+    // rows r0 + 8 (l / 32) + e of column c0 + pi(l % 32): the LDS transpose read hands lane
+    // i of a 16-lane group column i of the group's 16, made of the four 4-column pieces
+    // its lanes point at; pointing at the pieces in the order 0, 2, 1, 3 gives pi
+    static __device__ __forceinline__ Op col8(const lds_t* t, int rs, int r0, int c0) {
+        const int l = threadIdx.x & 63, i = l & 15, q = i & 3;
+        const lds_t* p = t + (r0 + 8 * (l >> 5) + (i >> 2)) * rs + (c0 + (l & 16) + 4 * ((q >> 1) | ((q & 1) << 1))) * 2;
+        const bf16x4 a = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)p));
+        const bf16x4 b = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p + 4 * rs)));
+        return bf16x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+    }
+};
+template <> struct Types<false> {
+    typedef f32x8 Op;
+    typedef f32x8 Formed;
+    static constexpr int es = 4, pad = 4;
+    static __device__ __forceinline__ f32x16 mma(const f32x8& a, const f32x8& b, f32x16 c) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[e], b[e], c, 0, 0, 0);
+        return c;
+    }
+    static __device__ __forceinline__ Formed form(f32x8 v) { return v; }
+    static __device__ __forceinline__ f32x8 widen(const Op& a) { return a; }
+    static __device__ __forceinline__ Op row8(const lds_t* t, int rs, int row, int c0) {
+        const lds_t* p = t + row * rs + c0 * 4;
+        const f32x4 a = *reinterpret_cast<const lds_f32x4*>(p), b = *reinterpret_cast<const lds_f32x4*>(p + 16);
+        return f32x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+    }
+    static __device__ __forceinline__ Op col8(const lds_t* t, int rs, int r0, int c0) {
+        const int l = threadIdx.x & 63;
+        const lds_t* p = t + (r0 + 8 * (l >> 5)) * rs + (c0 + pi(l & 31)) * 4;
+        f32x8 v;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = *reinterpret_cast<const lds_f32*>(p + e * rs);
+        return v;
+    }
+};
+
+__device__ __forceinline__ f32x8 half_of(const f32x16& a, int s) {
+    f32x8 v;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = a[8 * s + e];
+    return v;
+}
+
+// Rows of a chunk of one of x1, x2, x3: D values of one head per step.
+template <int D, int NT, bool BF16>
+struct Rows {
+    static constexpr int P = D * Types<BF16>::es / 16;  // 16-byte pieces per row
+    static constexpr int N = kC * P / NT;               // pieces per thread
+    static constexpr int RS = (D + Types<BF16>::pad) * Types<BF16>::es;  // LDS row stride (bytes)
+    static constexpr int BYTES = kC * RS;
+    u32x4 v[N];
+    // rows t0 .. t0 + n - 1 (the others as zeros: out of the buffer's range)
+    __device__ __forceinline__ void load(const void* x, size_t b, int L, int nh, int h, int t0, int n) {
+        const uint32_t row = (uint32_t)nh * D * Types<BF16>::es;
+        const char* base = static_cast<const char*>(x) + ((b * L + t0) * nh + h) * (size_t)(D * Types<BF16>::es);
+        const auto r = make_rsrc(base, (uint32_t)(n - 1) * row + D * Types<BF16>::es);
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const int q = threadIdx.x + k * NT;
+            // rows past n are kept out of range explicitly: their offset may fall in the
+            // last row's range of a narrow head slice otherwise
+            const uint32_t off = (uint32_t)(q / P) * row + (q % P) * 16;
+            v[k] = __builtin_amdgcn_raw_buffer_load_b128(r, (int)(q / P < n ? off : 0x80000000u), 0, 0);
         }
     }
-    if (a.final_state)
+    __device__ __forceinline__ void store(lds_t* t) const {
 #pragma unroll
-        for (int i = 0; i < KD; ++i) a.final_state[((size_t)bh * KD + i) * VD + j] = S[i];
+        for (int k = 0; k < N; ++k) {
+            const int q = threadIdx.x + k * NT;
+            *reinterpret_cast<lds_u32x4*>(t + (q / P) * RS + (q % P) * 16) = v[k];
+        }
+    }
+};
+
+// Workgroup -> (head, super-chunk, batch). Workgroups go round-robin to the 8 XCDs
+// (each with its own L2); consecutive coordinates, heads fastest, go to one XCD where
+// the count allows, so that heads sharing queries and keys share its L2.
+__device__ __forceinline__ void block_coords(int H, int Kp, int& h, int& k, int& b) {
+    const int total = (int)gridDim.x, id = (int)blockIdx.x;
+    const int idp = (total % 8 == 0) ? (id % 8) * (total / 8) + id / 8 : id;
+    h = idp % H;
+    const int r = idp / H;
+    k = r % Kp;
+    b = r / Kp;
+}
+
+// The state tiles of one wave: rows k = 32 T + 16 (r / 8) + 8 hf + r % 8, column
+// 32 wave + pi(lane % 32), of a [KD, VD] matrix (or its transpose) in memory.
+template <int KD, int VD, typename F>
+__device__ __forceinline__ void each_state_element(bool trans, F&& f) {
+    const int lane = threadIdx.x & 63, hf = lane >> 5;
+    const int col = 32 * (threadIdx.x >> 6) + pi(lane & 31);
+#pragma unroll
+    for (int T = 0; T < KD / 32; ++T)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            const int k = 32 * T + 16 * (r >> 3) + 8 * hf + (r & 7);
+            f(T, r, trans ? col * KD + k : k * VD + col);
+        }
+}
+
+template <int KD, int VD, bool BF16, bool REV, bool AGG>
+__global__ void __launch_bounds__(2 * VD) mix_chunks(Mix a, Geom geo) {
+    typedef Types<BF16> Ty;
+    typedef typename Ty::Op Op;
+    constexpr int NT = 2 * VD, KS = KD / 16, KT = KD / 32;
+    typedef Rows<KD, NT, BF16> RowsK;
+    typedef Rows<VD, NT, BF16> RowsV;
+    constexpr int X2 = 0, X3 = X2 + RowsK::BYTES, W = X3 + RowsV::BYTES, TAB = W + 128 * 4,
+                  X1 = TAB + (AGG ? 0 : 2 * 4 * 64 * 16), TOTAL = X1 + (AGG ? 0 : RowsK::BYTES);
+    __shared__ __attribute__((aligned(16))) char lds_raw[TOTAL];
+    lds_t* lds = (lds_t*)lds_raw;
+    int h, sc, b;
+    block_coords(a.H, AGG ? geo.NS - 1 : geo.NS, h, sc, b);
+    if (AGG && REV) ++sc;
+    const int tid = threadIdx.x, lane = tid & 63, hf = lane >> 5, c = lane & 31;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const size_t bh = (size_t)b * a.H + h;
+    const int G = a.H / a.r, hg = h / a.r;
+    const int h1 = a.g1 ? hg : h, n1 = a.g1 ? G : a.H;
+    const int h2 = a.g2 ? hg : h, n2 = a.g2 ? G : a.H;
+    const int h3 = a.g3 ? hg : h, n3 = a.g3 ? G : a.H;
+    const int len = seq_len(a.seqlens, b, a.L);
+    const float la = log_decay_of(a.log_decay, h), la2 = la * kLog2e;
+    auto power = [&](int n) { return exp2_fast((float)n * la2); };
+
+    // chunks [c0, c1) of this super-chunk, of which [c0, ca) hold steps of the sequence
+    const int c0 = sc * geo.cps, c1 = min(geo.NC, c0 + geo.cps);
+    const int ca = max(c0, min(c1, (len + kC - 1) / kC));
+
+    // the state entering the super-chunk
+    f32x16 S[KT];
+#pragma unroll
+    for (int T = 0; T < KT; ++T)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) S[T][r] = 0.0f;
+    if constexpr (!AGG) {
+        const bool first = REV ? sc == geo.NS - 1 : sc == 0;
+        const float* src = first ? (a.init ? a.init + bh * KD * VD : nullptr)
+                                 : a.slots + (bh * (geo.NS - 1) + (REV ? sc : sc - 1)) * KD * VD;
+        if (src) each_state_element<KD, VD>(a.trans, [&](int T, int r, int at) { S[T][r] = src[at]; });
+    }
+
+    // W[x]: weight of row j of x3 in the state's update; forwards lam^(n-1-j) = W[j + 64 - n],
+    // backwards lam^(j+1) = W[j]; times kv_scale
+    lds_f32* wt = reinterpret_cast<lds_f32*>(lds + W);
+    for (int x = tid; x < 128; x += NT) wt[x] = x < kC ? power(REV ? x + 1 : kC - 1 - x) * a.kv_scale : 0.0f;
+    // decay of the scores: this lane's 16 factors of a tile on the diagonal (masked) and of
+    // the one off it; row i = 32 I + c, column j = 32 J + 16 (r / 8) + 8 hf + r % 8
+    lds_f32x4* tab = reinterpret_cast<lds_f32x4*>(lds + TAB);
+    if constexpr (!AGG) {
+        if (tid < 64) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                f32x4 d0, d1;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int j = 16 * (q >> 1) + 8 * hf + 4 * (q & 1) + e, lag = REV ? j - c : c - j;
+                    d0[e] = lag >= 0 ? power(lag) * a.kv_scale : 0.0f;
+                    d1[e] = power(32 + lag) * a.kv_scale;
+                }
+                tab[q * 64 + lane] = d0;
+                tab[(4 + q) * 64 + lane] = d1;
+            }
+        }
+    }
+
+    RowsK r1, r2;
+    RowsV r3;
+    auto load = [&](int ch) {
+        const int t0 = ch * kC, n = min(kC, len - t0);
+        if constexpr (!AGG) r1.load(a.x1, b, a.L, n1, h1, t0, n);
+        r2.load(a.x2, b, a.L, n2, h2, t0, n);
+        r3.load(a.x3, b, a.L, n3, h3, t0, n);
+    };
+    auto stage = [&]() {
+        if constexpr (!AGG) r1.store(lds + X1);
+        r2.store(lds + X2);
+        r3.store(lds + X3);
+    };
+
+    // outputs of this wave's 32 columns of row block I (rows t0 + 32 I + c)
+    auto put = [&](int t0, int I, const f32x16& acc) {
+        const int row = 32 * I + c;
+        if (t0 + row >= a.L) return;
+        const size_t at = ((size_t)((size_t)b * a.L + t0 + row) * a.H + h) * VD + 32 * wave + 8 * hf;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            if (BF16 && !a.out_f32) {
+                bf16x8 y;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[e] = (__bf16)(acc[8 * s + e] * a.out_scale);
+                *reinterpret_cast<bf16x8*>(static_cast<uint16_t*>(a.out) + at + 16 * s) = y;
+            } else {
+                f32x4* p = reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + at + 16 * s);
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    f32x4 y;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) y[e] = acc[8 * s + 4 * u + e] * a.out_scale;
+                    p[u] = y;
+                }
+            }
+        }
+    };
+
+    if constexpr (!AGG) {  // chunks of padding alone
+        f32x16 zero;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) zero[r] = 0.0f;
+        for (int ch = ca; ch < c1; ++ch)
+            for (int I = 0; I < 2; ++I) put(ch * kC, I, zero);
+    }
+    const int nch = ca - c0;
+    auto chunk_at = [&](int u) { return REV ? ca - 1 - u : c0 + u; };
+    if (nch > 0) {
+        load(chunk_at(0));
+        stage();
+    }
+    __syncthreads();
+    for (int u = 0; u < nch; ++u) {
+        const int t0 = chunk_at(u) * kC, n = min(kC, len - t0);
+        if (u + 1 < nch) load(chunk_at(u + 1));
+        Op v[4];
+#pragma unroll
+        for (int s = 0; s < 4; ++s) v[s] = Ty::col8(lds + X3, RowsV::RS, 16 * s, 32 * wave);
+        if constexpr (!AGG) {
+            f32x16 acc[2], m00, m11, mx;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[0][r] = acc[1][r] = m00[r] = m11[r] = mx[r] = 0.0f;
+            // scores (rows j in the order pi, columns i) and x1 S (rows: columns of S)
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+                const Op q0 = Ty::row8(lds + X1, RowsK::RS, c, 16 * ks + 8 * hf);
+                const Op q1 = Ty::row8(lds + X1, RowsK::RS, 32 + c, 16 * ks + 8 * hf);
+                const Op k0 = Ty::row8(lds + X2, RowsK::RS, pi(c), 16 * ks + 8 * hf);
+                const Op k1 = Ty::row8(lds + X2, RowsK::RS, 32 + pi(c), 16 * ks + 8 * hf);
+                const typename Ty::Formed sf = Ty::form(half_of(S[ks >> 1], ks & 1));
+                m00 = Ty::mma(k0, q0, m00);
+                m11 = Ty::mma(k1, q1, m11);
+                mx = REV ? Ty::mma(k1, q0, mx) : Ty::mma(k0, q1, mx);
+                acc[0] = Ty::mma(sf, q0, acc[0]);
+                acc[1] = Ty::mma(sf, q1, acc[1]);
+            }
+            const float w0 = power(REV ? max(n - 1 - c, 0) : c + 1), w1 = power(REV ? max(n - 33 - c, 0) : c + 33);
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                acc[0][r] *= w0;
+                acc[1][r] *= w1;
+            }
+            auto decayed = [&](const f32x16& m, int which, int s) {
+                const f32x4 d0 = tab[(4 * which + 2 * s) * 64 + lane], d1 = tab[(4 * which + 2 * s + 1) * 64 + lane];
+                f32x8 x;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    x[e] = m[8 * s + e] * d0[e];
+                    x[4 + e] = m[8 * s + 4 + e] * d1[e];
+                }
+                return Ty::form(x);
+            };
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                acc[0] = Ty::mma(v[s], decayed(m00, 0, s), acc[0]);
+                acc[1] = Ty::mma(v[2 + s], decayed(m11, 0, s), acc[1]);
+                if constexpr (REV) acc[0] = Ty::mma(v[2 + s], decayed(mx, 1, s), acc[0]);
+                else acc[1] = Ty::mma(v[s], decayed(mx, 1, s), acc[1]);
+            }
+            if (n < kC) {  // rows of padding are 0 whatever the state holds
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    if (c >= n) acc[0][r] = 0.0f;
+                    if (32 + c >= n) acc[1][r] = 0.0f;
+                }
+            }
+            put(t0, 0, acc[0]);
+            put(t0, 1, acc[1]);
+        }
+        if (AGG || u + 1 < nch || a.final_state) {
+            const Decay decay(la * (float)n);
+#pragma unroll
+            for (int T = 0; T < KT; ++T)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) S[T][r] = decay(S[T][r]);
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                f32x8 x = Ty::widen(v[s]);
+                const lds_f32* w = wt + 16 * s + 8 * hf + (REV ? 0 : kC - n);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] *= w[e];
+                const typename Ty::Formed wv = Ty::form(x);
+#pragma unroll
+                for (int T = 0; T < KT; ++T)
+                    S[T] = Ty::mma(Ty::col8(lds + X2, RowsK::RS, 16 * s, 32 * T), wv, S[T]);
+            }
+        }
+        __syncthreads();
+        if (u + 1 < nch) {
+            stage();
+            __syncthreads();
+        }
+    }
+
+    float* dst = nullptr;
+    if constexpr (AGG) dst = a.slots + (bh * (geo.NS - 1) + (REV ? sc - 1 : sc)) * KD * VD;
+    else if (a.final_state && (REV ? sc == 0 : sc == geo.NS - 1)) dst = a.final_state + bh * KD * VD;
+    if (dst) each_state_element<KD, VD>(AGG && a.trans, [&](int T, int r, int at) { dst[at] = S[T][r]; });
+}
+
+// Aggregates -> entering states, in the run's direction: what super-chunk s adds, plus
+// lam^(its steps) times the state entering it, enters the next. One lane per four
+// state elements; eight slots are loaded before any is written.
+__global__ void __launch_bounds__(256) mix_carry(Mix a, Geom geo, int n4, int rev) {
+    const int e = blockIdx.x * 256 + threadIdx.x;
+    const int bh = blockIdx.y, b = bh / a.H, h = bh % a.H;
+    if (e >= n4) return;
+    const int len = seq_len(a.seqlens, b, a.L), K = geo.NS - 1;
+    const float la = log_decay_of(a.log_decay, h);
+    const float4* init = reinterpret_cast<const float4*>(a.init);
+    float4* slot = reinterpret_cast<float4*>(a.slots) + (size_t)bh * K * n4 + e;
+    float4 v = init ? init[(size_t)bh * n4 + e] : make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k0 = 0; k0 < K; k0 += 8) {
+        float4 sl[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int k = min(k0 + j, K - 1);
+            sl[j] = slot[(size_t)(rev ? K - 1 - k : k) * n4];
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int k = k0 + j;
+            if (k >= K) break;
+            const int sc = rev ? K - k : k, t0 = sc * geo.cps * kC;
+            const Decay decay(la * (float)max(0, min(len - t0, geo.cps * kC)));
+            v.x = decay(v.x) + sl[j].x;
+            v.y = decay(v.y) + sl[j].y;
+            v.z = decay(v.z) + sl[j].z;
+            v.w = decay(v.w) + sl[j].w;
+            slot[(size_t)(rev ? K - 1 - k : k) * n4] = v;
+        }
+    }
 }
 
 // Sum over the r heads of each group of an fp32 [rows, G, r, D] tensor, in head order,
@@ -114,63 +506,86 @@ __global__ void __launch_bounds__(256) sum_heads(const float* __restrict__ p, vo
     st1<BF16>(out, e, s);
 }
 
-template <int KD, int VD, bool BF16>
-hipError_t run_mix_t(const Mix& m, bool rev, hipStream_t st) {
-    const dim3 grid((unsigned)m.B * m.H);
-    if (rev) launch((mix_kernel<KD, VD, BF16, true>), grid, dim3(VD), 0, st, m);
-    else launch((mix_kernel<KD, VD, BF16, false>), grid, dim3(VD), 0, st, m);
+// With agg, the aggregates and the carry first (where there is more than one
+// super-chunk); without, the slots already hold the entering states.
+template <int KD, int VD, bool BF16, bool REV>
+hipError_t run_mix_t(const Mix& m, bool agg, hipStream_t st) {
+    const Geom g = geom(m.B, m.L, m.H);
+    const dim3 block(2 * VD);
+    hipError_t e;
+    if (agg && g.NS > 1) {
+        launch((mix_chunks<KD, VD, BF16, REV, true>), dim3((unsigned)m.B * m.H * (g.NS - 1)), block, 0, st, m, g);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+        const int n4 = KD * VD / 4;
+        launch(mix_carry, dim3((n4 + 255) / 256, (unsigned)m.B * m.H), dim3(256), 0, st, m, g, n4, (int)REV);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    launch((mix_chunks<KD, VD, BF16, REV, false>), dim3((unsigned)m.B * m.H * g.NS), block, 0, st, m, g);
     return hipGetLastError();
 }
 
-hipError_t run_mix(const Mix& m, int KD, int VD, bool bf16, bool rev, hipStream_t st) {
-    if (KD == 64 && VD == 64) return bf16 ? run_mix_t<64, 64, true>(m, rev, st) : run_mix_t<64, 64, false>(m, rev, st);
-    if (KD == 64) return bf16 ? run_mix_t<64, 128, true>(m, rev, st) : run_mix_t<64, 128, false>(m, rev, st);
-    if (VD == 64) return bf16 ? run_mix_t<128, 64, true>(m, rev, st) : run_mix_t<128, 64, false>(m, rev, st);
-    return bf16 ? run_mix_t<128, 128, true>(m, rev, st) : run_mix_t<128, 128, false>(m, rev, st);
+template <int KD, int VD>
+hipError_t run_mix_d(const Mix& m, bool bf16, bool rev, bool agg, hipStream_t st) {
+    if (bf16) return rev ? run_mix_t<KD, VD, true, true>(m, agg, st) : run_mix_t<KD, VD, true, false>(m, agg, st);
+    return rev ? run_mix_t<KD, VD, false, true>(m, agg, st) : run_mix_t<KD, VD, false, false>(m, agg, st);
+}
+
+hipError_t run_mix(const Mix& m, int KD, int VD, bool bf16, bool rev, bool agg, hipStream_t st) {
+    if (KD == 64) return VD == 64 ? run_mix_d<64, 64>(m, bf16, rev, agg, st) : run_mix_d<64, 128>(m, bf16, rev, agg, st);
+    return VD == 64 ? run_mix_d<128, 64>(m, bf16, rev, agg, st) : run_mix_d<128, 128>(m, bf16, rev, agg, st);
 }
 
 hipError_t run_sum_heads(const float* p, void* out, size_t n, int r, int D, bool bf16, hipStream_t st) {
+    if (n == 0) return hipSuccess;
     const dim3 grid((unsigned)((n + 255) / 256));
     if (bf16) launch(sum_heads<true>, grid, dim3(256), 0, st, p, out, n, r, D);
     else launch(sum_heads<false>, grid, dim3(256), 0, st, p, out, n, r, D);
     return hipGetLastError();
 }
 
+size_t slot_bytes(int B, int L, int H, int K, int V) {
+    return (size_t)B * H * (geom(B, L, H).NS - 1) * K * V * 4;
+}
+
 }  // namespace
 
 bool linattn_supported_dim(int d) { return d == 64 || d == 128; }
 
-size_t linattn_workspace_bytes(int, int, int, int, int, int, bool) { return 0; }
+// entering states of the super-chunks
+size_t linattn_workspace_bytes(int B, int L, int H, int, int K, int V, bool) { return slot_bytes(B, L, H, K, V); }
 
-// fp32 dq or dk per head, where heads share a group
-size_t linattn_bwd_workspace_bytes(int B, int L, int H, int G, int K, int, bool) {
-    return H == G ? 0 : (size_t)B * L * H * K * 4;
+// the same (one direction at a time), and the fp32 dq or dk per head where heads share a group
+size_t linattn_bwd_workspace_bytes(int B, int L, int H, int G, int K, int V, bool) {
+    return slot_bytes(B, L, H, K, V) + (H == G ? 0 : (size_t)B * L * H * K * 4);
 }
 
 hipError_t launch_linattn_fwd(const LinattnArgs& a, hipStream_t st) {
     const Mix m{a.B, a.L, a.H, a.H / a.G, a.q, a.k, a.v, 1, 1, 0, a.log_decay, a.seqlens,
-                a.scale, 1.0f, a.h0, 0, a.o, 0, a.h_final};
-    return run_mix(m, a.K, a.V, a.bf16, false, st);
+                a.scale, 1.0f, a.h0, static_cast<float*>(a.ws), 0, a.o, 0, a.h_final};
+    return run_mix(m, a.K, a.V, a.bf16, false, true, st);
 }
 
 hipError_t launch_linattn_bwd(const LinattnBwdArgs& a, hipStream_t st) {
     const int r = a.H / a.G;
     const bool shared = r > 1;
     const size_t ng = (size_t)a.B * a.L * a.G * a.K;
+    float* slots = static_cast<float*>(a.ws);
+    float* heads = slots + slot_bytes(a.B, a.L, a.H, a.K, a.V) / 4;
     hipError_t e;
+    // dq: the state v (x) k of the forward run, held transposed (as [K, V], like h0)
     const Mix mq{a.B, a.L, a.H, r, a.dout, a.v, a.k, 0, 0, 1, a.log_decay, a.seqlens,
-                 a.scale, 1.0f, a.h0, 1, shared ? a.ws : a.dq, shared, nullptr};
-    if ((e = run_mix(mq, a.V, a.K, a.bf16, false, st)) != hipSuccess) return e;
-    if (shared && ng > 0)
-        if ((e = run_sum_heads(static_cast<float*>(a.ws), a.dq, ng, r, a.K, a.bf16, st)) != hipSuccess) return e;
-    const Mix mk{a.B, a.L, a.H, r, a.v, a.dout, a.q, 0, 0, 1, a.log_decay, a.seqlens,
-                 1.0f, a.scale, a.dh_final, 1, shared ? a.ws : a.dk, shared, nullptr};
-    if ((e = run_mix(mk, a.V, a.K, a.bf16, true, st)) != hipSuccess) return e;
-    if (shared && ng > 0)
-        if ((e = run_sum_heads(static_cast<float*>(a.ws), a.dk, ng, r, a.K, a.bf16, st)) != hipSuccess) return e;
+                 a.scale, 1.0f, a.h0, slots, 1, shared ? heads : a.dq, shared, nullptr};
+    if ((e = run_mix(mq, a.V, a.K, a.bf16, false, true, st)) != hipSuccess) return e;
+    if (shared)
+        if ((e = run_sum_heads(heads, a.dq, ng, r, a.K, a.bf16, st)) != hipSuccess) return e;
+    // dv, then dk from the same entering states, read transposed
     const Mix mv{a.B, a.L, a.H, r, a.k, a.q, a.dout, 1, 1, 0, a.log_decay, a.seqlens,
-                 1.0f, a.scale, a.dh_final, 0, a.dv, 0, a.dh0};
-    return run_mix(mv, a.K, a.V, a.bf16, true, st);
+                 1.0f, a.scale, a.dh_final, slots, 0, a.dv, 0, a.dh0};
+    if ((e = run_mix(mv, a.K, a.V, a.bf16, true, true, st)) != hipSuccess) return e;
+    const Mix mk{a.B, a.L, a.H, r, a.v, a.dout, a.q, 0, 0, 1, a.log_decay, a.seqlens,
+                 1.0f, a.scale, a.dh_final, slots, 1, shared ? heads : a.dk, shared, nullptr};
+    if ((e = run_mix(mk, a.V, a.K, a.bf16, true, false, st)) != hipSuccess) return e;
+    return shared ? run_sum_heads(heads, a.dk, ng, r, a.K, a.bf16, st) : hipSuccess;
 }
 
 }  // namespace ssm
