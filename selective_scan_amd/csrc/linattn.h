@@ -11,12 +11,17 @@ namespace ssm {
 // lam - 1 = expm1(a): the rounding of lam itself (up to 2^-25) would act in the same
 // direction on every application to a slowly decaying state. Below, S lam keeps the
 // relative precision of what is left.
+// Both are one fma with the state masked to itself or to 0 as the addend: no branch.
 struct Decay {
-    float lam, m1;
-    bool slow;
-    __device__ __forceinline__ explicit Decay(float a) : lam(expf(a)), m1(expm1f(a)), slow(a > -0.69f) {}
+    float m;
+    unsigned keep;
+    __device__ __forceinline__ explicit Decay(float a) {
+        const bool slow = a > -0.69f;
+        m = slow ? expm1f(a) : expf(a);
+        keep = slow ? 0xffffffffu : 0u;
+    }
     __device__ __forceinline__ float operator()(float s) const {
-        return slow ? __builtin_fmaf(s, m1, s) : s * lam;
+        return __builtin_fmaf(s, m, __uint_as_float(__float_as_uint(s) & keep));
     }
 };
 

@@ -48,6 +48,8 @@ namespace {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef short i16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x8 __attribute__((ext_vector_type(8)));
@@ -130,16 +132,26 @@ template <> struct Types<true> {
     static __device__ __forceinline__ f32x16 mma(Op a, Op b, f32x16 c) {
         return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
     }
-    static __device__ __forceinline__ f32x16 mma(const Formed& a, Op b, f32x16 c) { return mma(a.lo, b, mma(a.hi, b, c)); }
-    static __device__ __forceinline__ f32x16 mma(Op a, const Formed& b, f32x16 c) { return mma(a, b.lo, mma(a, b.hi, c)); }
+    // the two products of a formed operand, apart, so that products into other accumulators
+    // can stand between them
+    template <int PART> static __device__ __forceinline__ f32x16 part(const Formed& a, Op b, f32x16 c) {
+        return mma(PART ? a.lo : a.hi, b, c);
+    }
+    template <int PART> static __device__ __forceinline__ f32x16 part(Op a, const Formed& b, f32x16 c) {
+        return mma(a, PART ? b.lo : b.hi, c);
+    }
+    static constexpr int PARTS = 2;
     static __device__ __forceinline__ Formed form(f32x8 v) {
-        Formed f;
+        u32x4 hi, lo;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            f.hi[e] = (__bf16)v[e];
-            f.lo[e] = (__bf16)(v[e] - (float)f.hi[e]);
+        for (int p = 0; p < 4; ++p) {
+            const f32x2 x = {v[2 * p], v[2 * p + 1]};
+            const uint32_t h = __builtin_bit_cast(uint32_t, __builtin_convertvector(x, bf16x2));
+            const f32x2 d = {x[0] - bf16_lo(h), x[1] - bf16_hi(h)};
+            hi[p] = h;
+            lo[p] = __builtin_bit_cast(uint32_t, __builtin_convertvector(d, bf16x2));
         }
-        return f;
+        return Formed{__builtin_bit_cast(bf16x8, hi), __builtin_bit_cast(bf16x8, lo)};
     }
     static __device__ __forceinline__ f32x8 widen(Op a) {
         f32x8 v;
@@ -171,6 +183,10 @@ template <> struct Types<false> {
         for (int e = 0; e < 8; ++e) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[e], b[e], c, 0, 0, 0);
         return c;
     }
+    template <int PART> static __device__ __forceinline__ f32x16 part(const f32x8& a, const f32x8& b, f32x16 c) {
+        return mma(a, b, c);
+    }
+    static constexpr int PARTS = 1;
     static __device__ __forceinline__ Formed form(f32x8 v) { return v; }
     static __device__ __forceinline__ f32x8 widen(const Op& a) { return a; }
     static __device__ __forceinline__ Op row8(const lds_t* t, int rs, int row, int c0) {
@@ -208,21 +224,17 @@ struct Rows {
         const uint32_t row = (uint32_t)nh * D * Types<BF16>::es;
         const char* base = static_cast<const char*>(x) + ((b * L + t0) * nh + h) * (size_t)(D * Types<BF16>::es);
         const auto r = make_rsrc(base, (uint32_t)(n - 1) * row + D * Types<BF16>::es);
+        // row i >= n starts at i row >= n row: past the range
+        uint32_t off = (threadIdx.x / P) * row + (threadIdx.x % P) * 16;
+        asm volatile("" : "+v"(off));  // N offsets kept across the chunk would cost N registers
 #pragma unroll
-        for (int k = 0; k < N; ++k) {
-            const int q = threadIdx.x + k * NT;
-            // rows past n are kept out of range explicitly: their offset may fall in the
-            // last row's range of a narrow head slice otherwise
-            const uint32_t off = (uint32_t)(q / P) * row + (q % P) * 16;
-            v[k] = __builtin_amdgcn_raw_buffer_load_b128(r, (int)(q / P < n ? off : 0x80000000u), 0, 0);
-        }
+        for (int k = 0; k < N; ++k)
+            v[k] = __builtin_amdgcn_raw_buffer_load_b128(r, (int)(off + (uint32_t)(k * (NT / P)) * row), 0, 0);
     }
     __device__ __forceinline__ void store(lds_t* t) const {
+        lds_t* p = t + (threadIdx.x / P) * RS + (threadIdx.x % P) * 16;
 #pragma unroll
-        for (int k = 0; k < N; ++k) {
-            const int q = threadIdx.x + k * NT;
-            *reinterpret_cast<lds_u32x4*>(t + (q / P) * RS + (q % P) * 16) = v[k];
-        }
+        for (int k = 0; k < N; ++k) *reinterpret_cast<lds_u32x4*>(p + k * (NT / P) * RS) = v[k];
     }
 };
 
@@ -254,7 +266,8 @@ __device__ __forceinline__ void each_state_element(bool trans, F&& f) {
 }
 
 template <int KD, int VD, bool BF16, bool REV, bool AGG>
-__global__ void __launch_bounds__(2 * VD) mix_chunks(Mix a, Geom geo) {
+__global__ void __launch_bounds__(2 * VD) __attribute__((amdgpu_waves_per_eu(BF16 ? 2 : 1, BF16 ? 2 : 1)))
+mix_chunks(Mix a, Geom geo) {
     typedef Types<BF16> Ty;
     typedef typename Ty::Op Op;
     constexpr int NT = 2 * VD, KS = KD / 16, KT = KD / 32;
@@ -299,7 +312,7 @@ __global__ void __launch_bounds__(2 * VD) mix_chunks(Mix a, Geom geo) {
     // backwards lam^(j+1) = W[j]; times kv_scale
     lds_f32* wt = reinterpret_cast<lds_f32*>(lds + W);
     for (int x = tid; x < 128; x += NT) wt[x] = x < kC ? power(REV ? x + 1 : kC - 1 - x) * a.kv_scale : 0.0f;
-    // decay of the scores: this lane's 16 factors of a tile on the diagonal (masked) and of
+    // decay (and factors) of the scores: this lane's 16 factors of a tile on the diagonal (masked) and of
     // the one off it; row i = 32 I + c, column j = 32 J + 16 (r / 8) + 8 hf + r % 8
     lds_f32x4* tab = reinterpret_cast<lds_f32x4*>(lds + TAB);
     if constexpr (!AGG) {
@@ -310,8 +323,8 @@ __global__ void __launch_bounds__(2 * VD) mix_chunks(Mix a, Geom geo) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int j = 16 * (q >> 1) + 8 * hf + 4 * (q & 1) + e, lag = REV ? j - c : c - j;
-                    d0[e] = lag >= 0 ? power(lag) * a.kv_scale : 0.0f;
-                    d1[e] = power(32 + lag) * a.kv_scale;
+                    d0[e] = lag >= 0 ? power(lag) * a.kv_scale * a.out_scale : 0.0f;
+                    d1[e] = power(32 + lag) * a.kv_scale * a.out_scale;
                 }
                 tab[q * 64 + lane] = d0;
                 tab[(4 + q) * 64 + lane] = d1;
@@ -343,7 +356,7 @@ __global__ void __launch_bounds__(2 * VD) mix_chunks(Mix a, Geom geo) {
             if (BF16 && !a.out_f32) {
                 bf16x8 y;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = (__bf16)(acc[8 * s + e] * a.out_scale);
+                for (int e = 0; e < 8; ++e) y[e] = (__bf16)acc[8 * s + e];
                 *reinterpret_cast<bf16x8*>(static_cast<uint16_t*>(a.out) + at + 16 * s) = y;
             } else {
                 f32x4* p = reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + at + 16 * s);
@@ -351,7 +364,7 @@ __global__ void __launch_bounds__(2 * VD) mix_chunks(Mix a, Geom geo) {
                 for (int u = 0; u < 2; ++u) {
                     f32x4 y;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) y[e] = acc[8 * s + 4 * u + e] * a.out_scale;
+                    for (int e = 0; e < 4; ++e) y[e] = acc[8 * s + 4 * u + e];
                     p[u] = y;
                 }
             }
@@ -365,6 +378,7 @@ __global__ void __launch_bounds__(2 * VD) mix_chunks(Mix a, Geom geo) {
         for (int ch = ca; ch < c1; ++ch)
             for (int I = 0; I < 2; ++I) put(ch * kC, I, zero);
     }
+    const Decay full(la * (float)kC);
     const int nch = ca - c0;
     auto chunk_at = [&](int u) { return REV ? ca - 1 - u : c0 + u; };
     if (nch > 0) {
@@ -374,29 +388,45 @@ __global__ void __launch_bounds__(2 * VD) mix_chunks(Mix a, Geom geo) {
     __syncthreads();
     for (int u = 0; u < nch; ++u) {
         const int t0 = chunk_at(u) * kC, n = min(kC, len - t0);
-        if (u + 1 < nch) load(chunk_at(u + 1));
         Op v[4];
+        auto read_v = [&]() {
 #pragma unroll
-        for (int s = 0; s < 4; ++s) v[s] = Ty::col8(lds + X3, RowsV::RS, 16 * s, 32 * wave);
+            for (int s = 0; s < 4; ++s) v[s] = Ty::col8(lds + X3, RowsV::RS, 16 * s, 32 * wave);
+        };
+        if constexpr (AGG) read_v();
         if constexpr (!AGG) {
             f32x16 acc[2], m00, m11, mx;
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[0][r] = acc[1][r] = m00[r] = m11[r] = mx[r] = 0.0f;
-            // scores (rows j in the order pi, columns i) and x1 S (rows: columns of S)
+            // scores (rows j in the order pi, columns i) and x1 S (rows: columns of S); the
+            // operands of step ks + 1 are read while those of ks multiply
+            Op q0, q1, k0, k1;
+            auto fetch = [&](int ks) {
+                q0 = Ty::row8(lds + X1, RowsK::RS, c, 16 * ks + 8 * hf);
+                q1 = Ty::row8(lds + X1, RowsK::RS, 32 + c, 16 * ks + 8 * hf);
+                k0 = Ty::row8(lds + X2, RowsK::RS, pi(c), 16 * ks + 8 * hf);
+                k1 = Ty::row8(lds + X2, RowsK::RS, 32 + pi(c), 16 * ks + 8 * hf);
+            };
+            fetch(0);
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
-                const Op q0 = Ty::row8(lds + X1, RowsK::RS, c, 16 * ks + 8 * hf);
-                const Op q1 = Ty::row8(lds + X1, RowsK::RS, 32 + c, 16 * ks + 8 * hf);
-                const Op k0 = Ty::row8(lds + X2, RowsK::RS, pi(c), 16 * ks + 8 * hf);
-                const Op k1 = Ty::row8(lds + X2, RowsK::RS, 32 + pi(c), 16 * ks + 8 * hf);
+                const Op p0 = q0, p1 = q1, l0 = k0, l1 = k1;
+                if (ks + 1 < KS) fetch(ks + 1);
                 const typename Ty::Formed sf = Ty::form(half_of(S[ks >> 1], ks & 1));
-                m00 = Ty::mma(k0, q0, m00);
-                m11 = Ty::mma(k1, q1, m11);
-                mx = REV ? Ty::mma(k1, q0, mx) : Ty::mma(k0, q1, mx);
-                acc[0] = Ty::mma(sf, q0, acc[0]);
-                acc[1] = Ty::mma(sf, q1, acc[1]);
+                m00 = Ty::mma(l0, p0, m00);
+                m11 = Ty::mma(l1, p1, m11);
+                mx = REV ? Ty::mma(l1, p0, mx) : Ty::mma(l0, p1, mx);
+                acc[0] = Ty::template part<0>(sf, p0, acc[0]);
+                acc[1] = Ty::template part<0>(sf, p1, acc[1]);
+                if constexpr (Ty::PARTS == 2) {
+                    acc[0] = Ty::template part<1>(sf, p0, acc[0]);
+                    acc[1] = Ty::template part<1>(sf, p1, acc[1]);
+                }
+                __builtin_amdgcn_sched_barrier(0);
             }
-            const float w0 = power(REV ? max(n - 1 - c, 0) : c + 1), w1 = power(REV ? max(n - 33 - c, 0) : c + 33);
+            read_v();
+            const float w0 = power(REV ? max(n - 1 - c, 0) : c + 1) * a.out_scale;
+            const float w1 = power(REV ? max(n - 33 - c, 0) : c + 33) * a.out_scale;
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
                 acc[0][r] *= w0;
@@ -414,10 +444,18 @@ __global__ void __launch_bounds__(2 * VD) mix_chunks(Mix a, Geom geo) {
             };
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
-                acc[0] = Ty::mma(v[s], decayed(m00, 0, s), acc[0]);
-                acc[1] = Ty::mma(v[2 + s], decayed(m11, 0, s), acc[1]);
-                if constexpr (REV) acc[0] = Ty::mma(v[2 + s], decayed(mx, 1, s), acc[0]);
-                else acc[1] = Ty::mma(v[s], decayed(mx, 1, s), acc[1]);
+                const typename Ty::Formed f0 = decayed(m00, 0, s), f1 = decayed(m11, 0, s), fx = decayed(mx, 1, s);
+                f32x16 &ax = acc[REV ? 0 : 1], &ay = acc[REV ? 1 : 0];
+                const typename Ty::Formed &gx = REV ? f0 : f1, &gy = REV ? f1 : f0;
+                const Op vx = v[REV ? s : 2 + s], vy = v[REV ? 2 + s : s];
+                ax = Ty::template part<0>(vx, gx, ax);
+                ay = Ty::template part<0>(vy, gy, ay);
+                ax = Ty::template part<0>(vy, fx, ax);
+                if constexpr (Ty::PARTS == 2) {
+                    ay = Ty::template part<1>(vy, gy, ay);
+                    ax = Ty::template part<1>(vx, gx, ax);
+                    ax = Ty::template part<1>(vy, fx, ax);
+                }
             }
             if (n < kC) {  // rows of padding are 0 whatever the state holds
 #pragma unroll
@@ -429,8 +467,10 @@ __global__ void __launch_bounds__(2 * VD) mix_chunks(Mix a, Geom geo) {
             put(t0, 0, acc[0]);
             put(t0, 1, acc[1]);
         }
+        __builtin_amdgcn_sched_barrier(0);
+        if (u + 1 < nch) load(chunk_at(u + 1));
         if (AGG || u + 1 < nch || a.final_state) {
-            const Decay decay(la * (float)n);
+            const Decay decay = n == kC ? full : Decay(la * (float)n);
 #pragma unroll
             for (int T = 0; T < KT; ++T)
 #pragma unroll
@@ -442,9 +482,15 @@ __global__ void __launch_bounds__(2 * VD) mix_chunks(Mix a, Geom geo) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) x[e] *= w[e];
                 const typename Ty::Formed wv = Ty::form(x);
+                Op k[KT];
 #pragma unroll
-                for (int T = 0; T < KT; ++T)
-                    S[T] = Ty::mma(Ty::col8(lds + X2, RowsK::RS, 16 * s, 32 * T), wv, S[T]);
+                for (int T = 0; T < KT; ++T) k[T] = Ty::col8(lds + X2, RowsK::RS, 16 * s, 32 * T);
+#pragma unroll
+                for (int T = 0; T < KT; ++T) S[T] = Ty::template part<0>(k[T], wv, S[T]);
+                if constexpr (Ty::PARTS == 2)
+#pragma unroll
+                    for (int T = 0; T < KT; ++T) S[T] = Ty::template part<1>(k[T], wv, S[T]);
+                __builtin_amdgcn_sched_barrier(0);
             }
         }
         __syncthreads();
