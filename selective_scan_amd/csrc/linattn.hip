@@ -122,13 +122,30 @@ __device__ __forceinline__ float log_decay_of(const float* p, int h) {
 
 __device__ __forceinline__ int pi(int m) { return (m & 0x13) | ((m & 4) << 1) | ((m & 8) >> 1); }
 
+// A chunk's rows of D values in LDS: kC rows of D es bytes without padding, the 16-byte
+// piece p of row r at position p ^ swz(r). Sixteen rows' pieces p, read together as operand
+// rows, then cover all 64 banks, and so do the two adjacent pieces of four rows that each
+// half wave's transpose read takes. (Loads straight into LDS put a wave's 1 KB down in lane
+// order, so the order within a row is chosen by what each lane loads, and rows cannot be
+// padded.)
+template <int D, bool BF16>
+struct Tile {
+    static constexpr int RB = D * (BF16 ? 2 : 4);  // bytes per row: 128, 256 or 512
+    static constexpr int P = RB / 16;              // pieces per row
+    static constexpr int BYTES = kC * RB;
+    static __device__ __forceinline__ int swz(int r) {
+        if constexpr (P == 8) return ((r << 1) & 4) | ((r >> 2) & 3);  // two rows span the banks
+        else return ((r & 3) << 2) | ((r >> 2) & 3);
+    }
+    static __device__ __forceinline__ int at(int r, int p) { return r * RB + ((p ^ swz(r)) << 4); }
+};
+
 // Operands of a 32 x 32 x 16 product: lane l holds row (or column) l % 32 and the eight
 // contraction indices 8 (l / 32) + e.
 template <bool BF16> struct Types;
 template <> struct Types<true> {
     typedef bf16x8 Op;
     struct Formed { bf16x8 hi, lo; };
-    static constexpr int es = 2, pad = 8;
     static __device__ __forceinline__ f32x16 mma(Op a, Op b, f32x16 c) {
         return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
     }
@@ -159,25 +176,27 @@ template <> struct Types<true> {
         for (int e = 0; e < 8; ++e) v[e] = (float)a[e];
         return v;
     }
-    // elements c0 .. c0 + 7 of row `row` of an LDS tile with rows of `rs` bytes
-    static __device__ __forceinline__ Op row8(const lds_t* t, int rs, int row, int c0) {
-        return *reinterpret_cast<const lds_bf16x8*>(t + row * rs + c0 * 2);
+    // elements 16 ks + 8 (l / 32) + e of row `row` (tiles: see Tile)
+    template <int D> static __device__ __forceinline__ Op row8(const lds_t* t, int row, int ks) {
+        return *reinterpret_cast<const lds_bf16x8*>(t + Tile<D, true>::at(row, 2 * ks + ((threadIdx.x >> 5) & 1)));
     }
     // rows r0 + 8 (l / 32) + e of column c0 + pi(l % 32): the LDS transpose read hands lane
     // i of a 16-lane group column i of the group's 16, made of the four 4-column pieces
     // its lanes point at; pointing at the pieces in the order 0, 2, 1, 3 gives pi
-    static __device__ __forceinline__ Op col8(const lds_t* t, int rs, int r0, int c0) {
+    template <int D> static __device__ __forceinline__ Op col8(const lds_t* t, int r0, int c0) {
         const int l = threadIdx.x & 63, i = l & 15, q = i & 3;
-        const lds_t* p = t + (r0 + 8 * (l >> 5) + (i >> 2)) * rs + (c0 + (l & 16) + 4 * ((q >> 1) | ((q & 1) << 1))) * 2;
-        const bf16x4 a = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)p));
-        const bf16x4 b = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p + 4 * rs)));
+        const int row = r0 + 8 * (l >> 5) + (i >> 2), piece = (c0 >> 3) + ((l >> 3) & 2) + (q & 1);
+        const lds_t* p = t + 4 * (q & 2);
+        const bf16x4 a = __builtin_bit_cast(
+            bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p + Tile<D, true>::at(row, piece))));
+        const bf16x4 b = __builtin_bit_cast(
+            bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p + Tile<D, true>::at(row + 4, piece))));
         return bf16x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
     }
 };
 template <> struct Types<false> {
     typedef f32x8 Op;
     typedef f32x8 Formed;
-    static constexpr int es = 4, pad = 4;
     static __device__ __forceinline__ f32x16 mma(const f32x8& a, const f32x8& b, f32x16 c) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[e], b[e], c, 0, 0, 0);
@@ -189,17 +208,18 @@ template <> struct Types<false> {
     static constexpr int PARTS = 1;
     static __device__ __forceinline__ Formed form(f32x8 v) { return v; }
     static __device__ __forceinline__ f32x8 widen(const Op& a) { return a; }
-    static __device__ __forceinline__ Op row8(const lds_t* t, int rs, int row, int c0) {
-        const lds_t* p = t + row * rs + c0 * 4;
-        const f32x4 a = *reinterpret_cast<const lds_f32x4*>(p), b = *reinterpret_cast<const lds_f32x4*>(p + 16);
+    template <int D> static __device__ __forceinline__ Op row8(const lds_t* t, int row, int ks) {
+        const int piece = 4 * ks + 2 * ((threadIdx.x >> 5) & 1);
+        const f32x4 a = *reinterpret_cast<const lds_f32x4*>(t + Tile<D, false>::at(row, piece));
+        const f32x4 b = *reinterpret_cast<const lds_f32x4*>(t + Tile<D, false>::at(row, piece + 1));
         return f32x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
     }
-    static __device__ __forceinline__ Op col8(const lds_t* t, int rs, int r0, int c0) {
-        const int l = threadIdx.x & 63;
-        const lds_t* p = t + (r0 + 8 * (l >> 5)) * rs + (c0 + pi(l & 31)) * 4;
+    template <int D> static __device__ __forceinline__ Op col8(const lds_t* t, int r0, int c0) {
+        const int l = threadIdx.x & 63, col = c0 + pi(l & 31);
         f32x8 v;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = *reinterpret_cast<const lds_f32*>(p + e * rs);
+        for (int e = 0; e < 8; ++e)
+            v[e] = *reinterpret_cast<const lds_f32*>(t + Tile<D, false>::at(r0 + 8 * (l >> 5) + e, col >> 2) + 4 * (col & 3));
         return v;
     }
 };
@@ -211,32 +231,55 @@ __device__ __forceinline__ f32x8 half_of(const f32x16& a, int s) {
     return v;
 }
 
-// Rows of a chunk of one of x1, x2, x3: D values of one head per step.
+// Rows t0 .. t0 + kC - 1 of one head of x1, x2 or x3 into a Tile. Rows at or past n are out
+// of the buffer's range (row i starts at i row bytes, the range ends inside row n - 1).
 template <int D, int NT, bool BF16>
 struct Rows {
-    static constexpr int P = D * Types<BF16>::es / 16;  // 16-byte pieces per row
-    static constexpr int N = kC * P / NT;               // pieces per thread
-    static constexpr int RS = (D + Types<BF16>::pad) * Types<BF16>::es;  // LDS row stride (bytes)
-    static constexpr int BYTES = kC * RS;
-    u32x4 v[N];
-    // rows t0 .. t0 + n - 1 (the others as zeros: out of the buffer's range)
-    __device__ __forceinline__ void load(const void* x, size_t b, int L, int nh, int h, int t0, int n) {
-        const uint32_t row = (uint32_t)nh * D * Types<BF16>::es;
-        const char* base = static_cast<const char*>(x) + ((b * L + t0) * nh + h) * (size_t)(D * Types<BF16>::es);
-        const auto r = make_rsrc(base, (uint32_t)(n - 1) * row + D * Types<BF16>::es);
-        // row i >= n starts at i row >= n row: past the range
-        uint32_t off = (threadIdx.x / P) * row + (threadIdx.x % P) * 16;
-        asm volatile("" : "+v"(off));  // N offsets kept across the chunk would cost N registers
+    typedef Tile<D, BF16> Ti;
+    static constexpr int P = Ti::P, N = kC * P / NT;  // pieces per row, per thread
+    u32x4 v[BF16 ? 1 : N];                            // fp32: on the way through registers
+    __device__ __forceinline__ void load(const void* x, size_t b, int L, int nh, int h, int t0, int n, lds_t* t) {
+        const uint32_t row = (uint32_t)nh * Ti::RB;
+        const char* base = static_cast<const char*>(x) + ((b * L + t0) * nh + h) * (size_t)Ti::RB;
+        const auto r = make_rsrc(base, (uint32_t)(n - 1) * row + Ti::RB);
+        const int tid = threadIdx.x;
+        if constexpr (BF16) {
+            // straight into LDS, 1 KB per wave and instruction; not known to the compiler:
+            // landed() and a barrier stand before the tile is read
+            const uint32_t base_lds = (uint32_t)(uintptr_t)t + (uint32_t)__builtin_amdgcn_readfirstlane(tid >> 6) * 1024;
 #pragma unroll
-        for (int k = 0; k < N; ++k)
-            v[k] = __builtin_amdgcn_raw_buffer_load_b128(r, (int)(off + (uint32_t)(k * (NT / P)) * row), 0, 0);
+            for (int k = 0; k < N; ++k) {
+                const int rr = tid / P + k * (NT / P);
+                const uint32_t off = (uint32_t)rr * row + (((tid % P) ^ Ti::swz(rr)) << 4);
+                uint32_t m0;  // the LDS address goes through m0, which is left as it was
+                asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\tbuffer_load_dwordx4 %2, %3, 0 offen lds\n\t"
+                             "s_mov_b32 m0, %0"
+                             : "=&s"(m0)
+                             : "s"(base_lds + k * NT * 16), "v"(off), "s"(r)
+                             : "memory");
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                uint32_t off = (uint32_t)(tid / P + k * (NT / P)) * row + (tid % P) * 16;
+                v[k] = __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, 0);
+            }
+        }
     }
     __device__ __forceinline__ void store(lds_t* t) const {
-        lds_t* p = t + (threadIdx.x / P) * RS + (threadIdx.x % P) * 16;
+        if constexpr (!BF16)
 #pragma unroll
-        for (int k = 0; k < N; ++k) *reinterpret_cast<lds_u32x4*>(p + k * (NT / P) * RS) = v[k];
+            for (int k = 0; k < N; ++k)
+                *reinterpret_cast<lds_u32x4*>(t + Ti::at(threadIdx.x / P + k * (NT / P), threadIdx.x % P)) = v[k];
+    }
+    // zeros in the rows at or past n
+    static __device__ __forceinline__ void clear(lds_t* t, int n) {
+        for (int q = n * P + threadIdx.x; q < kC * P; q += NT)
+            *reinterpret_cast<lds_u32x4*>(t + q * 16) = u32x4{0u, 0u, 0u, 0u};
     }
 };
+
+__device__ __forceinline__ void landed() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 // Workgroup -> (head, super-chunk, batch). Workgroups go round-robin to the 8 XCDs
 // (each with its own L2); consecutive coordinates, heads fastest, go to one XCD where
@@ -273,8 +316,12 @@ mix_chunks(Mix a, Geom geo) {
     constexpr int NT = 2 * VD, KS = KD / 16, KT = KD / 32;
     typedef Rows<KD, NT, BF16> RowsK;
     typedef Rows<VD, NT, BF16> RowsV;
-    constexpr int X2 = 0, X3 = X2 + RowsK::BYTES, W = X3 + RowsV::BYTES, TAB = W + 128 * 4,
-                  X1 = TAB + (AGG ? 0 : 2 * 4 * 64 * 16), TOTAL = X1 + (AGG ? 0 : RowsK::BYTES);
+    // bf16: x2's tile twice (the next chunk's arrives while the state's update reads this
+    // one's). The tiles lie below 64 KB, as far as a load into LDS is given its address.
+    constexpr int BK = Tile<KD, BF16>::BYTES, BV = Tile<VD, BF16>::BYTES, NB2 = BF16 ? 2 : 1;
+    constexpr int X2 = 0, X3 = X2 + NB2 * BK, X1 = X3 + BV, W = X1 + (AGG ? 0 : BK), TAB = W + 128 * 4,
+                  TOTAL = TAB + (AGG ? 0 : 2 * 4 * 64 * 16);
+    static_assert(!BF16 || W <= 65536, "tiles below 64 KB");
     __shared__ __attribute__((aligned(16))) char lds_raw[TOTAL];
     lds_t* lds = (lds_t*)lds_raw;
     int h, sc, b;
@@ -334,16 +381,29 @@ mix_chunks(Mix a, Geom geo) {
 
     RowsK r1, r2;
     RowsV r3;
-    auto load = [&](int ch) {
+    auto load = [&](int ch, int buf) {
         const int t0 = ch * kC, n = min(kC, len - t0);
-        if constexpr (!AGG) r1.load(a.x1, b, a.L, n1, h1, t0, n);
-        r2.load(a.x2, b, a.L, n2, h2, t0, n);
-        r3.load(a.x3, b, a.L, n3, h3, t0, n);
+        r2.load(a.x2, b, a.L, n2, h2, t0, n, lds + X2 + buf * BK);
+        if constexpr (!AGG) r1.load(a.x1, b, a.L, n1, h1, t0, n, lds + X1);
+        r3.load(a.x3, b, a.L, n3, h3, t0, n, lds + X3);
     };
-    auto stage = [&]() {
-        if constexpr (!AGG) r1.store(lds + X1);
-        r2.store(lds + X2);
-        r3.store(lds + X3);
+    // the loaded chunk's tiles complete and visible to every wave
+    auto stage = [&](int ch, int buf) {
+        const int n = min(kC, len - ch * kC);
+        if constexpr (BF16) {
+            landed();
+            if (n < kC) {
+                __syncthreads();
+                if constexpr (!AGG) RowsK::clear(lds + X1, n);
+                RowsK::clear(lds + X2 + buf * BK, n);
+                RowsV::clear(lds + X3, n);
+            }
+        } else {
+            if constexpr (!AGG) r1.store(lds + X1);
+            r2.store(lds + X2);
+            r3.store(lds + X3);
+        }
+        __syncthreads();
     };
 
     // outputs of this wave's 32 columns of row block I (rows t0 + 32 I + c)
@@ -382,18 +442,24 @@ mix_chunks(Mix a, Geom geo) {
     const int nch = ca - c0;
     auto chunk_at = [&](int u) { return REV ? ca - 1 - u : c0 + u; };
     if (nch > 0) {
-        load(chunk_at(0));
-        stage();
+        load(chunk_at(0), 0);
+        stage(chunk_at(0), 0);
     }
-    __syncthreads();
     for (int u = 0; u < nch; ++u) {
         const int t0 = chunk_at(u) * kC, n = min(kC, len - t0);
+        const lds_t* x2 = lds + X2 + (BF16 ? (u & 1) * BK : 0);
         Op v[4];
         auto read_v = [&]() {
 #pragma unroll
-            for (int s = 0; s < 4; ++s) v[s] = Ty::col8(lds + X3, RowsV::RS, 16 * s, 32 * wave);
+            for (int s = 0; s < 4; ++s) v[s] = Ty::template col8<VD>(lds + X3, 16 * s, 32 * wave);
         };
         if constexpr (AGG) read_v();
+        // x1 and x3 are read: their tiles take the next chunk
+        auto next = [&]() {
+            __syncthreads();
+            if (u + 1 < nch) load(chunk_at(u + 1), (u + 1) & 1);
+        };
+        if constexpr (AGG && BF16) next();
         if constexpr (!AGG) {
             f32x16 acc[2], m00, m11, mx;
 #pragma unroll
@@ -402,10 +468,10 @@ mix_chunks(Mix a, Geom geo) {
             // operands of step ks + 1 are read while those of ks multiply
             Op q0, q1, k0, k1;
             auto fetch = [&](int ks) {
-                q0 = Ty::row8(lds + X1, RowsK::RS, c, 16 * ks + 8 * hf);
-                q1 = Ty::row8(lds + X1, RowsK::RS, 32 + c, 16 * ks + 8 * hf);
-                k0 = Ty::row8(lds + X2, RowsK::RS, pi(c), 16 * ks + 8 * hf);
-                k1 = Ty::row8(lds + X2, RowsK::RS, 32 + pi(c), 16 * ks + 8 * hf);
+                q0 = Ty::template row8<KD>(lds + X1, c, ks);
+                q1 = Ty::template row8<KD>(lds + X1, 32 + c, ks);
+                k0 = Ty::template row8<KD>(x2, pi(c), ks);
+                k1 = Ty::template row8<KD>(x2, 32 + pi(c), ks);
             };
             fetch(0);
 #pragma unroll
@@ -425,6 +491,7 @@ mix_chunks(Mix a, Geom geo) {
                 __builtin_amdgcn_sched_barrier(0);
             }
             read_v();
+            if constexpr (BF16) next();
             const float w0 = power(REV ? max(n - 1 - c, 0) : c + 1) * a.out_scale;
             const float w1 = power(REV ? max(n - 33 - c, 0) : c + 33) * a.out_scale;
 #pragma unroll
@@ -467,8 +534,9 @@ mix_chunks(Mix a, Geom geo) {
             put(t0, 0, acc[0]);
             put(t0, 1, acc[1]);
         }
-        __builtin_amdgcn_sched_barrier(0);
-        if (u + 1 < nch) load(chunk_at(u + 1));
+        if constexpr (!BF16) {
+            if (u + 1 < nch) load(chunk_at(u + 1), 0);
+        }
         if (AGG || u + 1 < nch || a.final_state) {
             const Decay decay = n == kC ? full : Decay(la * (float)n);
 #pragma unroll
@@ -484,7 +552,7 @@ mix_chunks(Mix a, Geom geo) {
                 const typename Ty::Formed wv = Ty::form(x);
                 Op k[KT];
 #pragma unroll
-                for (int T = 0; T < KT; ++T) k[T] = Ty::col8(lds + X2, RowsK::RS, 16 * s, 32 * T);
+                for (int T = 0; T < KT; ++T) k[T] = Ty::template col8<KD>(x2, 16 * s, 32 * T);
 #pragma unroll
                 for (int T = 0; T < KT; ++T) S[T] = Ty::template part<0>(k[T], wv, S[T]);
                 if constexpr (Ty::PARTS == 2)
@@ -493,11 +561,8 @@ mix_chunks(Mix a, Geom geo) {
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
-        __syncthreads();
-        if (u + 1 < nch) {
-            stage();
-            __syncthreads();
-        }
+        if constexpr (!BF16) __syncthreads();  // every read of the tiles done
+        if (u + 1 < nch) stage(chunk_at(u + 1), (u + 1) & 1);
     }
 
     float* dst = nullptr;
