@@ -279,7 +279,14 @@ struct Rows {
     }
 };
 
-__device__ __forceinline__ void landed() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+// all but the last N of this wave's loads and stores are done
+template <int N>
+__device__ __forceinline__ void landed() {
+    static_assert(N == 0 || N == 4 || N == 8, "");
+    if constexpr (N == 0) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    else if constexpr (N == 4) asm volatile("s_waitcnt vmcnt(4)" ::: "memory");
+    else asm volatile("s_waitcnt vmcnt(8)" ::: "memory");
+}
 
 // Workgroup -> (head, super-chunk, batch). Workgroups go round-robin to the 8 XCDs
 // (each with its own L2); consecutive coordinates, heads fastest, go to one XCD where
@@ -294,35 +301,58 @@ __device__ __forceinline__ void block_coords(int H, int Kp, int& h, int& k, int&
 }
 
 // The state tiles of one wave: rows k = 32 T + 16 (r / 8) + 8 hf + r % 8, column
-// 32 wave + pi(lane % 32), of a [KD, VD] matrix (or its transpose) in memory.
-template <int KD, int VD, typename F>
-__device__ __forceinline__ void each_state_element(bool trans, F&& f) {
+// 32 wave + pi(lane % 32). f(T, r, k, column).
+template <int KD, typename F>
+__device__ __forceinline__ void each_state_element(F&& f) {
     const int lane = threadIdx.x & 63, hf = lane >> 5;
     const int col = 32 * (threadIdx.x >> 6) + pi(lane & 31);
 #pragma unroll
     for (int T = 0; T < KD / 32; ++T)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-            const int k = 32 * T + 16 * (r >> 3) + 8 * hf + (r & 7);
-            f(T, r, trans ? col * KD + k : k * VD + col);
-        }
+        for (int r = 0; r < 16; ++r) f(T, r, 32 * T + 16 * (r >> 3) + 8 * hf + (r & 7), col);
 }
+
+// Where a slot holds element (i, j) of a state of I x J: eight i next to each other for
+// one j, j next, so that a wave's tile is read and written in whole lines. A run on the
+// transposed state (dk on dv's) finds its elements eight lanes to a line.
+__device__ __forceinline__ int slot_at(int i, int j, int J) { return ((i >> 3) * J + j) * 8 + (i & 7); }
+
+// lam^64 as the factor of one chunk after another. Rounded once, it would err in the same
+// direction on every chunk of a slowly decaying state; so each chunk takes the float that
+// brings the product so far nearest to the exact one.
+struct ChunkDecay {
+    double lam, inv, err = 0.0;
+    __device__ __forceinline__ explicit ChunkDecay(float a) : lam(exp((double)a)), inv(lam > 0.5 ? 1.0 / lam : 0.0) {}
+    __device__ __forceinline__ float next() {
+        const float m = (float)(lam - lam * err);
+        err = inv != 0.0 ? (1.0 + err) * ((double)m * inv) - 1.0 : 0.0;
+        return m;
+    }
+};
+
+// The tiles of a workgroup in LDS. Two buffers where they are filled while the other is
+// read: of x2, and, if full, of x1 and x3 as well; where two workgroups would not fit a CU
+// with that, x1 and x3 have one, filled once the chunk's scores and x1 S are done.
+template <int KD, int VD, bool BF16, bool AGG>
+struct Lds {
+    static constexpr int BK = Tile<KD, BF16>::BYTES, BV = Tile<VD, BF16>::BYTES;
+    static constexpr bool FULL = BF16 && (AGG || (KD == 64 && VD == 128));
+    static constexpr int N2 = BF16 ? 2 : 1, N13 = FULL ? 2 : 1;
+    static constexpr int X2 = 0, X3 = X2 + N2 * BK, X1 = X3 + N13 * BV, W = X1 + (AGG ? 0 : N13 * BK),
+                         M = W + 128 * 4, TOTAL = M + (AGG ? 0 : 3 * 2 * 2048);
+};
 
 template <int KD, int VD, bool BF16, bool REV, bool AGG>
 __global__ void __launch_bounds__(2 * VD) __attribute__((amdgpu_waves_per_eu(BF16 ? 2 : 1, BF16 ? 2 : 1)))
 mix_chunks(Mix a, Geom geo) {
     typedef Types<BF16> Ty;
     typedef typename Ty::Op Op;
+    typedef typename Ty::Formed Formed;
+    typedef Lds<KD, VD, BF16, AGG> Ld;
     constexpr int NT = 2 * VD, KS = KD / 16, KT = KD / 32;
     typedef Rows<KD, NT, BF16> RowsK;
     typedef Rows<VD, NT, BF16> RowsV;
-    // bf16: x2's tile twice (the next chunk's arrives while the state's update reads this
-    // one's). The tiles lie below 64 KB, as far as a load into LDS is given its address.
-    constexpr int BK = Tile<KD, BF16>::BYTES, BV = Tile<VD, BF16>::BYTES, NB2 = BF16 ? 2 : 1;
-    constexpr int X2 = 0, X3 = X2 + NB2 * BK, X1 = X3 + BV, W = X1 + (AGG ? 0 : BK), TAB = W + 128 * 4,
-                  TOTAL = TAB + (AGG ? 0 : 2 * 4 * 64 * 16);
-    static_assert(!BF16 || W <= 65536, "tiles below 64 KB");
-    __shared__ __attribute__((aligned(16))) char lds_raw[TOTAL];
+    __shared__ __attribute__((aligned(16))) char lds_raw[Ld::TOTAL];
     lds_t* lds = (lds_t*)lds_raw;
     int h, sc, b;
     block_coords(a.H, AGG ? geo.NS - 1 : geo.NS, h, sc, b);
@@ -335,12 +365,25 @@ mix_chunks(Mix a, Geom geo) {
     const int h2 = a.g2 ? hg : h, n2 = a.g2 ? G : a.H;
     const int h3 = a.g3 ? hg : h, n3 = a.g3 ? G : a.H;
     const int len = seq_len(a.seqlens, b, a.L);
-    const float la = log_decay_of(a.log_decay, h), la2 = la * kLog2e;
-    auto power = [&](int n) { return exp2_fast((float)n * la2); };
 
     // chunks [c0, c1) of this super-chunk, of which [c0, ca) hold steps of the sequence
     const int c0 = sc * geo.cps, c1 = min(geo.NC, c0 + geo.cps);
-    const int ca = max(c0, min(c1, (len + kC - 1) / kC));
+    const int ca = max(c0, min(c1, (len + kC - 1) / kC)), nch = ca - c0;
+    auto chunk_at = [&](int u) { return REV ? ca - 1 - u : c0 + u; };
+
+    RowsK r1, r2;
+    RowsV r3;
+    // chunk u's rows into its buffers
+    auto load = [&](int u) {
+        const int t0 = chunk_at(u) * kC, n = min(kC, len - t0), b2 = u % Ld::N2, b13 = u % Ld::N13;
+        r2.load(a.x2, b, a.L, n2, h2, t0, n, lds + Ld::X2 + b2 * Ld::BK);
+        if constexpr (!AGG) r1.load(a.x1, b, a.L, n1, h1, t0, n, lds + Ld::X1 + b13 * Ld::BK);
+        r3.load(a.x3, b, a.L, n3, h3, t0, n, lds + Ld::X3 + b13 * Ld::BV);
+    };
+    if (nch > 0) load(0);
+
+    const float la = log_decay_of(a.log_decay, h), la2 = la * kLog2e;
+    auto power = [&](int n) { return exp2_fast((float)n * la2); };
 
     // the state entering the super-chunk
     f32x16 S[KT];
@@ -350,148 +393,179 @@ mix_chunks(Mix a, Geom geo) {
         for (int r = 0; r < 16; ++r) S[T][r] = 0.0f;
     if constexpr (!AGG) {
         const bool first = REV ? sc == geo.NS - 1 : sc == 0;
-        const float* src = first ? (a.init ? a.init + bh * KD * VD : nullptr)
-                                 : a.slots + (bh * (geo.NS - 1) + (REV ? sc : sc - 1)) * KD * VD;
-        if (src) each_state_element<KD, VD>(a.trans, [&](int T, int r, int at) { S[T][r] = src[at]; });
+        if (first) {
+            const float* src = a.init + bh * KD * VD;
+            if (a.init)
+                each_state_element<KD>([&](int T, int r, int k, int j) { S[T][r] = src[a.trans ? j * KD + k : k * VD + j]; });
+        } else {
+            const float* src = a.slots + (bh * (geo.NS - 1) + (REV ? sc : sc - 1)) * KD * VD;
+            if (a.trans) each_state_element<KD>([&](int T, int r, int k, int j) { S[T][r] = src[slot_at(j, k, KD)]; });
+            else each_state_element<KD>([&](int T, int r, int k, int j) { S[T][r] = src[slot_at(k, j, VD)]; });
+        }
     }
 
     // W[x]: weight of row j of x3 in the state's update; forwards lam^(n-1-j) = W[j + 64 - n],
     // backwards lam^(j+1) = W[j]; times kv_scale
-    lds_f32* wt = reinterpret_cast<lds_f32*>(lds + W);
+    lds_f32* wt = reinterpret_cast<lds_f32*>(lds + Ld::W);
     for (int x = tid; x < 128; x += NT) wt[x] = x < kC ? power(REV ? x + 1 : kC - 1 - x) * a.kv_scale : 0.0f;
-    // decay (and factors) of the scores: this lane's 16 factors of a tile on the diagonal (masked) and of
-    // the one off it; row i = 32 I + c, column j = 32 J + 16 (r / 8) + 8 hf + r % 8
-    lds_f32x4* tab = reinterpret_cast<lds_f32x4*>(lds + TAB);
+    // The scores' tiles that count are (J, I) = (0, 0) and (1, 1) on the diagonal and one off
+    // it, (0, 1) forwards, (1, 0) backwards. Each is computed by one wave, decayed (this
+    // lane's 16 factors: row i = 32 I + c, column j = 32 J + 16 (r / 8) + 8 hf + r % 8),
+    // formed and passed to the others through LDS as operands. Of four waves the last
+    // repeats tile (0, 0) for nothing; of two, each has a diagonal tile and both the other,
+    // which the first passes on.
+    const bool off_diag = NT == 256 && wave == 2;
+    const int Ja = off_diag ? (REV ? 1 : 0) : wave & 1 & (wave >> 1 ^ 1), Ia = off_diag ? (REV ? 0 : 1) : Ja;
+    f32x16 d_a, d_b;
     if constexpr (!AGG) {
-        if (tid < 64) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                f32x4 d0, d1;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int j = 16 * (q >> 1) + 8 * hf + 4 * (q & 1) + e, lag = REV ? j - c : c - j;
-                    d0[e] = lag >= 0 ? power(lag) * a.kv_scale * a.out_scale : 0.0f;
-                    d1[e] = power(32 + lag) * a.kv_scale * a.out_scale;
-                }
-                tab[q * 64 + lane] = d0;
-                tab[(4 + q) * 64 + lane] = d1;
-            }
+        for (int r = 0; r < 16; ++r) {
+            const int j = 16 * (r >> 3) + 8 * hf + (r & 7), lag = REV ? j - c : c - j;
+            const float f = a.kv_scale * a.out_scale, on = lag >= 0 ? power(lag) * f : 0.0f, off = power(32 + lag) * f;
+            d_a[r] = off_diag ? off : on;
+            d_b[r] = off;
         }
     }
 
-    RowsK r1, r2;
-    RowsV r3;
-    auto load = [&](int ch, int buf) {
-        const int t0 = ch * kC, n = min(kC, len - t0);
-        r2.load(a.x2, b, a.L, n2, h2, t0, n, lds + X2 + buf * BK);
-        if constexpr (!AGG) r1.load(a.x1, b, a.L, n1, h1, t0, n, lds + X1);
-        r3.load(a.x3, b, a.L, n3, h3, t0, n, lds + X3);
-    };
-    // the loaded chunk's tiles complete and visible to every wave
-    auto stage = [&](int ch, int buf) {
-        const int n = min(kC, len - ch * kC);
-        if constexpr (BF16) {
-            landed();
-            if (n < kC) {
-                __syncthreads();
-                if constexpr (!AGG) RowsK::clear(lds + X1, n);
-                RowsK::clear(lds + X2 + buf * BK, n);
-                RowsV::clear(lds + X3, n);
-            }
-        } else {
-            if constexpr (!AGG) r1.store(lds + X1);
-            r2.store(lds + X2);
-            r3.store(lds + X3);
-        }
-        __syncthreads();
-    };
-
-    // outputs of this wave's 32 columns of row block I (rows t0 + 32 I + c)
+    // outputs of this wave's 32 columns of row block I (rows t0 + 32 I + c); rows past the
+    // sequence's end are out of range, so the number of stores is always the same
+    // A lane holds 32 (or, fp32, 64) bytes of one row in pieces of 16; pieces are exchanged
+    // between lanes 16 apart so that a store covers 64 consecutive bytes of 16 rows and not
+    // 32 of 32.
+    const uint32_t orow = (uint32_t)a.H * VD * (BF16 && !a.out_f32 ? 2 : 4);
     auto put = [&](int t0, int I, const f32x16& acc) {
-        const int row = 32 * I + c;
-        if (t0 + row >= a.L) return;
-        const size_t at = ((size_t)((size_t)b * a.L + t0 + row) * a.H + h) * VD + 32 * wave + 8 * hf;
+        const int es = BF16 && !a.out_f32 ? 2 : 4;
+        const int nr = min(kC, a.L - t0);
+        const auto out = make_rsrc(static_cast<char*>(a.out) + (((size_t)b * a.L + t0) * a.H + h) * (size_t)(VD * es),
+                                   (uint32_t)(nr - 1) * orow + VD * es);
+        // pieces x and y of this lane's row; col: where the piece this lane then has begins
+        auto pair = [&](u32x4 x, u32x4 y, uint32_t col) {
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            if (BF16 && !a.out_f32) {
-                bf16x8 y;
+            for (int e = 0; e < 4; ++e) {
+                const auto z = __builtin_amdgcn_permlane16_swap(x[e], y[e], false, false);
+                x[e] = z[0];
+                y[e] = z[1];
+            }
+            const uint32_t off = (uint32_t)(32 * I + (c & 15)) * orow + (uint32_t)(32 * wave * es) + col;
+            __builtin_amdgcn_raw_buffer_store_b128(x, out, (int)off, 0, 0);
+            __builtin_amdgcn_raw_buffer_store_b128(y, out, (int)(off + 16 * orow), 0, 0);
+        };
+        if (BF16 && !a.out_f32) {
+            bf16x8 y[2];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = (__bf16)acc[8 * s + e];
-                *reinterpret_cast<bf16x8*>(static_cast<uint16_t*>(a.out) + at + 16 * s) = y;
-            } else {
-                f32x4* p = reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + at + 16 * s);
+            for (int e = 0; e < 16; ++e) y[e >> 3][e & 7] = (__bf16)acc[e];
+            pair(__builtin_bit_cast(u32x4, y[0]), __builtin_bit_cast(u32x4, y[1]), (c >> 4) * 32 + hf * 16);
+        } else {
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    f32x4 y;
+            for (int s = 0; s < 2; ++s) {
+                u32x4 y[2];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) y[e] = acc[8 * s + 4 * u + e];
-                    p[u] = y;
-                }
+                for (int e = 0; e < 8; ++e) y[e >> 2][e & 3] = __float_as_uint(acc[8 * s + e]);
+                pair(y[0], y[1], 64 * s + hf * 32 + (c >> 4) * 16);
             }
         }
     };
-
     if constexpr (!AGG) {  // chunks of padding alone
         f32x16 zero;
 #pragma unroll
         for (int r = 0; r < 16; ++r) zero[r] = 0.0f;
         for (int ch = ca; ch < c1; ++ch)
-            for (int I = 0; I < 2; ++I) put(ch * kC, I, zero);
+            for (int I = 0; I < 2; ++I)
+                if (ch * kC < a.L) put(ch * kC, I, zero);
     }
-    const Decay full(la * (float)kC);
-    const int nch = ca - c0;
-    auto chunk_at = [&](int u) { return REV ? ca - 1 - u : c0 + u; };
-    if (nch > 0) {
-        load(chunk_at(0), 0);
-        stage(chunk_at(0), 0);
-    }
+
+    // chunk u's tiles complete and visible to every wave. A chunk's stores of outputs are
+    // issued after the loads of the next one's rows and need not be waited for (vmcnt
+    // counts both in the order of issue; every wave issues 4 of bf16, 8 of fp32).
+    auto stage = [&](int u, bool stores) {
+        const int n = min(kC, len - chunk_at(u) * kC);
+        lds_t* x1 = lds + Ld::X1 + u % Ld::N13 * Ld::BK;
+        lds_t* x2 = lds + Ld::X2 + u % Ld::N2 * Ld::BK;
+        lds_t* x3 = lds + Ld::X3 + u % Ld::N13 * Ld::BV;
+        if constexpr (BF16) {
+            if (!stores) landed<0>();
+            else if (a.out_f32) landed<8>();
+            else landed<4>();
+            if (n < kC) {
+                __syncthreads();
+                if constexpr (!AGG) RowsK::clear(x1, n);
+                RowsK::clear(x2, n);
+                RowsV::clear(x3, n);
+            }
+        } else {
+            if constexpr (!AGG) r1.store(x1);
+            r2.store(x2);
+            r3.store(x3);
+        }
+        __syncthreads();
+    };
+
+    ChunkDecay full(la * (float)kC);
+    if (nch > 0) stage(0, false);
     for (int u = 0; u < nch; ++u) {
         const int t0 = chunk_at(u) * kC, n = min(kC, len - t0);
-        const lds_t* x2 = lds + X2 + (BF16 ? (u & 1) * BK : 0);
+        const lds_t* x1 = lds + Ld::X1 + u % Ld::N13 * Ld::BK;
+        const lds_t* x2 = lds + Ld::X2 + u % Ld::N2 * Ld::BK;
+        const lds_t* x3 = lds + Ld::X3 + u % Ld::N13 * Ld::BV;
+        if (Ld::FULL && u + 1 < nch) load(u + 1);
         Op v[4];
         auto read_v = [&]() {
 #pragma unroll
-            for (int s = 0; s < 4; ++s) v[s] = Ty::template col8<VD>(lds + X3, 16 * s, 32 * wave);
+            for (int s = 0; s < 4; ++s) v[s] = Ty::template col8<VD>(x3, 16 * s, 32 * wave);
         };
-        if constexpr (AGG) read_v();
-        // x1 and x3 are read: their tiles take the next chunk
-        auto next = [&]() {
-            __syncthreads();
-            if (u + 1 < nch) load(chunk_at(u + 1), (u + 1) & 1);
-        };
-        if constexpr (AGG && BF16) next();
-        if constexpr (!AGG) {
-            f32x16 acc[2], m00, m11, mx;
-#pragma unroll
-            for (int r = 0; r < 16; ++r) acc[0][r] = acc[1][r] = m00[r] = m11[r] = mx[r] = 0.0f;
+        if constexpr (AGG) {
+            read_v();
+        } else {
             // scores (rows j in the order pi, columns i) and x1 S (rows: columns of S); the
             // operands of step ks + 1 are read while those of ks multiply
-            Op q0, q1, k0, k1;
+            f32x16 acc[2], ma, mb;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[0][r] = acc[1][r] = ma[r] = mb[r] = 0.0f;
+            const lds_t* xj = x2 + Ja * (Ld::BK / 2);
+            const lds_t* xi = x1 + Ia * (Ld::BK / 2);
+            Op q0, q1, qa, ka, kb;
             auto fetch = [&](int ks) {
-                q0 = Ty::template row8<KD>(lds + X1, c, ks);
-                q1 = Ty::template row8<KD>(lds + X1, 32 + c, ks);
-                k0 = Ty::template row8<KD>(x2, pi(c), ks);
-                k1 = Ty::template row8<KD>(x2, 32 + pi(c), ks);
+                q0 = Ty::template row8<KD>(x1, c, ks);
+                q1 = Ty::template row8<KD>(x1, 32 + c, ks);
+                ka = Ty::template row8<KD>(xj, pi(c), ks);
+                if constexpr (NT == 256) qa = Ty::template row8<KD>(xi, c, ks);
+                else kb = Ty::template row8<KD>(x2, (REV ? 32 : 0) + pi(c), ks);
             };
             fetch(0);
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
-                const Op p0 = q0, p1 = q1, l0 = k0, l1 = k1;
+                const Op p0 = q0, p1 = q1, pa = NT == 256 ? qa : (wave ? q1 : q0), la_ = ka, lb = kb;
                 if (ks + 1 < KS) fetch(ks + 1);
-                const typename Ty::Formed sf = Ty::form(half_of(S[ks >> 1], ks & 1));
-                m00 = Ty::mma(l0, p0, m00);
-                m11 = Ty::mma(l1, p1, m11);
-                mx = REV ? Ty::mma(l1, p0, mx) : Ty::mma(l0, p1, mx);
+                const Formed sf = Ty::form(half_of(S[ks >> 1], ks & 1));
+                ma = Ty::mma(la_, pa, ma);
                 acc[0] = Ty::template part<0>(sf, p0, acc[0]);
                 acc[1] = Ty::template part<0>(sf, p1, acc[1]);
+                if constexpr (NT != 256) mb = Ty::mma(lb, REV ? p0 : p1, mb);
                 if constexpr (Ty::PARTS == 2) {
                     acc[0] = Ty::template part<1>(sf, p0, acc[0]);
                     acc[1] = Ty::template part<1>(sf, p1, acc[1]);
                 }
                 __builtin_amdgcn_sched_barrier(0);
             }
+            auto pass = [&](const f32x16& m, const f32x16& d, int slot) {
+                f32x16 x;
+#pragma unroll
+                for (int r = 0; r < 16; ++r) x[r] = m[r] * d[r];
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    const Formed f = Ty::form(half_of(x, s));
+                    u32x4 q[2];
+                    __builtin_memcpy(q, &f, 32);
+                    lds_u32x4* to = reinterpret_cast<lds_u32x4*>(lds + Ld::M + (2 * slot + s) * 2048) + lane;
+                    to[0] = q[0];
+                    to[64] = q[1];
+                }
+            };
+            if (wave < 3) pass(ma, d_a, wave);
+            if (NT != 256 && wave == 0) pass(mb, d_b, 2);
             read_v();
-            if constexpr (BF16) next();
+            __syncthreads();  // the scores visible; x1 and x3 read
+            if (BF16 && !Ld::FULL && u + 1 < nch) load(u + 1);
             const float w0 = power(REV ? max(n - 1 - c, 0) : c + 1) * a.out_scale;
             const float w1 = power(REV ? max(n - 33 - c, 0) : c + 33) * a.out_scale;
 #pragma unroll
@@ -499,21 +573,18 @@ mix_chunks(Mix a, Geom geo) {
                 acc[0][r] *= w0;
                 acc[1][r] *= w1;
             }
-            auto decayed = [&](const f32x16& m, int which, int s) {
-                const f32x4 d0 = tab[(4 * which + 2 * s) * 64 + lane], d1 = tab[(4 * which + 2 * s + 1) * 64 + lane];
-                f32x8 x;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    x[e] = m[8 * s + e] * d0[e];
-                    x[4 + e] = m[8 * s + 4 + e] * d1[e];
-                }
-                return Ty::form(x);
+            auto formed = [&](int slot, int s) {
+                const lds_u32x4* m = reinterpret_cast<const lds_u32x4*>(lds + Ld::M + (2 * slot + s) * 2048) + lane;
+                const u32x4 q[2] = {m[0], m[64]};
+                Formed f;
+                __builtin_memcpy(&f, q, 32);
+                return f;
             };
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
-                const typename Ty::Formed f0 = decayed(m00, 0, s), f1 = decayed(m11, 0, s), fx = decayed(mx, 1, s);
+                const Formed f0 = formed(0, s), f1 = formed(1, s), fx = formed(2, s);
                 f32x16 &ax = acc[REV ? 0 : 1], &ay = acc[REV ? 1 : 0];
-                const typename Ty::Formed &gx = REV ? f0 : f1, &gy = REV ? f1 : f0;
+                const Formed &gx = REV ? f0 : f1, &gy = REV ? f1 : f0;
                 const Op vx = v[REV ? s : 2 + s], vy = v[REV ? 2 + s : s];
                 ax = Ty::template part<0>(vx, gx, ax);
                 ay = Ty::template part<0>(vy, gy, ay);
@@ -534,55 +605,77 @@ mix_chunks(Mix a, Geom geo) {
             put(t0, 0, acc[0]);
             put(t0, 1, acc[1]);
         }
-        if constexpr (!BF16) {
-            if (u + 1 < nch) load(chunk_at(u + 1), 0);
-        }
+        if (!BF16 && u + 1 < nch) load(u + 1);
         if (AGG || u + 1 < nch || a.final_state) {
-            const Decay decay = n == kC ? full : Decay(la * (float)n);
-#pragma unroll
-            for (int T = 0; T < KT; ++T)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) S[T][r] = decay(S[T][r]);
-#pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                f32x8 x = Ty::widen(v[s]);
-                const lds_f32* w = wt + 16 * s + 8 * hf + (REV ? 0 : kC - n);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] *= w[e];
-                const typename Ty::Formed wv = Ty::form(x);
-                Op k[KT];
+            // the operands of step s + 1 are read and formed while those of step s multiply
+            const lds_f32* w0 = wt + 8 * hf + (REV ? 0 : kC - n);
+            Op k[KT];
+            f32x8 w;
+            auto fetch = [&](int s) {
 #pragma unroll
                 for (int T = 0; T < KT; ++T) k[T] = Ty::template col8<KD>(x2, 16 * s, 32 * T);
 #pragma unroll
-                for (int T = 0; T < KT; ++T) S[T] = Ty::template part<0>(k[T], wv, S[T]);
+                for (int e = 0; e < 8; ++e) w[e] = w0[16 * s + e];
+            };
+            auto weighted = [&](int s) {
+                f32x8 x = Ty::widen(v[s]);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] *= w[e];
+                return Ty::form(x);
+            };
+            fetch(0);
+            const float m = n == kC ? full.next() : expf(la * (float)n);  // at most one chunk is shorter
+#pragma unroll
+            for (int T = 0; T < KT; ++T)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) S[T][r] *= m;
+            Formed wv = weighted(0);
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                Op kn[KT];
+#pragma unroll
+                for (int T = 0; T < KT; ++T) kn[T] = k[T];
+                if (s < 3) fetch(s + 1);
+#pragma unroll
+                for (int T = 0; T < KT; ++T) S[T] = Ty::template part<0>(kn[T], wv, S[T]);
+                const Formed next = s < 3 ? weighted(s + 1) : wv;
                 if constexpr (Ty::PARTS == 2)
 #pragma unroll
-                    for (int T = 0; T < KT; ++T) S[T] = Ty::template part<1>(k[T], wv, S[T]);
+                    for (int T = 0; T < KT; ++T) S[T] = Ty::template part<1>(kn[T], wv, S[T]);
+                wv = next;
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
         if constexpr (!BF16) __syncthreads();  // every read of the tiles done
-        if (u + 1 < nch) stage(chunk_at(u + 1), (u + 1) & 1);
+        if (u + 1 < nch) stage(u + 1, !AGG);
     }
 
-    float* dst = nullptr;
-    if constexpr (AGG) dst = a.slots + (bh * (geo.NS - 1) + (REV ? sc - 1 : sc)) * KD * VD;
-    else if (a.final_state && (REV ? sc == 0 : sc == geo.NS - 1)) dst = a.final_state + bh * KD * VD;
-    if (dst) each_state_element<KD, VD>(AGG && a.trans, [&](int T, int r, int at) { dst[at] = S[T][r]; });
+    if constexpr (AGG) {
+        float* dst = a.slots + (bh * (geo.NS - 1) + (REV ? sc - 1 : sc)) * KD * VD;
+        if (a.trans) each_state_element<KD>([&](int T, int r, int k, int j) { dst[slot_at(j, k, KD)] = S[T][r]; });
+        else each_state_element<KD>([&](int T, int r, int k, int j) { dst[slot_at(k, j, VD)] = S[T][r]; });
+    } else if (a.final_state && (REV ? sc == 0 : sc == geo.NS - 1)) {
+        float* dst = a.final_state + bh * KD * VD;
+        each_state_element<KD>([&](int T, int r, int k, int j) { dst[k * VD + j] = S[T][r]; });
+    }
 }
 
 // Aggregates -> entering states, in the run's direction: what super-chunk s adds, plus
 // lam^(its steps) times the state entering it, enters the next. One lane per four
 // state elements; eight slots are loaded before any is written.
-__global__ void __launch_bounds__(256) mix_carry(Mix a, Geom geo, int n4, int rev) {
+__global__ void __launch_bounds__(256) mix_carry(Mix a, Geom geo, int n4, int J, int rev) {
     const int e = blockIdx.x * 256 + threadIdx.x;
     const int bh = blockIdx.y, b = bh / a.H, h = bh % a.H;
     if (e >= n4) return;
     const int len = seq_len(a.seqlens, b, a.L), K = geo.NS - 1;
     const float la = log_decay_of(a.log_decay, h);
-    const float4* init = reinterpret_cast<const float4*>(a.init);
     float4* slot = reinterpret_cast<float4*>(a.slots) + (size_t)bh * K * n4 + e;
-    float4 v = init ? init[(size_t)bh * n4 + e] : make_float4(0.f, 0.f, 0.f, 0.f);
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (a.init) {  // elements 4 e .. 4 e + 3 of a slot: rows i .. i + 3 of column j of [I, J]
+        const int j = (e >> 1) % J, i = ((e >> 1) / J) * 8 + 4 * (e & 1);
+        const float* p = a.init + ((size_t)bh * (n4 / J * 4) + i) * J + j;
+        v = make_float4(p[0], p[J], p[2 * J], p[3 * J]);
+    }
     for (int k0 = 0; k0 < K; k0 += 8) {
         float4 sl[8];
 #pragma unroll
@@ -628,7 +721,8 @@ hipError_t run_mix_t(const Mix& m, bool agg, hipStream_t st) {
         launch((mix_chunks<KD, VD, BF16, REV, true>), dim3((unsigned)m.B * m.H * (g.NS - 1)), block, 0, st, m, g);
         if ((e = hipGetLastError()) != hipSuccess) return e;
         const int n4 = KD * VD / 4;
-        launch(mix_carry, dim3((n4 + 255) / 256, (unsigned)m.B * m.H), dim3(256), 0, st, m, g, n4, (int)REV);
+        launch(mix_carry, dim3((n4 + 255) / 256, (unsigned)m.B * m.H), dim3(256), 0, st, m, g, n4,
+               m.trans ? KD : VD, (int)REV);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     launch((mix_chunks<KD, VD, BF16, REV, false>), dim3((unsigned)m.B * m.H * g.NS), block, 0, st, m, g);
