@@ -231,46 +231,31 @@ __device__ __forceinline__ f32x8 half_of(const f32x16& a, int s) {
     return v;
 }
 
-// Rows t0 .. t0 + kC - 1 of one head of x1, x2 or x3 into a Tile. Rows at or past n are out
-// of the buffer's range (row i starts at i row bytes, the range ends inside row n - 1).
+// Rows t0 .. t0 + kC - 1 of one head of x1, x2 or x3 into a Tile, straight into LDS, 1 KB per
+// wave and instruction. The compiler does not know of these loads: landed() and a barrier
+// stand before the tile is read. Rows at or past n are out of the buffer's range (row i
+// starts at i row bytes, the range ends inside row n - 1) and are cleared where there are any.
 template <int D, int NT, bool BF16>
 struct Rows {
     typedef Tile<D, BF16> Ti;
     static constexpr int P = Ti::P, N = kC * P / NT;  // pieces per row, per thread
-    u32x4 v[BF16 ? 1 : N];                            // fp32: on the way through registers
-    __device__ __forceinline__ void load(const void* x, size_t b, int L, int nh, int h, int t0, int n, lds_t* t) {
+    static __device__ __forceinline__ void load(const void* x, size_t b, int L, int nh, int h, int t0, int n, lds_t* t) {
         const uint32_t row = (uint32_t)nh * Ti::RB;
         const char* base = static_cast<const char*>(x) + ((b * L + t0) * nh + h) * (size_t)Ti::RB;
         const auto r = make_rsrc(base, (uint32_t)(n - 1) * row + Ti::RB);
         const int tid = threadIdx.x;
-        if constexpr (BF16) {
-            // straight into LDS, 1 KB per wave and instruction; not known to the compiler:
-            // landed() and a barrier stand before the tile is read
-            const uint32_t base_lds = (uint32_t)(uintptr_t)t + (uint32_t)__builtin_amdgcn_readfirstlane(tid >> 6) * 1024;
+        const uint32_t to = (uint32_t)(uintptr_t)t + (uint32_t)__builtin_amdgcn_readfirstlane(tid >> 6) * 1024;
 #pragma unroll
-            for (int k = 0; k < N; ++k) {
-                const int rr = tid / P + k * (NT / P);
-                const uint32_t off = (uint32_t)rr * row + (((tid % P) ^ Ti::swz(rr)) << 4);
-                uint32_t m0;  // the LDS address goes through m0, which is left as it was
-                asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\tbuffer_load_dwordx4 %2, %3, 0 offen lds\n\t"
-                             "s_mov_b32 m0, %0"
-                             : "=&s"(m0)
-                             : "s"(base_lds + k * NT * 16), "v"(off), "s"(r)
-                             : "memory");
-            }
-        } else {
-#pragma unroll
-            for (int k = 0; k < N; ++k) {
-                uint32_t off = (uint32_t)(tid / P + k * (NT / P)) * row + (tid % P) * 16;
-                v[k] = __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, 0);
-            }
+        for (int k = 0; k < N; ++k) {
+            const int rr = tid / P + k * (NT / P);
+            const uint32_t off = (uint32_t)rr * row + (((tid % P) ^ Ti::swz(rr)) << 4);
+            uint32_t m0;  // the LDS address goes through m0, which is left as it was
+            asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\tbuffer_load_dwordx4 %2, %3, 0 offen lds\n\t"
+                         "s_mov_b32 m0, %0"
+                         : "=&s"(m0)
+                         : "s"(to + k * NT * 16), "v"(off), "s"(r)
+                         : "memory");
         }
-    }
-    __device__ __forceinline__ void store(lds_t* t) const {
-        if constexpr (!BF16)
-#pragma unroll
-            for (int k = 0; k < N; ++k)
-                *reinterpret_cast<lds_u32x4*>(t + Ti::at(threadIdx.x / P + k * (NT / P), threadIdx.x % P)) = v[k];
     }
     // zeros in the rows at or past n
     static __device__ __forceinline__ void clear(lds_t* t, int n) {
@@ -336,8 +321,8 @@ struct ChunkDecay {
 template <int KD, int VD, bool BF16, bool AGG>
 struct Lds {
     static constexpr int BK = Tile<KD, BF16>::BYTES, BV = Tile<VD, BF16>::BYTES;
-    static constexpr bool FULL = BF16 && (AGG || (KD == 64 && VD == 128));
-    static constexpr int N2 = BF16 ? 2 : 1, N13 = FULL ? 2 : 1;
+    static constexpr bool FULL = AGG || (BF16 && KD == 64 && VD == 128);
+    static constexpr int N2 = 2, N13 = FULL ? 2 : 1;
     static constexpr int X2 = 0, X3 = X2 + N2 * BK, X1 = X3 + N13 * BV, W = X1 + (AGG ? 0 : N13 * BK),
                          M = W + 128 * 4, TOTAL = M + (AGG ? 0 : 3 * 2 * 2048);
 };
@@ -371,14 +356,12 @@ mix_chunks(Mix a, Geom geo) {
     const int ca = max(c0, min(c1, (len + kC - 1) / kC)), nch = ca - c0;
     auto chunk_at = [&](int u) { return REV ? ca - 1 - u : c0 + u; };
 
-    RowsK r1, r2;
-    RowsV r3;
     // chunk u's rows into its buffers
     auto load = [&](int u) {
         const int t0 = chunk_at(u) * kC, n = min(kC, len - t0), b2 = u % Ld::N2, b13 = u % Ld::N13;
-        r2.load(a.x2, b, a.L, n2, h2, t0, n, lds + Ld::X2 + b2 * Ld::BK);
-        if constexpr (!AGG) r1.load(a.x1, b, a.L, n1, h1, t0, n, lds + Ld::X1 + b13 * Ld::BK);
-        r3.load(a.x3, b, a.L, n3, h3, t0, n, lds + Ld::X3 + b13 * Ld::BV);
+        RowsK::load(a.x2, b, a.L, n2, h2, t0, n, lds + Ld::X2 + b2 * Ld::BK);
+        if constexpr (!AGG) RowsK::load(a.x1, b, a.L, n1, h1, t0, n, lds + Ld::X1 + b13 * Ld::BK);
+        RowsV::load(a.x3, b, a.L, n3, h3, t0, n, lds + Ld::X3 + b13 * Ld::BV);
     };
     if (nch > 0) load(0);
 
@@ -482,20 +465,14 @@ mix_chunks(Mix a, Geom geo) {
         lds_t* x1 = lds + Ld::X1 + u % Ld::N13 * Ld::BK;
         lds_t* x2 = lds + Ld::X2 + u % Ld::N2 * Ld::BK;
         lds_t* x3 = lds + Ld::X3 + u % Ld::N13 * Ld::BV;
-        if constexpr (BF16) {
-            if (!stores) landed<0>();
-            else if (a.out_f32) landed<8>();
-            else landed<4>();
-            if (n < kC) {
-                __syncthreads();
-                if constexpr (!AGG) RowsK::clear(x1, n);
-                RowsK::clear(x2, n);
-                RowsV::clear(x3, n);
-            }
-        } else {
-            if constexpr (!AGG) r1.store(x1);
-            r2.store(x2);
-            r3.store(x3);
+        if (!stores) landed<0>();
+        else if (!BF16 || a.out_f32) landed<8>();
+        else landed<4>();
+        if (n < kC) {
+            __syncthreads();
+            if constexpr (!AGG) RowsK::clear(x1, n);
+            RowsK::clear(x2, n);
+            RowsV::clear(x3, n);
         }
         __syncthreads();
     };
@@ -565,7 +542,7 @@ mix_chunks(Mix a, Geom geo) {
             if (NT != 256 && wave == 0) pass(mb, d_b, 2);
             read_v();
             __syncthreads();  // the scores visible; x1 and x3 read
-            if (BF16 && !Ld::FULL && u + 1 < nch) load(u + 1);
+            if (!Ld::FULL && u + 1 < nch) load(u + 1);
             const float w0 = power(REV ? max(n - 1 - c, 0) : c + 1) * a.out_scale;
             const float w1 = power(REV ? max(n - 33 - c, 0) : c + 33) * a.out_scale;
 #pragma unroll
@@ -605,7 +582,6 @@ mix_chunks(Mix a, Geom geo) {
             put(t0, 0, acc[0]);
             put(t0, 1, acc[1]);
         }
-        if (!BF16 && u + 1 < nch) load(u + 1);
         if (AGG || u + 1 < nch || a.final_state) {
             // the operands of step s + 1 are read and formed while those of step s multiply
             const lds_f32* w0 = wt + 8 * hf + (REV ? 0 : kC - n);
@@ -646,7 +622,6 @@ mix_chunks(Mix a, Geom geo) {
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
-        if constexpr (!BF16) __syncthreads();  // every read of the tiles done
         if (u + 1 < nch) stage(u + 1, !AGG);
     }
 
