@@ -64,11 +64,6 @@ typedef __attribute__((address_space(3))) bf16x8 lds_bf16x8;
 typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
 
 constexpr int kC = 64;  // steps per chunk
-#ifndef SSM_LINATTN_BLOCKS
-#define SSM_LINATTN_BLOCKS 512
-#endif
-constexpr int kTargetBlocks = SSM_LINATTN_BLOCKS;
-
 // One run of the operator: x1, x2 [B, L, ., KD], x3 [B, L, ., VD], out [B, L, H, VD].
 struct Mix {
     int B, L, H, r;       // r heads share a group of queries and keys
@@ -88,26 +83,67 @@ struct Mix {
     float* final_state;   // [B, H, KD, VD] or NULL
 };
 
+// Up to three runs that one launch does side by side.
+struct Jobs {
+    Mix m[3];
+    int rev[3];  // backwards in time
+    int n;
+};
+
 struct Geom {
     int NC;   // chunks per sequence
     int cps;  // chunks per super-chunk
     int NS;   // super-chunks per sequence
 };
 
-Geom geom(int B, int L, int H) {
-    Geom g;
-    g.NC = std::max(1, (L + kC - 1) / kC);
-    const long bh = (long)B * H;
-    const long want = std::max<long>(1, std::min<long>((kTargetBlocks + bh - 1) / bh, g.NC));
-    g.cps = (int)((g.NC + want - 1) / want);
-    g.NS = (g.NC + g.cps - 1) / g.cps;
-    return g;
+// How many workgroups of mix_chunks fit a CU, by their LDS and registers.
+int per_cu(int KD, int VD, bool bf16) {
+    const int es = bf16 ? 2 : 4, lds = kC * (3 * KD + VD) * es + 128 * 4 + 3 * 2 * 2048;
+    return std::min(163840 / lds, VD == 128 ? 2 : 3);
 }
 
-template <bool BF16>
-__device__ __forceinline__ void st1(void* p, size_t i, float v) {
-    if constexpr (BF16) static_cast<uint16_t*>(p)[i] = f32_to_bf16(v);
-    else static_cast<float*>(p)[i] = v;
+// The number of super-chunks with the least estimated time. The unit is one chunk of a
+// bf16 workgroup that has its CU to itself (3.3 us at K = V = 128). Workgroups that share a
+// CU slow each other down: by 1.25 while every wave still has a SIMD of its own, by 1.6
+// beyond that (measured at B4 L4096 H16 K = V = 128: 3.3 us a chunk alone, 5.2 as one of two;
+// B4 L8000 H24 K128 V64: 3.7 and 4.7); fp32 takes three times as long. A workgroup begins and
+// ends with its state (2 units). No launch is faster than its rows at 4 TB/s (13 MB a unit;
+// rows shared by heads are read once). More than one super-chunk adds the aggregates (half
+// a unit a chunk) and the carry. Measured optima are within 4% of what this picks: B1 L4096
+// H16 K = V = 128 takes 197 us with one, 55 with 8, 50 with 16, 55 with 32.
+Geom geom(int B, int L, int H, int G, int K, int V, bool bf16, bool bwd) {
+    const long bh = (long)B * H;
+    const int NC = std::max(1, (L + kC - 1) / kC), r = H / G;
+    const double rows = (double)B * G * L * (bf16 ? 2 : 4) / 13e6;  // units per value of a group's row
+    auto scan = [&](int jobs, int KD, int VD, double values, int NS, int cps) {
+        const long wg = jobs * bh * NS, slots = 256L * per_cu(KD, VD, bf16);
+        const double share = wg <= 256 ? 1.0 : VD == 64 || slots == 256 ? 1.25 : 1.6;
+        const double t = (double)((wg + slots - 1) / slots) * share * (cps * (bf16 ? 1.0 : 3.0) + 2.0);
+        return std::max(t, rows * values);
+    };
+    const int dqk = 2 * (2 * r * V + K + r * K), dv = 2 * K + 2 * r * V;
+    Geom best{NC, NC, 1};
+    double least = 0.0;
+    for (int want = 1; want <= NC && (want == 1 || bh * want <= 1536); ++want) {
+        const int cps = (NC + want - 1) / want, NS = (NC + cps - 1) / cps;
+        if (NS != want) continue;
+        double t;
+        if (!bwd) t = scan(1, K, V, 2 * K + 2 * r * V, NS, cps);
+        else if (K == V) t = scan(3, K, V, dqk + dv, NS, cps);
+        else t = scan(2, V, K, dqk, NS, cps) + scan(1, K, V, dv, NS, cps);
+        if (NS > 1) {
+            const int dirs = bwd ? 2 : 1;
+            const long wg = dirs * bh * (NS - 1);
+            t += std::max((double)((wg + 511) / 512) * (0.5 * cps * (bf16 ? 1.0 : 2.0) + 1.0),
+                          dirs * rows * (K + r * V) * (NS - 1) / NS);
+            t += 2.4 + 0.27e-6 * dirs * bh * NS * K * V;
+        }
+        if (want == 1 || t < least) {
+            least = t;
+            best = Geom{NC, cps, NS};
+        }
+    }
+    return best;
 }
 
 __device__ __forceinline__ int seq_len(const int* seqlens, int b, int L) {
@@ -328,8 +364,7 @@ struct Lds {
 };
 
 template <int KD, int VD, bool BF16, bool REV, bool AGG>
-__global__ void __launch_bounds__(2 * VD) __attribute__((amdgpu_waves_per_eu(BF16 ? 2 : 1, BF16 ? 2 : 1)))
-mix_chunks(Mix a, Geom geo) {
+__device__ __forceinline__ void run_chunks(const Mix& a, const Geom& geo, lds_t* lds) {
     typedef Types<BF16> Ty;
     typedef typename Ty::Op Op;
     typedef typename Ty::Formed Formed;
@@ -337,8 +372,6 @@ mix_chunks(Mix a, Geom geo) {
     constexpr int NT = 2 * VD, KS = KD / 16, KT = KD / 32;
     typedef Rows<KD, NT, BF16> RowsK;
     typedef Rows<VD, NT, BF16> RowsV;
-    __shared__ __attribute__((aligned(16))) char lds_raw[Ld::TOTAL];
-    lds_t* lds = (lds_t*)lds_raw;
     int h, sc, b;
     block_coords(a.H, AGG ? geo.NS - 1 : geo.NS, h, sc, b);
     if (AGG && REV) ++sc;
@@ -500,7 +533,7 @@ mix_chunks(Mix a, Geom geo) {
             for (int r = 0; r < 16; ++r) acc[0][r] = acc[1][r] = ma[r] = mb[r] = 0.0f;
             const lds_t* xj = x2 + Ja * (Ld::BK / 2);
             const lds_t* xi = x1 + Ia * (Ld::BK / 2);
-            Op q0, q1, qa, ka, kb;
+            Op q0, q1, qa{}, ka, kb{};
             auto fetch = [&](int ks) {
                 q0 = Ty::template row8<KD>(x1, c, ks);
                 q1 = Ty::template row8<KD>(x1, 32 + c, ks);
@@ -635,10 +668,21 @@ mix_chunks(Mix a, Geom geo) {
     }
 }
 
+template <int KD, int VD, bool BF16, bool AGG>
+__global__ void __launch_bounds__(2 * VD) __attribute__((amdgpu_waves_per_eu(BF16 ? 2 : 1, BF16 ? 2 : 1)))
+mix_chunks(Jobs jobs, Geom geo) {
+    __shared__ __attribute__((aligned(16))) char lds[Lds<KD, VD, BF16, AGG>::TOTAL];
+    const int j = blockIdx.y;
+    if (jobs.rev[j]) run_chunks<KD, VD, BF16, true, AGG>(jobs.m[j], geo, (lds_t*)lds);
+    else run_chunks<KD, VD, BF16, false, AGG>(jobs.m[j], geo, (lds_t*)lds);
+}
+
 // Aggregates -> entering states, in the run's direction: what super-chunk s adds, plus
 // lam^(its steps) times the state entering it, enters the next. One lane per four
 // state elements; eight slots are loaded before any is written.
-__global__ void __launch_bounds__(256) mix_carry(Mix a, Geom geo, int n4, int J, int rev) {
+__global__ void __launch_bounds__(256) mix_carry(Jobs jobs, Geom geo, int n4, int J) {
+    const Mix& a = jobs.m[blockIdx.z];
+    const int rev = jobs.rev[blockIdx.z];
     const int e = blockIdx.x * 256 + threadIdx.x;
     const int bh = blockIdx.y, b = bh / a.H, h = bh % a.H;
     if (e >= n4) return;
@@ -674,98 +718,108 @@ __global__ void __launch_bounds__(256) mix_carry(Mix a, Geom geo, int n4, int J,
 }
 
 // Sum over the r heads of each group of an fp32 [rows, G, r, D] tensor, in head order,
-// rounded once to [rows, G, D].
+// rounded once to [rows, G, D]; two tensors, one after the other. Four values a lane.
 template <bool BF16>
-__global__ void __launch_bounds__(256) sum_heads(const float* __restrict__ p, void* out, size_t n, int r, int D) {
+__global__ void __launch_bounds__(256)
+sum_heads(const float* __restrict__ p, void* out0, void* out1, size_t n4, int r, int D4) {
     const size_t e = (size_t)blockIdx.x * 256 + threadIdx.x;
-    if (e >= n) return;
-    const float* q = p + (e / D) * r * D + e % D;
-    float s = 0.0f;
-    for (int k = 0; k < r; ++k) s += q[(size_t)k * D];
-    st1<BF16>(out, e, s);
-}
-
-// With agg, the aggregates and the carry first (where there is more than one
-// super-chunk); without, the slots already hold the entering states.
-template <int KD, int VD, bool BF16, bool REV>
-hipError_t run_mix_t(const Mix& m, bool agg, hipStream_t st) {
-    const Geom g = geom(m.B, m.L, m.H);
-    const dim3 block(2 * VD);
-    hipError_t e;
-    if (agg && g.NS > 1) {
-        launch((mix_chunks<KD, VD, BF16, REV, true>), dim3((unsigned)m.B * m.H * (g.NS - 1)), block, 0, st, m, g);
-        if ((e = hipGetLastError()) != hipSuccess) return e;
-        const int n4 = KD * VD / 4;
-        launch(mix_carry, dim3((n4 + 255) / 256, (unsigned)m.B * m.H), dim3(256), 0, st, m, g, n4,
-               m.trans ? KD : VD, (int)REV);
-        if ((e = hipGetLastError()) != hipSuccess) return e;
+    if (e >= n4) return;
+    const f32x4* q = reinterpret_cast<const f32x4*>(p) + blockIdx.y * n4 * r + (e / D4) * r * D4 + e % D4;
+    f32x4 s = q[0];
+    for (int k = 1; k < r; ++k) s += q[(size_t)k * D4];
+    void* out = blockIdx.y ? out1 : out0;
+    if constexpr (BF16) {
+        const bf16x4 y = {(__bf16)s[0], (__bf16)s[1], (__bf16)s[2], (__bf16)s[3]};
+        reinterpret_cast<bf16x4*>(out)[e] = y;
+    } else {
+        reinterpret_cast<f32x4*>(out)[e] = s;
     }
-    launch((mix_chunks<KD, VD, BF16, REV, false>), dim3((unsigned)m.B * m.H * g.NS), block, 0, st, m, g);
-    return hipGetLastError();
 }
 
 template <int KD, int VD>
-hipError_t run_mix_d(const Mix& m, bool bf16, bool rev, bool agg, hipStream_t st) {
-    if (bf16) return rev ? run_mix_t<KD, VD, true, true>(m, agg, st) : run_mix_t<KD, VD, true, false>(m, agg, st);
-    return rev ? run_mix_t<KD, VD, false, true>(m, agg, st) : run_mix_t<KD, VD, false, false>(m, agg, st);
-}
-
-hipError_t run_mix(const Mix& m, int KD, int VD, bool bf16, bool rev, bool agg, hipStream_t st) {
-    if (KD == 64) return VD == 64 ? run_mix_d<64, 64>(m, bf16, rev, agg, st) : run_mix_d<64, 128>(m, bf16, rev, agg, st);
-    return VD == 64 ? run_mix_d<128, 64>(m, bf16, rev, agg, st) : run_mix_d<128, 128>(m, bf16, rev, agg, st);
-}
-
-hipError_t run_sum_heads(const float* p, void* out, size_t n, int r, int D, bool bf16, hipStream_t st) {
-    if (n == 0) return hipSuccess;
-    const dim3 grid((unsigned)((n + 255) / 256));
-    if (bf16) launch(sum_heads<true>, grid, dim3(256), 0, st, p, out, n, r, D);
-    else launch(sum_heads<false>, grid, dim3(256), 0, st, p, out, n, r, D);
+hipError_t run_t(const Jobs& jobs, const Geom& g, bool bf16, bool agg, hipStream_t st) {
+    const Mix& m = jobs.m[0];
+    const dim3 grid((unsigned)m.B * m.H * (agg ? g.NS - 1 : g.NS), (unsigned)jobs.n);
+    if (bf16 && agg) launch((mix_chunks<KD, VD, true, true>), grid, dim3(2 * VD), 0, st, jobs, g);
+    else if (bf16) launch((mix_chunks<KD, VD, true, false>), grid, dim3(2 * VD), 0, st, jobs, g);
+    else if (agg) launch((mix_chunks<KD, VD, false, true>), grid, dim3(2 * VD), 0, st, jobs, g);
+    else launch((mix_chunks<KD, VD, false, false>), grid, dim3(2 * VD), 0, st, jobs, g);
     return hipGetLastError();
 }
 
-size_t slot_bytes(int B, int L, int H, int K, int V) {
-    return (size_t)B * H * (geom(B, L, H).NS - 1) * K * V * 4;
+hipError_t run(const Jobs& jobs, const Geom& g, int KD, int VD, bool bf16, bool agg, hipStream_t st) {
+    if (KD == 64) return VD == 64 ? run_t<64, 64>(jobs, g, bf16, agg, st) : run_t<64, 128>(jobs, g, bf16, agg, st);
+    return VD == 64 ? run_t<128, 64>(jobs, g, bf16, agg, st) : run_t<128, 128>(jobs, g, bf16, agg, st);
 }
+
+// Aggregates and carry of runs whose states are K x V, or held as such (trans). More than
+// one super-chunk means fewer than 4096 (batch, head)s, which the carry's grid.y holds.
+hipError_t run_carry(const Jobs& jobs, const Geom& g, int KD, int VD, bool bf16, hipStream_t st) {
+    if (g.NS == 1) return hipSuccess;
+    const hipError_t e = run(jobs, g, KD, VD, bf16, true, st);
+    if (e != hipSuccess) return e;
+    const Mix& m = jobs.m[0];
+    const int n4 = KD * VD / 4;
+    launch(mix_carry, dim3((n4 + 255) / 256, (unsigned)m.B * m.H, (unsigned)jobs.n), dim3(256), 0, st, jobs, g, n4,
+           m.trans ? KD : VD);
+    return hipGetLastError();
+}
+
+size_t slot_bytes(int B, int H, int K, int V, const Geom& g) { return (size_t)B * H * (g.NS - 1) * K * V * 4; }
 
 }  // namespace
 
 bool linattn_supported_dim(int d) { return d == 64 || d == 128; }
 
 // entering states of the super-chunks
-size_t linattn_workspace_bytes(int B, int L, int H, int, int K, int V, bool) { return slot_bytes(B, L, H, K, V); }
+size_t linattn_workspace_bytes(int B, int L, int H, int G, int K, int V, bool bf16) {
+    return slot_bytes(B, H, K, V, geom(B, L, H, G, K, V, bf16, false));
+}
 
-// the same (one direction at a time), and the fp32 dq or dk per head where heads share a group
-size_t linattn_bwd_workspace_bytes(int B, int L, int H, int G, int K, int V, bool) {
-    return slot_bytes(B, L, H, K, V) + (H == G ? 0 : (size_t)B * L * H * K * 4);
+// those of both directions, and fp32 dq and dk per head where heads share a group
+size_t linattn_bwd_workspace_bytes(int B, int L, int H, int G, int K, int V, bool bf16) {
+    return 2 * slot_bytes(B, H, K, V, geom(B, L, H, G, K, V, bf16, true)) + (H == G ? 0 : 2 * (size_t)B * L * H * K * 4);
 }
 
 hipError_t launch_linattn_fwd(const LinattnArgs& a, hipStream_t st) {
+    const Geom g = geom(a.B, a.L, a.H, a.G, a.K, a.V, a.bf16, false);
     const Mix m{a.B, a.L, a.H, a.H / a.G, a.q, a.k, a.v, 1, 1, 0, a.log_decay, a.seqlens,
                 a.scale, 1.0f, a.h0, static_cast<float*>(a.ws), 0, a.o, 0, a.h_final};
-    return run_mix(m, a.K, a.V, a.bf16, false, true, st);
+    const Jobs jobs{{m}, {0}, 1};
+    const hipError_t e = run_carry(jobs, g, a.K, a.V, a.bf16, st);
+    return e != hipSuccess ? e : run(jobs, g, a.K, a.V, a.bf16, false, st);
 }
 
 hipError_t launch_linattn_bwd(const LinattnBwdArgs& a, hipStream_t st) {
+    const Geom g = geom(a.B, a.L, a.H, a.G, a.K, a.V, a.bf16, true);
     const int r = a.H / a.G;
     const bool shared = r > 1;
-    const size_t ng = (size_t)a.B * a.L * a.G * a.K;
+    const size_t ng = (size_t)a.B * a.L * a.G * a.K, ns = slot_bytes(a.B, a.H, a.K, a.V, g) / 4;
     float* slots = static_cast<float*>(a.ws);
-    float* heads = slots + slot_bytes(a.B, a.L, a.H, a.K, a.V) / 4;
-    hipError_t e;
+    float* heads = slots + 2 * ns;
     // dq: the state v (x) k of the forward run, held transposed (as [K, V], like h0)
     const Mix mq{a.B, a.L, a.H, r, a.dout, a.v, a.k, 0, 0, 1, a.log_decay, a.seqlens,
                  a.scale, 1.0f, a.h0, slots, 1, shared ? heads : a.dq, shared, nullptr};
-    if ((e = run_mix(mq, a.V, a.K, a.bf16, false, true, st)) != hipSuccess) return e;
-    if (shared)
-        if ((e = run_sum_heads(heads, a.dq, ng, r, a.K, a.bf16, st)) != hipSuccess) return e;
-    // dv, then dk from the same entering states, read transposed
+    // dv, and dk from the same entering states, read transposed
     const Mix mv{a.B, a.L, a.H, r, a.k, a.q, a.dout, 1, 1, 0, a.log_decay, a.seqlens,
-                 1.0f, a.scale, a.dh_final, slots, 0, a.dv, 0, a.dh0};
-    if ((e = run_mix(mv, a.K, a.V, a.bf16, true, true, st)) != hipSuccess) return e;
+                 1.0f, a.scale, a.dh_final, slots + ns, 0, a.dv, 0, a.dh0};
     const Mix mk{a.B, a.L, a.H, r, a.v, a.dout, a.q, 0, 0, 1, a.log_decay, a.seqlens,
-                 1.0f, a.scale, a.dh_final, slots, 1, shared ? heads : a.dk, shared, nullptr};
-    if ((e = run_mix(mk, a.V, a.K, a.bf16, true, false, st)) != hipSuccess) return e;
-    return shared ? run_sum_heads(heads, a.dk, ng, r, a.K, a.bf16, st) : hipSuccess;
+                 1.0f, a.scale, a.dh_final, slots + ns, 1, shared ? heads + ng * r : a.dk, shared, nullptr};
+    hipError_t e;
+    // the backwards state's aggregates as those of dk's run: the same orientation as dq's, so
+    // that one launch does both
+    if ((e = run_carry(Jobs{{mq, mk}, {0, 1}, 2}, g, a.V, a.K, a.bf16, st)) != hipSuccess) return e;
+    if (a.K == a.V) {
+        if ((e = run(Jobs{{mq, mk, mv}, {0, 1, 1}, 3}, g, a.V, a.K, a.bf16, false, st)) != hipSuccess) return e;
+    } else {  // other workgroup sizes
+        if ((e = run(Jobs{{mq, mk}, {0, 1}, 2}, g, a.V, a.K, a.bf16, false, st)) != hipSuccess) return e;
+        if ((e = run(Jobs{{mv}, {1}, 1}, g, a.K, a.V, a.bf16, false, st)) != hipSuccess) return e;
+    }
+    if (!shared || ng == 0) return hipSuccess;
+    const dim3 grid((unsigned)((ng / 4 + 255) / 256), 2);
+    if (a.bf16) launch(sum_heads<true>, grid, dim3(256), 0, st, heads, a.dq, a.dk, ng / 4, r, a.K / 4);
+    else launch(sum_heads<false>, grid, dim3(256), 0, st, heads, a.dq, a.dk, ng / 4, r, a.K / 4);
+    return hipGetLastError();
 }
 
 }  // namespace ssm
