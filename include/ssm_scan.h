@@ -522,7 +522,7 @@ int ssm_linattn_step(int B, int H, int G, int K, int V, ssm_dtype_t io,
  *   workspace    : at least ssm_group_norm_workspace_size(M, S, C, G, io) bytes
  * Statistics are fp32, from squared distances to a mean (no difference of large
  * sums). Supported: C >= 1 a multiple of G, C <= 65536; M >= 0 and S >= 1 (M = 0 does
- * nothing); M * S * C <= 2^40, M * S < 2^31. Every pointer must be 16-byte
+ * nothing); M * S * C <= 2^38, M * S < 2^31. Every pointer must be 16-byte
  * aligned. Errors as for ssm_scan_fwd.
  * ------------------------------------------------------------------------- */
 typedef enum { SSM_ACT_NONE = 0, SSM_ACT_SILU = 1, SSM_ACT_INT_RANGE_ = 0x7fffffff } ssm_act_t;

@@ -460,13 +460,13 @@ int group_norm_dims(const char* fn, int M, int S, int C, int G, int io, int act)
     if (C % G != 0) return fail(SSM_ERR_INVALID_ARG, fn, "G must divide C");
     if (C > 65536) return fail(SSM_ERR_UNSUPPORTED, fn, "C must be <= 65536");
     if (!product_ok({M, S}, 0x7fffffffLL)) return fail(SSM_ERR_UNSUPPORTED, fn, "M * S must be < 2^31");
-    if (!product_ok({M, S, C}, 1LL << 40)) return fail(SSM_ERR_INVALID_ARG, fn, "tensor sizes overflow");
+    if (!product_ok({M, S, C}, 1LL << 38)) return fail(SSM_ERR_INVALID_ARG, fn, "tensor sizes overflow");
     return SSM_OK;
 }
 
 bool group_norm_dims_ok(int M, int S, int C, int G, int io) {
     return M >= 0 && S >= 1 && C >= 1 && C <= 65536 && G >= 1 && C % G == 0 && (io == SSM_F32 || io == SSM_BF16) &&
-           product_ok({M, S}, 0x7fffffffLL) && product_ok({M, S, C}, 1LL << 40);
+           product_ok({M, S}, 0x7fffffffLL) && product_ok({M, S, C}, 1LL << 38);
 }
 
 }  // namespace
@@ -495,8 +495,8 @@ int ssm_linattn_fwd(int B, int L, int H, int G, int K, int V, ssm_dtype_t io,
     if (h0 && h0 == h_final) return fail(SSM_ERR_INVALID_ARG, fn, "h_final must not be h0");
     ssm::LinattnNorm nm;
     if ((s = linattn_norm_args(fn, norm, &nm)) != SSM_OK) return s;
-    if (nm.on && ((long long)H * V > 65536 || !product_ok({B, L}, 0x7fffffffLL)))
-        return fail(SSM_ERR_UNSUPPORTED, fn, "norm: H * V must be <= 65536 and B * L < 2^31");
+    if (nm.on && ((long long)H * V > 65536 || !product_ok({B, L}, 0x7fffffffLL) || !product_ok({B, L, H, V}, 1LL << 38)))
+        return fail(SSM_ERR_UNSUPPORTED, fn, "norm: H * V must be <= 65536, B * L < 2^31 and B * L * H * V <= 2^38");
     const size_t need = ssm::linattn_workspace_bytes(B, L, H, G, K, V, io == SSM_BF16);
     if (need > 0 && (workspace == nullptr || workspace_bytes < need))
         return fail(SSM_ERR_WORKSPACE, fn, "workspace missing or smaller than ssm_linattn_workspace_size()");
