@@ -368,7 +368,7 @@ __global__ void __launch_bounds__(kT) gn_stats(GroupNormArgs a, Tiles t, float2*
     int n = 0;
     if (p.on && p.s0 + p.row < p.s1) {
         load<BF16, V>(a.x, base + (size_t)(p.s0 + p.row) * a.C, k0);
-#pragma unroll 4
+#pragma unroll 8
         for (int i = p.s0 + p.row; i < p.s1; i += p.rl, ++n) {
             float x[V];
             load<BF16, V>(a.x, base + (size_t)i * a.C, x);
@@ -465,7 +465,7 @@ __global__ void __launch_bounds__(kT) gn_apply(GroupNormArgs a, Tiles t, const f
         rstd[v] = s.y;
     }
     const size_t base = (size_t)m * a.S * a.C + p.c0 + p.col;
-#pragma unroll 4
+#pragma unroll 8
     for (int i = p.s0 + p.row; i < p.s1; i += p.rl) {
         float x[V], z[V];
         load<BF16, V>(a.x, base + (size_t)i * a.C, x);
@@ -642,19 +642,20 @@ __global__ void __launch_bounds__(kT) gn_bwd_affine(GroupNormBwdArgs a, long lon
     }
 }
 
-// dweight and dbias from n parts [n][2][C]: 32 of the 2 C sums per workgroup, eight lanes each.
+// dweight and dbias from n parts [n][2][C]: 16 of the 2 C sums per workgroup (a 64-byte line
+// of a part), sixteen lanes each.
 __global__ void __launch_bounds__(kT) gn_sum_parts(const float* __restrict__ part, int n, int C, float* dweight,
                                                    float* dbias) {
-    __shared__ float s[8][33];
-    const int i = threadIdx.x & 31, r = threadIdx.x >> 5, e = blockIdx.x * 32 + i;
+    __shared__ float s[16][17];
+    const int i = threadIdx.x & 15, r = threadIdx.x >> 4, e = blockIdx.x * 16 + i;
     float v = 0.0f;
     if (e < 2 * C)
-#pragma unroll 4
-        for (int k = r; k < n; k += 8) v += part[(size_t)k * 2 * C + e];
+#pragma unroll 8
+        for (int k = r; k < n; k += 16) v += part[(size_t)k * 2 * C + e];
     s[r][i] = v;
     __syncthreads();
     if (r != 0 || e >= 2 * C) return;
-    for (int k = 1; k < 8; ++k) v += s[k][i];
+    for (int k = 1; k < 16; ++k) v += s[k][i];
     if (e < C) {
         if (dweight) dweight[e] = v;
     } else if (dbias) {
@@ -663,7 +664,9 @@ __global__ void __launch_bounds__(kT) gn_sum_parts(const float* __restrict__ par
 }
 
 // ------------------------------------------------------------------ choices
-constexpr int kParts = 512;  // parts of dw and db that gn_rows_bwd and gn_bwd_affine leave
+// Parts of dw and db that gn_rows_bwd and gn_bwd_affine leave, at most: 32768 x 1536 bf16 takes
+// 163 us with 512, 123 with 1024, 131 with 2048 (whose parts cost 4 us more to sum).
+constexpr int kParts = 1024;
 
 bool pieces(int C, int cg, int V) { return C % V == 0 && cg % V == 0; }
 
@@ -709,9 +712,10 @@ Tiles tiles_of(int M, int S, int C, int G, bool bf16, int* V) {
         }
         *V = 1;
     }
-    // enough workgroups to fill the card four times over, but at least eight rows a lane
+    // three workgroups a CU, but at least eight rows a lane (16 samples of 64 x 64 x 512 bf16:
+    // 53 us with 512 workgroups, 49 with 768, 53 with 1024, 67 with 2048)
     const int rl = std::max(1, kT / (t.width / *V));
-    const long want = std::max<long>(1, 1024 / std::max<long>(1, (long)M * t.tiles));
+    const long want = std::max<long>(1, 768 / std::max<long>(1, (long)M * t.tiles));
     const long most = std::max<long>(1, (S + 8L * rl - 1) / (8L * rl));
     t.splits = (int)std::min(std::min(want, most), 256L);
     t.rows = (S + t.splits - 1) / t.splits;
@@ -739,9 +743,9 @@ Path bwd_path(int S, int C, int G, bool bf16) {
     return S == 1 && rows_shape(cg, V, 4, &T, &R) ? kRows : kTiles;
 }
 
-// Samples' worth of rows per part below which a part per sample and range would not be small
-// against the data.
-bool parts_by_range(const Tiles& t) { return t.rows >= 64; }
+// Whether a part of dw and db per sample and range (8 bytes a channel) is small against the
+// range's rows (6 or more bytes a channel and row).
+bool parts_by_range(const Tiles& t) { return t.rows >= 8; }
 
 int row_parts(long long rows) { return (int)std::min<long long>(kParts, std::max<long long>(1, (rows + 7) / 8)); }
 
@@ -869,7 +873,7 @@ hipError_t launch_group_norm_bwd(const GroupNormBwdArgs& a, hipStream_t st) {
         else e = gate ? tiles_bwd<false, 1, true>(a, t, part, st) : tiles_bwd<false, 1, false>(a, t, part, st);
     }
     if (e != hipSuccess || !affine) return e;
-    launch(gn_sum_parts, dim3((unsigned)((2 * a.C + 31) / 32)), dim3(kT), 0, st, part, n, a.C, a.dweight, a.dbias);
+    launch(gn_sum_parts, dim3((unsigned)((2 * a.C + 15) / 16)), dim3(kT), 0, st, part, n, a.C, a.dweight, a.dbias);
     return hipGetLastError();
 }
 

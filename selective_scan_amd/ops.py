@@ -444,10 +444,40 @@ class _LinattnNorm(ctypes.Structure):
                 ("eps", ctypes.c_float)]
 
 
-def _device_of(t):
-    """Makes the tensors' device current for the launch where it is not."""
-    return (contextlib.nullcontext() if not t.is_cuda or torch.cuda.current_device() == t.device.index
-            else torch.cuda.device(t.device))
+def _fits(t, name, shape, dtype, device, required=True):
+    """``_check``, and the tensor's address (None without one), at the cost of a few attribute
+    reads: a decode step's calls take about as long as its kernels."""
+    if t is None and not required:
+        return None
+    if (type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and t.device == device
+            and t.is_contiguous()):
+        return t.data_ptr()
+    _check(t, name, shape, dtype, device, required)
+    return t.data_ptr()
+
+
+# the current stream's handle without a Stream object around it, where torch offers that
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+class _Launch:
+    """Makes the tensors' device current where it is not, and gives the stream's handle."""
+
+    def __init__(self, device, stream):
+        if device.type != "cuda":
+            raise ValueError(f"the tensors are on {device}, not on a GPU")
+        self.other = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+        self.handle = _raw_stream(device.index) if stream is None else stream.cuda_stream
+
+    def __enter__(self):
+        if self.other is not None:
+            self.other.__enter__()
+        return self.handle
+
+    def __exit__(self, *exc):
+        if self.other is not None:
+            self.other.__exit__(*exc)
 
 
 def _norm_arg(eps, weight, bias, z, HV, shape, io, dev):
@@ -456,10 +486,26 @@ def _norm_arg(eps, weight, bias, z, HV, shape, io, dev):
         if weight is not None or bias is not None or z is not None:
             raise ValueError("norm_weight, norm_bias and z need norm_eps")
         return None
-    _check(weight, "norm_weight", (HV,), torch.float32, dev, required=False)
-    _check(bias, "norm_bias", (HV,), torch.float32, dev, required=False)
-    _check(z, "z", shape, io, dev, required=False)
-    return ctypes.byref(_LinattnNorm(_ptr(weight), _ptr(bias), _ptr(z), float(eps)))
+    return ctypes.byref(_LinattnNorm(_fits(weight, "norm_weight", (HV,), torch.float32, dev, False),
+                                     _fits(bias, "norm_bias", (HV,), torch.float32, dev, False),
+                                     _fits(z, "z", shape, io, dev, False), float(eps)))
+
+
+def _space(need, workspace, dev):
+    """A workspace of ``need`` bytes: (tensor, address, size)."""
+    if workspace is None:
+        if need == 0:
+            return None, None, 0
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on {dev}")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _linattn_dims(q, v):
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError(f"q and v must be [B, L, heads, dim], got {tuple(q.shape)} and {tuple(v.shape)}")
+    return (*q.shape, v.shape[2], v.shape[3])
 
 
 def ssm_linattn_workspace_size(B, L, H, G, K, V, io=SSM_BF16):
@@ -474,34 +520,28 @@ def ssm_linattn_fwd(q, k, v, log_decay, *, scale=None, seqlens=None, h0=None, no
     int32, rows past a length are padding (o is 0 there); h0: [B, H, K, V] fp32. With
     ``norm_eps`` o goes through the per-head group norm (norm_weight, norm_bias: [H * V]
     fp32) and the gate silu(z). Returns (o [B, L, H, V], h_final [B, H, K, V])."""
-    B, L, G, K = q.shape
-    H, V = v.shape[2], v.shape[3]
+    B, L, G, K, H, V = _linattn_dims(q, v)
     dev, io = q.device, q.dtype
     code = _io_code(q)
-    _check(q, "q", (B, L, G, K), io, dev)
-    _check(k, "k", (B, L, G, K), io, dev)
-    _check(v, "v", (B, L, H, V), io, dev)
-    _check(log_decay, "log_decay", (H,), torch.float32, dev)
-    _check(seqlens, "seqlens", (B,), torch.int32, dev, required=False)
-    _check(h0, "h0", (B, H, K, V), torch.float32, dev, required=False)
-    norm = _norm_arg(norm_eps, norm_weight, norm_bias, z, H * V, (B, L, H, V), io, dev)
-    need = ssm_linattn_workspace_size(B, L, H, G, K, V, code)
+    qk, ov, st = (B, L, G, K), (B, L, H, V), (B, H, K, V)
+    p = (_fits(q, "q", qk, io, dev), _fits(k, "k", qk, io, dev), _fits(v, "v", ov, io, dev),
+         _fits(log_decay, "log_decay", (H,), torch.float32, dev))
+    lens = _fits(seqlens, "seqlens", (B,), torch.int32, dev, False)
+    h0p = _fits(h0, "h0", st, torch.float32, dev, False)
+    norm = _norm_arg(norm_eps, norm_weight, norm_bias, z, H * V, ov, io, dev)
+    need = lib().ssm_linattn_workspace_size(B, L, H, G, K, V, code)
     with _on(stream):
         if o is None:
-            o = torch.empty((B, L, H, V), dtype=io, device=dev)
+            o = torch.empty(ov, dtype=io, device=dev)
         if want_final_state and h_final is None:
-            h_final = torch.empty((B, H, K, V), dtype=torch.float32, device=dev)
-        if workspace is None and need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    _check(o, "o", (B, L, H, V), io, dev)
-    _check(h_final, "h_final", (B, H, K, V), torch.float32, dev, required=False)
-    wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    with _device_of(q):
-        st = lib().ssm_linattn_fwd(B, L, H, G, K, V, code, _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay),
-                                   K ** -0.5 if scale is None else float(scale), _ptr(seqlens), _ptr(h0), norm,
-                                   _ptr(o), _ptr(h_final), _ptr(workspace), wbytes, _stream(dev, stream))
-    if st != SSM_OK:
-        _raise("ssm_linattn_fwd", st)
+            h_final = torch.empty(st, dtype=torch.float32, device=dev)
+        workspace, wp, wbytes = _space(need, workspace, dev)
+    op, hp = _fits(o, "o", ov, io, dev), _fits(h_final, "h_final", st, torch.float32, dev, False)
+    with _Launch(dev, stream) as s:
+        rc = lib().ssm_linattn_fwd(B, L, H, G, K, V, code, *p, K ** -0.5 if scale is None else scale, lens, h0p, norm,
+                                   op, hp, wp, wbytes, s)
+    if rc != SSM_OK:
+        _raise("ssm_linattn_fwd", rc)
     return o, h_final
 
 
@@ -515,41 +555,31 @@ def ssm_linattn_bwd(q, k, v, log_decay, dout, *, scale=None, seqlens=None, h0=No
     h_final). Inputs as for ``ssm_linattn_fwd``; dout: [B, L, H, V]; dh_final: [B, H, K, V]
     fp32 or None. Returns a dict with dq, dk [B, L, G, K], dv [B, L, H, V] (0 at padding) and
     dh0 [B, H, K, V] fp32 (None unless want_dh0). ``out`` may supply any of these tensors."""
-    B, L, G, K = q.shape
-    H, V = v.shape[2], v.shape[3]
+    B, L, G, K, H, V = _linattn_dims(q, v)
     dev, io = q.device, q.dtype
     code = _io_code(q)
-    _check(q, "q", (B, L, G, K), io, dev)
-    _check(k, "k", (B, L, G, K), io, dev)
-    _check(v, "v", (B, L, H, V), io, dev)
-    _check(log_decay, "log_decay", (H,), torch.float32, dev)
-    _check(dout, "dout", (B, L, H, V), io, dev)
-    _check(seqlens, "seqlens", (B,), torch.int32, dev, required=False)
-    _check(h0, "h0", (B, H, K, V), torch.float32, dev, required=False)
-    _check(dh_final, "dh_final", (B, H, K, V), torch.float32, dev, required=False)
-    shapes = dict(dq=((B, L, G, K), io), dk=((B, L, G, K), io), dv=((B, L, H, V), io),
-                  dh0=((B, H, K, V), torch.float32))
-    g = dict(out or {})
-    need = ssm_linattn_bwd_workspace_size(B, L, H, G, K, V, code)
+    qk, ov, st = (B, L, G, K), (B, L, H, V), (B, H, K, V)
+    p = (_fits(q, "q", qk, io, dev), _fits(k, "k", qk, io, dev), _fits(v, "v", ov, io, dev),
+         _fits(log_decay, "log_decay", (H,), torch.float32, dev))
+    dp = _fits(dout, "dout", ov, io, dev)
+    lens = _fits(seqlens, "seqlens", (B,), torch.int32, dev, False)
+    h0p = _fits(h0, "h0", st, torch.float32, dev, False)
+    tp = _fits(dh_final, "dh_final", st, torch.float32, dev, False)
+    g, gp = dict(out or {}), []
+    need = lib().ssm_linattn_bwd_workspace_size(B, L, H, G, K, V, code)
     with _on(stream):
-        for n, (shp, dt) in shapes.items():
+        for n, shape, dt in (("dq", qk, io), ("dk", qk, io), ("dv", ov, io), ("dh0", st, torch.float32)):
             if n == "dh0" and not want_dh0:
                 g[n] = None
-                continue
-            if g.get(n) is None:
-                g[n] = torch.empty(shp, dtype=dt, device=dev)
-            else:
-                _check(g[n], n, shp, dt, dev)
-        if workspace is None and need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    with _device_of(q):
-        st = lib().ssm_linattn_bwd(B, L, H, G, K, V, code, _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay),
-                                   K ** -0.5 if scale is None else float(scale), _ptr(seqlens), _ptr(h0),
-                                   _ptr(dout), _ptr(dh_final), *(_ptr(g[n]) for n in ("dq", "dk", "dv", "dh0")),
-                                   _ptr(workspace), wbytes, _stream(dev, stream))
-    if st != SSM_OK:
-        _raise("ssm_linattn_bwd", st)
+            elif g.get(n) is None:
+                g[n] = torch.empty(shape, dtype=dt, device=dev)
+            gp.append(_fits(g[n], n, shape, dt, dev, n != "dh0"))
+        workspace, wp, wbytes = _space(need, workspace, dev)
+    with _Launch(dev, stream) as s:
+        rc = lib().ssm_linattn_bwd(B, L, H, G, K, V, code, *p, K ** -0.5 if scale is None else scale, lens, h0p, dp, tp,
+                                   *gp, wp, wbytes, s)
+    if rc != SSM_OK:
+        _raise("ssm_linattn_bwd", rc)
     return g
 
 
@@ -558,27 +588,25 @@ def ssm_linattn_step(state, q, k, v, log_decay, *, scale=None, norm_eps=None, no
     """One decode step of ``ssm_linattn_fwd``. state: [B, H, K, V] fp32 (updated in place);
     q, k: [B, G, K]; v, z: [B, H, V]; log_decay: [H]; norm arguments as there. Returns o
     [B, H, V]."""
+    if state.dim() != 4 or q.dim() != 3:
+        raise ValueError(f"state must be [B, H, K, V] and q [B, G, K], got {tuple(state.shape)} and {tuple(q.shape)}")
     B, H, K, V = state.shape
     G = q.shape[1]
     dev, io = q.device, q.dtype
     code = _io_code(q)
-    _check(state, "state", (B, H, K, V), torch.float32, dev)
-    _check(q, "q", (B, G, K), io, dev)
-    _check(k, "k", (B, G, K), io, dev)
-    _check(v, "v", (B, H, V), io, dev)
-    _check(log_decay, "log_decay", (H,), torch.float32, dev)
-    norm = _norm_arg(norm_eps, norm_weight, norm_bias, z, H * V, (B, H, V), io, dev)
+    qk, ov = (B, G, K), (B, H, V)
+    p = (_fits(state, "state", (B, H, K, V), torch.float32, dev), _fits(q, "q", qk, io, dev),
+         _fits(k, "k", qk, io, dev), _fits(v, "v", ov, io, dev),
+         _fits(log_decay, "log_decay", (H,), torch.float32, dev))
+    norm = _norm_arg(norm_eps, norm_weight, norm_bias, z, H * V, ov, io, dev)
     if o is None:
         with _on(stream):
-            o = torch.empty((B, H, V), dtype=io, device=dev)
-    else:
-        _check(o, "o", (B, H, V), io, dev)
-    with _device_of(q):
-        st = lib().ssm_linattn_step(B, H, G, K, V, code, _ptr(state), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay),
-                                    K ** -0.5 if scale is None else float(scale), norm, _ptr(o),
-                                    _stream(dev, stream))
-    if st != SSM_OK:
-        _raise("ssm_linattn_step", st)
+            o = torch.empty(ov, dtype=io, device=dev)
+    op = _fits(o, "o", ov, io, dev)
+    with _Launch(dev, stream) as s:
+        rc = lib().ssm_linattn_step(B, H, G, K, V, code, *p, K ** -0.5 if scale is None else scale, norm, op, s)
+    if rc != SSM_OK:
+        _raise("ssm_linattn_step", rc)
     return o
 
 
@@ -604,32 +632,25 @@ def ssm_group_norm_fwd(x, groups, weight=None, bias=None, z=None, *, eps=1e-5, a
     or fp32; weight, bias: [C] fp32; act: "none" | "silu"; y may be x. Returns (y, mean, rstd),
     mean and rstd [M, groups] fp32."""
     M, S, C = _norm_dims(x)
-    dev, io, G = x.device, x.dtype, int(groups)
-    code = _io_code(x)
-    _check(x, "x", x.shape, io, dev)
-    _check(weight, "weight", (C,), torch.float32, dev, required=False)
-    _check(bias, "bias", (C,), torch.float32, dev, required=False)
-    _check(z, "z", x.shape, io, dev, required=False)
-    need = ssm_group_norm_workspace_size(M, S, C, G, code)
+    dev, io, G, act = x.device, x.dtype, int(groups), SSM_ACT[act]
+    code, shape = _io_code(x), x.shape
+    p = (_fits(x, "x", shape, io, dev), _fits(weight, "weight", (C,), torch.float32, dev, False),
+         _fits(bias, "bias", (C,), torch.float32, dev, False), _fits(z, "z", shape, io, dev, False))
+    need = lib().ssm_group_norm_workspace_size(M, S, C, G, code)
     with _on(stream):
         if y is None:
-            y = torch.empty(x.shape, dtype=io, device=dev)
+            y = torch.empty(shape, dtype=io, device=dev)
         if mean is None:
             mean = torch.empty((M, G), dtype=torch.float32, device=dev)
         if rstd is None:
             rstd = torch.empty((M, G), dtype=torch.float32, device=dev)
-        if workspace is None and need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    _check(y, "y", x.shape, io, dev)
-    _check(mean, "mean", (M, G), torch.float32, dev)
-    _check(rstd, "rstd", (M, G), torch.float32, dev)
-    wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    with _device_of(x):
-        st = lib().ssm_group_norm_fwd(M, S, C, G, code, SSM_ACT[act], _ptr(x), _ptr(weight), _ptr(bias), _ptr(z),
-                                      float(eps), _ptr(y), _ptr(mean), _ptr(rstd), _ptr(workspace), wbytes,
-                                      _stream(dev, stream))
-    if st != SSM_OK:
-        _raise("ssm_group_norm_fwd", st)
+        workspace, wp, wbytes = _space(need, workspace, dev)
+    out = (_fits(y, "y", shape, io, dev), _fits(mean, "mean", (M, G), torch.float32, dev),
+           _fits(rstd, "rstd", (M, G), torch.float32, dev))
+    with _Launch(dev, stream) as s:
+        rc = lib().ssm_group_norm_fwd(M, S, C, G, code, act, *p, eps, *out, wp, wbytes, s)
+    if rc != SSM_OK:
+        _raise("ssm_group_norm_fwd", rc)
     return y, mean, rstd
 
 
@@ -643,38 +664,26 @@ def ssm_group_norm_bwd(x, groups, mean, rstd, dy, weight=None, bias=None, z=None
     rstd. Returns a dict with dx, dweight, dbias [C] fp32 (None unless want_affine), dz (None
     without z). ``out`` may supply any of these tensors."""
     M, S, C = _norm_dims(x)
-    dev, io, G = x.device, x.dtype, int(groups)
-    code = _io_code(x)
-    _check(x, "x", x.shape, io, dev)
-    _check(mean, "mean", (M, G), torch.float32, dev)
-    _check(rstd, "rstd", (M, G), torch.float32, dev)
-    _check(dy, "dy", x.shape, io, dev)
-    _check(weight, "weight", (C,), torch.float32, dev, required=False)
-    _check(bias, "bias", (C,), torch.float32, dev, required=False)
-    _check(z, "z", x.shape, io, dev, required=False)
-    shapes = dict(dx=(x.shape, io), dweight=((C,), torch.float32), dbias=((C,), torch.float32), dz=(x.shape, io))
-    wanted = dict(dweight=want_affine, dbias=want_affine, dz=z is not None)
-    g = dict(out or {})
-    need = ssm_group_norm_bwd_workspace_size(M, S, C, G, code)
+    dev, io, G, act = x.device, x.dtype, int(groups), SSM_ACT[act]
+    code, shape, f32 = _io_code(x), x.shape, torch.float32
+    p = (_fits(x, "x", shape, io, dev), _fits(weight, "weight", (C,), f32, dev, False),
+         _fits(bias, "bias", (C,), f32, dev, False), _fits(z, "z", shape, io, dev, False),
+         _fits(mean, "mean", (M, G), f32, dev), _fits(rstd, "rstd", (M, G), f32, dev), _fits(dy, "dy", shape, io, dev))
+    g, gp = dict(out or {}), []
+    need = lib().ssm_group_norm_bwd_workspace_size(M, S, C, G, code)
     with _on(stream):
-        for n, (shp, dt) in shapes.items():
-            if not wanted.get(n, True):
+        for n, sh, dt, wanted in (("dx", shape, io, True), ("dweight", (C,), f32, want_affine),
+                                  ("dbias", (C,), f32, want_affine), ("dz", shape, io, z is not None)):
+            if not wanted:
                 g[n] = None
-                continue
-            if g.get(n) is None:
-                g[n] = torch.empty(shp, dtype=dt, device=dev)
-            else:
-                _check(g[n], n, shp, dt, dev)
-        if workspace is None and need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    with _device_of(x):
-        st = lib().ssm_group_norm_bwd(M, S, C, G, code, SSM_ACT[act], _ptr(x), _ptr(weight), _ptr(bias), _ptr(z),
-                                      _ptr(mean), _ptr(rstd), _ptr(dy),
-                                      *(_ptr(g[n]) for n in ("dx", "dweight", "dbias", "dz")),
-                                      _ptr(workspace), wbytes, _stream(dev, stream))
-    if st != SSM_OK:
-        _raise("ssm_group_norm_bwd", st)
+            elif g.get(n) is None:
+                g[n] = torch.empty(sh, dtype=dt, device=dev)
+            gp.append(_fits(g[n], n, sh, dt, dev, wanted))
+        workspace, wp, wbytes = _space(need, workspace, dev)
+    with _Launch(dev, stream) as s:
+        rc = lib().ssm_group_norm_bwd(M, S, C, G, code, act, *p, *gp, wp, wbytes, s)
+    if rc != SSM_OK:
+        _raise("ssm_group_norm_bwd", rc)
     return g
 
 
