@@ -76,11 +76,13 @@ struct Mix {
     float out_scale;      // factor of every output
     float kv_scale;       // factor of x2 (x) x3
     const float* init;    // [B, H, KD, VD], transposed ([B, H, VD, KD]) if trans; or NULL
-    float* slots;         // [B, H, NS - 1, KD, VD] (or transposed): entering states
+    float* slots;         // [B, H, NS - 1, P, KD, VD] (or transposed): aggregates, then, in each
+                          // first piece, entering states
     int trans;
     void* out;            // io dtype, or fp32 if out_f32
     int out_f32;
     float* final_state;   // [B, H, KD, VD] or NULL
+    int exact;            // the state to fp32's last bits: x3 weighted enters it in three parts
 };
 
 // Up to three runs that one launch does side by side.
@@ -94,6 +96,8 @@ struct Geom {
     int NC;   // chunks per sequence
     int cps;  // chunks per super-chunk
     int NS;   // super-chunks per sequence
+    int P;    // pieces that a super-chunk's aggregate is computed in
+    int cpp;  // chunks per piece
 };
 
 // How many workgroups of mix_chunks fit a CU, by their LDS and registers.
@@ -109,7 +113,9 @@ int per_cu(int KD, int VD, bool bf16) {
 // B4 L8000 H24 K128 V64: 3.7 and 4.7); fp32 takes three times as long. A workgroup begins and
 // ends with its state (2 units). No launch is faster than its rows at 4 TB/s (13 MB a unit;
 // rows shared by heads are read once). More than one super-chunk adds the aggregates (half
-// a unit a chunk) and the carry. Measured optima are within 4% of what this picks: B1 L4096
+// a unit a chunk) and the carry; where these have few workgroups of many chunks, each
+// aggregate is computed in pieces that the carry joins (B4 L8000 H24 K128 V64: 70 us whole,
+// 49 in two). Measured optima are within 4% of what this picks: B1 L4096
 // H16 K = V = 128 takes 197 us with one, 55 with 8, 50 with 16, 55 with 32.
 Geom geom(int B, int L, int H, int G, int K, int V, bool bf16, bool bwd) {
     const long bh = (long)B * H;
@@ -122,25 +128,27 @@ Geom geom(int B, int L, int H, int G, int K, int V, bool bf16, bool bwd) {
         return std::max(t, rows * values);
     };
     const int dqk = 2 * (2 * r * V + K + r * K), dv = 2 * K + 2 * r * V;
-    Geom best{NC, NC, 1};
+    Geom best{NC, NC, 1, 1, NC};
     double least = 0.0;
     for (int want = 1; want <= NC && (want == 1 || bh * want <= 1536); ++want) {
         const int cps = (NC + want - 1) / want, NS = (NC + cps - 1) / cps;
         if (NS != want) continue;
         double t;
+        int P = 1;
         if (!bwd) t = scan(1, K, V, 2 * K + 2 * r * V, NS, cps);
         else if (K == V) t = scan(3, K, V, dqk + dv, NS, cps);
         else t = scan(2, V, K, dqk, NS, cps) + scan(1, K, V, dv, NS, cps);
         if (NS > 1) {
             const int dirs = bwd ? 2 : 1;
             const long wg = dirs * bh * (NS - 1);
-            t += std::max((double)((wg + 511) / 512) * (0.5 * cps * (bf16 ? 1.0 : 2.0) + 1.0),
+            P = (int)std::max<long>(1, std::min<long>({768 / wg, cps / 8, 4}));
+            t += std::max((double)((wg * P + 511) / 512) * (0.5 * cps / P * (bf16 ? 1.0 : 2.0) + 1.0),
                           dirs * rows * (K + r * V) * (NS - 1) / NS);
-            t += 2.4 + 0.27e-6 * dirs * bh * NS * K * V;
+            t += 2.4 + 0.14e-6 * dirs * bh * NS * K * V * (1 + P);
         }
         if (want == 1 || t < least) {
             least = t;
-            best = Geom{NC, cps, NS};
+            best = Geom{NC, cps, NS, P, (cps + P - 1) / P};
         }
     }
     return best;
@@ -205,6 +213,13 @@ template <> struct Types<true> {
             lo[p] = __builtin_bit_cast(uint32_t, __builtin_convertvector(d, bf16x2));
         }
         return Formed{__builtin_bit_cast(bf16x8, hi), __builtin_bit_cast(bf16x8, lo)};
+    }
+    // what hi + lo leave of v, to the last bit of fp32
+    static __device__ __forceinline__ Op rest(f32x8 v, const Formed& f) {
+        Op r;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) r[e] = (__bf16)((v[e] - (float)f.hi[e]) - (float)f.lo[e]);
+        return r;
     }
     static __device__ __forceinline__ f32x8 widen(Op a) {
         f32x8 v;
@@ -363,7 +378,7 @@ struct Lds {
                          M = W + 128 * 4, TOTAL = M + (AGG ? 0 : 3 * 2 * 2048);
 };
 
-template <int KD, int VD, bool BF16, bool REV, bool AGG>
+template <int KD, int VD, bool BF16, bool REV, bool AGG, bool EXACT>
 __device__ __forceinline__ void run_chunks(const Mix& a, const Geom& geo, lds_t* lds) {
     typedef Types<BF16> Ty;
     typedef typename Ty::Op Op;
@@ -373,8 +388,9 @@ __device__ __forceinline__ void run_chunks(const Mix& a, const Geom& geo, lds_t*
     typedef Rows<KD, NT, BF16> RowsK;
     typedef Rows<VD, NT, BF16> RowsV;
     int h, sc, b;
-    block_coords(a.H, AGG ? geo.NS - 1 : geo.NS, h, sc, b);
-    if (AGG && REV) ++sc;
+    block_coords(a.H, AGG ? (geo.NS - 1) * geo.P : geo.NS, h, sc, b);
+    const int piece = AGG ? sc % geo.P : 0;
+    if (AGG) sc = sc / geo.P + (REV ? 1 : 0);
     const int tid = threadIdx.x, lane = tid & 63, hf = lane >> 5, c = lane & 31;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const size_t bh = (size_t)b * a.H + h;
@@ -385,7 +401,8 @@ __device__ __forceinline__ void run_chunks(const Mix& a, const Geom& geo, lds_t*
     const int len = seq_len(a.seqlens, b, a.L);
 
     // chunks [c0, c1) of this super-chunk, of which [c0, ca) hold steps of the sequence
-    const int c0 = sc * geo.cps, c1 = min(geo.NC, c0 + geo.cps);
+    const int c0 = sc * geo.cps + piece * geo.cpp;
+    const int c1 = max(c0, min(min(geo.NC, (sc + 1) * geo.cps), AGG ? c0 + geo.cpp : geo.NC));
     const int ca = max(c0, min(c1, (len + kC - 1) / kC)), nch = ca - c0;
     auto chunk_at = [&](int u) { return REV ? ca - 1 - u : c0 + u; };
 
@@ -414,7 +431,7 @@ __device__ __forceinline__ void run_chunks(const Mix& a, const Geom& geo, lds_t*
             if (a.init)
                 each_state_element<KD>([&](int T, int r, int k, int j) { S[T][r] = src[a.trans ? j * KD + k : k * VD + j]; });
         } else {
-            const float* src = a.slots + (bh * (geo.NS - 1) + (REV ? sc : sc - 1)) * KD * VD;
+            const float* src = a.slots + (bh * (geo.NS - 1) + (REV ? sc : sc - 1)) * geo.P * KD * VD;
             if (a.trans) each_state_element<KD>([&](int T, int r, int k, int j) { S[T][r] = src[slot_at(j, k, KD)]; });
             else each_state_element<KD>([&](int T, int r, int k, int j) { S[T][r] = src[slot_at(k, j, VD)]; });
         }
@@ -626,11 +643,14 @@ __device__ __forceinline__ void run_chunks(const Mix& a, const Geom& geo, lds_t*
 #pragma unroll
                 for (int e = 0; e < 8; ++e) w[e] = w0[16 * s + e];
             };
+            Op rest{};
             auto weighted = [&](int s) {
                 f32x8 x = Ty::widen(v[s]);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) x[e] *= w[e];
-                return Ty::form(x);
+                const Formed f = Ty::form(x);
+                if constexpr (BF16 && EXACT) rest = Ty::rest(x, f);
+                return f;
             };
             fetch(0);
             const float m = n == kC ? full.next() : expf(la * (float)n);  // at most one chunk is shorter
@@ -647,10 +667,14 @@ __device__ __forceinline__ void run_chunks(const Mix& a, const Geom& geo, lds_t*
                 if (s < 3) fetch(s + 1);
 #pragma unroll
                 for (int T = 0; T < KT; ++T) S[T] = Ty::template part<0>(kn[T], wv, S[T]);
+                const Op third = rest;
                 const Formed next = s < 3 ? weighted(s + 1) : wv;
                 if constexpr (Ty::PARTS == 2)
 #pragma unroll
                     for (int T = 0; T < KT; ++T) S[T] = Ty::template part<1>(kn[T], wv, S[T]);
+                if constexpr (BF16 && EXACT)
+#pragma unroll
+                    for (int T = 0; T < KT; ++T) S[T] = Ty::mma(kn[T], third, S[T]);
                 wv = next;
                 __builtin_amdgcn_sched_barrier(0);
             }
@@ -659,7 +683,7 @@ __device__ __forceinline__ void run_chunks(const Mix& a, const Geom& geo, lds_t*
     }
 
     if constexpr (AGG) {
-        float* dst = a.slots + (bh * (geo.NS - 1) + (REV ? sc - 1 : sc)) * KD * VD;
+        float* dst = a.slots + ((bh * (geo.NS - 1) + (REV ? sc - 1 : sc)) * geo.P + piece) * KD * VD;
         if (a.trans) each_state_element<KD>([&](int T, int r, int k, int j) { dst[slot_at(j, k, KD)] = S[T][r]; });
         else each_state_element<KD>([&](int T, int r, int k, int j) { dst[slot_at(k, j, VD)] = S[T][r]; });
     } else if (a.final_state && (REV ? sc == 0 : sc == geo.NS - 1)) {
@@ -673,8 +697,14 @@ __global__ void __launch_bounds__(2 * VD) __attribute__((amdgpu_waves_per_eu(BF1
 mix_chunks(Jobs jobs, Geom geo) {
     __shared__ __attribute__((aligned(16))) char lds[Lds<KD, VD, BF16, AGG>::TOTAL];
     const int j = blockIdx.y;
-    if (jobs.rev[j]) run_chunks<KD, VD, BF16, true, AGG>(jobs.m[j], geo, (lds_t*)lds);
-    else run_chunks<KD, VD, BF16, false, AGG>(jobs.m[j], geo, (lds_t*)lds);
+    const Mix& m = jobs.m[j];
+    if (BF16 && m.exact) {
+        if (jobs.rev[j]) run_chunks<KD, VD, BF16, true, AGG, true>(m, geo, (lds_t*)lds);
+        else run_chunks<KD, VD, BF16, false, AGG, true>(m, geo, (lds_t*)lds);
+    } else {
+        if (jobs.rev[j]) run_chunks<KD, VD, BF16, true, AGG, false>(m, geo, (lds_t*)lds);
+        else run_chunks<KD, VD, BF16, false, AGG, false>(m, geo, (lds_t*)lds);
+    }
 }
 
 // Aggregates -> entering states, in the run's direction: what super-chunk s adds, plus
@@ -686,33 +716,35 @@ __global__ void __launch_bounds__(256) mix_carry(Jobs jobs, Geom geo, int n4, in
     const int e = blockIdx.x * 256 + threadIdx.x;
     const int bh = blockIdx.y, b = bh / a.H, h = bh % a.H;
     if (e >= n4) return;
-    const int len = seq_len(a.seqlens, b, a.L), K = geo.NS - 1;
+    // piece i in the run's direction: of slot i / P, the same place from the end if backwards
+    const int len = seq_len(a.seqlens, b, a.L), n = (geo.NS - 1) * geo.P;
     const float la = log_decay_of(a.log_decay, h);
-    float4* slot = reinterpret_cast<float4*>(a.slots) + (size_t)bh * K * n4 + e;
+    float4* slot = reinterpret_cast<float4*>(a.slots) + (size_t)bh * n * n4 + e;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     if (a.init) {  // elements 4 e .. 4 e + 3 of a slot: rows i .. i + 3 of column j of [I, J]
         const int j = (e >> 1) % J, i = ((e >> 1) / J) * 8 + 4 * (e & 1);
         const float* p = a.init + ((size_t)bh * (n4 / J * 4) + i) * J + j;
         v = make_float4(p[0], p[J], p[2 * J], p[3 * J]);
     }
-    for (int k0 = 0; k0 < K; k0 += 8) {
+    for (int i0 = 0; i0 < n; i0 += 8) {
         float4 sl[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const int k = min(k0 + j, K - 1);
-            sl[j] = slot[(size_t)(rev ? K - 1 - k : k) * n4];
+            const int i = min(i0 + j, n - 1);
+            sl[j] = slot[(size_t)(rev ? n - 1 - i : i) * n4];
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const int k = k0 + j;
-            if (k >= K) break;
-            const int sc = rev ? K - k : k, t0 = sc * geo.cps * kC;
-            const Decay decay(la * (float)max(0, min(len - t0, geo.cps * kC)));
+            const int i = i0 + j;
+            if (i >= n) break;
+            const int at = rev ? n - 1 - i : i, sc = at / geo.P + (rev ? 1 : 0), piece = at % geo.P;
+            const int c0 = sc * geo.cps + piece * geo.cpp, c1 = min(min(geo.NC, (sc + 1) * geo.cps), c0 + geo.cpp);
+            const Decay decay(la * (float)max(0, min(len - c0 * kC, (c1 - c0) * kC)));
             v.x = decay(v.x) + sl[j].x;
             v.y = decay(v.y) + sl[j].y;
             v.z = decay(v.z) + sl[j].z;
             v.w = decay(v.w) + sl[j].w;
-            slot[(size_t)(rev ? K - 1 - k : k) * n4] = v;
+            if (piece == (rev ? 0 : geo.P - 1)) slot[(size_t)(at - piece) * n4] = v;
         }
     }
 }
@@ -739,7 +771,7 @@ sum_heads(const float* __restrict__ p, void* out0, void* out1, size_t n4, int r,
 template <int KD, int VD>
 hipError_t run_t(const Jobs& jobs, const Geom& g, bool bf16, bool agg, hipStream_t st) {
     const Mix& m = jobs.m[0];
-    const dim3 grid((unsigned)m.B * m.H * (agg ? g.NS - 1 : g.NS), (unsigned)jobs.n);
+    const dim3 grid((unsigned)m.B * m.H * (agg ? (g.NS - 1) * g.P : g.NS), (unsigned)jobs.n);
     if (bf16 && agg) launch((mix_chunks<KD, VD, true, true>), grid, dim3(2 * VD), 0, st, jobs, g);
     else if (bf16) launch((mix_chunks<KD, VD, true, false>), grid, dim3(2 * VD), 0, st, jobs, g);
     else if (agg) launch((mix_chunks<KD, VD, false, true>), grid, dim3(2 * VD), 0, st, jobs, g);
@@ -765,7 +797,7 @@ hipError_t run_carry(const Jobs& jobs, const Geom& g, int KD, int VD, bool bf16,
     return hipGetLastError();
 }
 
-size_t slot_bytes(int B, int H, int K, int V, const Geom& g) { return (size_t)B * H * (g.NS - 1) * K * V * 4; }
+size_t slot_bytes(int B, int H, int K, int V, const Geom& g) { return (size_t)B * H * (g.NS - 1) * g.P * K * V * 4; }
 
 }  // namespace
 
@@ -784,7 +816,7 @@ size_t linattn_bwd_workspace_bytes(int B, int L, int H, int G, int K, int V, boo
 hipError_t launch_linattn_fwd(const LinattnArgs& a, hipStream_t st) {
     const Geom g = geom(a.B, a.L, a.H, a.G, a.K, a.V, a.bf16, false);
     const Mix m{a.B, a.L, a.H, a.H / a.G, a.q, a.k, a.v, 1, 1, 0, a.log_decay, a.seqlens,
-                a.scale, 1.0f, a.h0, static_cast<float*>(a.ws), 0, a.o, 0, a.h_final};
+                a.scale, 1.0f, a.h0, static_cast<float*>(a.ws), 0, a.o, 0, a.h_final, a.h_final != nullptr};
     const Jobs jobs{{m}, {0}, 1};
     const hipError_t e = run_carry(jobs, g, a.K, a.V, a.bf16, st);
     return e != hipSuccess ? e : run(jobs, g, a.K, a.V, a.bf16, false, st);
@@ -799,16 +831,17 @@ hipError_t launch_linattn_bwd(const LinattnBwdArgs& a, hipStream_t st) {
     float* heads = slots + 2 * ns;
     // dq: the state v (x) k of the forward run, held transposed (as [K, V], like h0)
     const Mix mq{a.B, a.L, a.H, r, a.dout, a.v, a.k, 0, 0, 1, a.log_decay, a.seqlens,
-                 a.scale, 1.0f, a.h0, slots, 1, shared ? heads : a.dq, shared, nullptr};
+                 a.scale, 1.0f, a.h0, slots, 1, shared ? heads : a.dq, shared, nullptr, 0};
     // dv, and dk from the same entering states, read transposed
     const Mix mv{a.B, a.L, a.H, r, a.k, a.q, a.dout, 1, 1, 0, a.log_decay, a.seqlens,
-                 1.0f, a.scale, a.dh_final, slots + ns, 0, a.dv, 0, a.dh0};
-    const Mix mk{a.B, a.L, a.H, r, a.v, a.dout, a.q, 0, 0, 1, a.log_decay, a.seqlens,
-                 1.0f, a.scale, a.dh_final, slots + ns, 1, shared ? heads + ng * r : a.dk, shared, nullptr};
+                 1.0f, a.scale, a.dh_final, slots + ns, 0, a.dv, 0, a.dh0, a.dh0 != nullptr};
+    Mix mk{a.B, a.L, a.H, r, a.v, a.dout, a.q, 0, 0, 1, a.log_decay, a.seqlens,
+           1.0f, a.scale, a.dh_final, slots + ns, 1, shared ? heads + ng * r : a.dk, shared, nullptr, a.dh0 != nullptr};
     hipError_t e;
     // the backwards state's aggregates as those of dk's run: the same orientation as dq's, so
     // that one launch does both
     if ((e = run_carry(Jobs{{mq, mk}, {0, 1}, 2}, g, a.V, a.K, a.bf16, st)) != hipSuccess) return e;
+    mk.exact = 0;  // its own state is no output
     if (a.K == a.V) {
         if ((e = run(Jobs{{mq, mk, mv}, {0, 1, 1}, 3}, g, a.V, a.K, a.bf16, false, st)) != hipSuccess) return e;
     } else {  // other workgroup sizes

@@ -169,15 +169,36 @@ def test_length_zero():
     assert torch.equal(g["dh0"], t["dh_final"])
 
 
-def test_optional_outputs():
-    t = dev(ref.inputs(1, 150, 2, 2, 64, 64, BF16, seed=3))
-    o, hf = ssa.ssm_linattn_fwd(t["q"], t["k"], t["v"], t["log_decay"], h0=t["h0"])
-    o2, none = ssa.ssm_linattn_fwd(t["q"], t["k"], t["v"], t["log_decay"], h0=t["h0"], want_final_state=False)
-    assert none is None and torch.equal(o, o2)
-    g = ssa.ssm_linattn_bwd(t["q"], t["k"], t["v"], t["log_decay"], t["dout"], h0=t["h0"], dh_final=t["dh_final"])
-    g2 = ssa.ssm_linattn_bwd(t["q"], t["k"], t["v"], t["log_decay"], t["dout"], h0=t["h0"], dh_final=t["dh_final"],
-                             want_dh0=False)
-    assert g2["dh0"] is None and all(torch.equal(g[n], g2[n]) for n in ("dq", "dk", "dv"))
+@pytest.mark.parametrize("L", [150, 3000])
+def test_optional_outputs(L):
+    """Without the final state, or dh0, the others stay what they are (the state is then formed with
+    fewer parts: the same bounds, not the same bits)."""
+    B, H, G, K, V = 1, 2, 2, 64, 64
+    t = ref.inputs(B, L, H, G, K, V, BF16, seed=3)
+    d = dev(t)
+    o, none = ssa.ssm_linattn_fwd(d["q"], d["k"], d["v"], d["log_decay"], h0=d["h0"], want_final_state=False)
+    args = (t["q"], t["k"], t["v"], t["log_decay"], K ** -0.5)
+    c = ref.term_error(L, K, V, True)
+    assert none is None
+    ref.close(o, ref.fwd(*args, h0=t["h0"])[0], ref.magnitude(ref.fwd, *args, h0=t["h0"])[0], c, "o")
+    g = check_bwd(t, K, V, what="without dh0", want_dh0=False)
+    assert g["dh0"] is None
+
+
+def test_the_state_is_good_to_single_precision():
+    """The state's products enter it in three bf16 parts (24 bits): the final state and dh0 are within a
+    few fp32 roundings of the 64-bit ones, in the 2-norm."""
+    B, L, H, G, K, V = 2, 2000, 4, 2, 128, 64
+    t = ref.inputs(B, L, H, G, K, V, BF16, seed=51)
+    d = dev(t)
+    _, hf = ssa.ssm_linattn_fwd(d["q"], d["k"], d["v"], d["log_decay"], h0=d["h0"])
+    g = ssa.ssm_linattn_bwd(d["q"], d["k"], d["v"], d["log_decay"], d["dout"], h0=d["h0"], dh_final=d["dh_final"])
+    args = (t["q"], t["k"], t["v"], t["log_decay"], K ** -0.5)
+    for got, want in ((hf, ref.fwd(*args, h0=t["h0"])[1]),
+                      (g["dh0"], ref.bwd(*args, t["dout"], h0=t["h0"], T=t["dh_final"])["dh0"])):
+        # each of the sum's roundings (at most L / 16 + a few, 2^-24 of a partial sum no larger than the
+        # sum of absolute values) adds independently: 16 of them in the norm is beyond what they reach
+        assert float((got.double().cpu() - want).norm() / want.norm()) < 16 * 2.0 ** -24
 
 
 def test_gradient_against_differences_of_the_forward():
