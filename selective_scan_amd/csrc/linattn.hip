@@ -100,6 +100,11 @@ struct Geom {
     int cpp;  // chunks per piece
 };
 
+// Whether the heads of a group share a workgroup in dq and dk, whose sum over the heads then
+// never leaves the registers (they hold the states of three heads of V = 64): B4 L2047 H24 of 8
+// K128 V64 takes 200 us with fp32 planes per head and their sum, 159 so.
+bool shared_heads(int r, int V, bool bf16) { return bf16 && V == 64 && (r == 2 || r == 3); }
+
 // How many workgroups of mix_chunks fit a CU, by their LDS and registers.
 int per_cu(int KD, int VD, bool bf16) {
     const int es = bf16 ? 2 : 4, lds = kC * (3 * KD + VD) * es + 128 * 4 + 3 * 2 * 2048;
@@ -136,6 +141,8 @@ Geom geom(int B, int L, int H, int G, int K, int V, bool bf16, bool bwd) {
         double t;
         int P = 1;
         if (!bwd) t = scan(1, K, V, 2 * K + 2 * r * V, NS, cps);
+        else if (shared_heads(r, V, bf16))  // one a CU, 0.8 units a head and chunk
+            t = (double)((2 * bh / r * NS + 255) / 256) * (0.8 * r * cps + 2.0) + scan(1, K, V, dv, NS, cps);
         else if (K == V) t = scan(3, K, V, dqk + dv, NS, cps);
         else t = scan(2, V, K, dqk, NS, cps) + scan(1, K, V, dv, NS, cps);
         if (NS > 1) {
@@ -357,8 +364,12 @@ __device__ __forceinline__ int slot_at(int i, int j, int J) { return ((i >> 3) *
 // direction on every chunk of a slowly decaying state; so each chunk takes the float that
 // brings the product so far nearest to the exact one.
 struct ChunkDecay {
-    double lam, inv, err = 0.0;
-    __device__ __forceinline__ explicit ChunkDecay(float a) : lam(exp((double)a)), inv(lam > 0.5 ? 1.0 / lam : 0.0) {}
+    double lam, inv, err;
+    __device__ __forceinline__ void set(float a) {
+        lam = exp((double)a);
+        inv = lam > 0.5 ? 1.0 / lam : 0.0;
+        err = 0.0;
+    }
     __device__ __forceinline__ float next() {
         const float m = (float)(lam - lam * err);
         err = inv != 0.0 ? (1.0 + err) * ((double)m * inv) - 1.0 : 0.0;
@@ -369,26 +380,30 @@ struct ChunkDecay {
 // The tiles of a workgroup in LDS. Two buffers where they are filled while the other is
 // read: of x2, and, if full, of x1 and x3 as well; where two workgroups would not fit a CU
 // with that, x1 and x3 have one, filled once the chunk's scores and x1 S are done.
-template <int KD, int VD, bool BF16, bool AGG>
+template <int KD, int VD, bool BF16, bool AGG, int R>
 struct Lds {
     static constexpr int BK = Tile<KD, BF16>::BYTES, BV = Tile<VD, BF16>::BYTES;
-    static constexpr bool FULL = AGG || (BF16 && KD == 64 && VD == 128);
+    static constexpr bool FULL = AGG || (BF16 && KD == 64 && VD == 128 && R == 1);
     static constexpr int N2 = 2, N13 = FULL ? 2 : 1;
     static constexpr int X2 = 0, X3 = X2 + N2 * BK, X1 = X3 + N13 * BV, W = X1 + (AGG ? 0 : N13 * BK),
-                         M = W + 128 * 4, TOTAL = M + (AGG ? 0 : 3 * 2 * 2048);
+                         M = W + R * 128 * 4, D = M + (AGG ? 0 : 3 * 2 * 2048),
+                         TOTAL = D + (R > 1 ? R * 2 * 4096 : 0);
 };
 
-template <int KD, int VD, bool BF16, bool REV, bool AGG, bool EXACT>
+// R > 1: the R heads of a group whose x3 they share, one after the other on every chunk, each
+// with a state of its own; the output is their sum.
+template <int KD, int VD, bool BF16, bool REV, bool AGG, bool EXACT, int R>
 __device__ __forceinline__ void run_chunks(const Mix& a, const Geom& geo, lds_t* lds) {
     typedef Types<BF16> Ty;
     typedef typename Ty::Op Op;
     typedef typename Ty::Formed Formed;
-    typedef Lds<KD, VD, BF16, AGG> Ld;
+    typedef Lds<KD, VD, BF16, AGG, R> Ld;
     constexpr int NT = 2 * VD, KS = KD / 16, KT = KD / 32;
     typedef Rows<KD, NT, BF16> RowsK;
     typedef Rows<VD, NT, BF16> RowsV;
     int h, sc, b;
-    block_coords(a.H, AGG ? (geo.NS - 1) * geo.P : geo.NS, h, sc, b);
+    block_coords(a.H / R, AGG ? (geo.NS - 1) * geo.P : geo.NS, h, sc, b);
+    h *= R;
     const int piece = AGG ? sc % geo.P : 0;
     if (AGG) sc = sc / geo.P + (REV ? 1 : 0);
     const int tid = threadIdx.x, lane = tid & 63, hf = lane >> 5, c = lane & 31;
@@ -406,41 +421,52 @@ __device__ __forceinline__ void run_chunks(const Mix& a, const Geom& geo, lds_t*
     const int ca = max(c0, min(c1, (len + kC - 1) / kC)), nch = ca - c0;
     auto chunk_at = [&](int u) { return REV ? ca - 1 - u : c0 + u; };
 
-    // chunk u's rows into its buffers
+    // step u: head u % R of the run's chunk u / R. Its rows into its buffers (x3's with the
+    // first head).
     auto load = [&](int u) {
-        const int t0 = chunk_at(u) * kC, n = min(kC, len - t0), b2 = u % Ld::N2, b13 = u % Ld::N13;
-        RowsK::load(a.x2, b, a.L, n2, h2, t0, n, lds + Ld::X2 + b2 * Ld::BK);
-        if constexpr (!AGG) RowsK::load(a.x1, b, a.L, n1, h1, t0, n, lds + Ld::X1 + b13 * Ld::BK);
-        RowsV::load(a.x3, b, a.L, n3, h3, t0, n, lds + Ld::X3 + b13 * Ld::BV);
+        const int t0 = chunk_at(u / R) * kC, n = min(kC, len - t0), b2 = u % Ld::N2, b13 = u % Ld::N13, hh = u % R;
+        RowsK::load(a.x2, b, a.L, n2, h2 + hh, t0, n, lds + Ld::X2 + b2 * Ld::BK);
+        if constexpr (!AGG) RowsK::load(a.x1, b, a.L, n1, h1 + hh, t0, n, lds + Ld::X1 + b13 * Ld::BK);
+        if (hh == 0) RowsV::load(a.x3, b, a.L, n3, h3, t0, n, lds + Ld::X3 + b13 * Ld::BV);
     };
     if (nch > 0) load(0);
 
-    const float la = log_decay_of(a.log_decay, h), la2 = la * kLog2e;
-    auto power = [&](int n) { return exp2_fast((float)n * la2); };
+    float la[R];
+#pragma unroll
+    for (int hh = 0; hh < R; ++hh) la[hh] = log_decay_of(a.log_decay, h + hh);
+    auto power = [&](int hh, int n) { return exp2_fast((float)n * (la[hh] * kLog2e)); };
 
-    // the state entering the super-chunk
-    f32x16 S[KT];
+    // the states entering the super-chunk
+    f32x16 S[R][KT];
 #pragma unroll
-    for (int T = 0; T < KT; ++T)
+    for (int hh = 0; hh < R; ++hh) {
 #pragma unroll
-        for (int r = 0; r < 16; ++r) S[T][r] = 0.0f;
-    if constexpr (!AGG) {
-        const bool first = REV ? sc == geo.NS - 1 : sc == 0;
-        if (first) {
-            const float* src = a.init + bh * KD * VD;
-            if (a.init)
-                each_state_element<KD>([&](int T, int r, int k, int j) { S[T][r] = src[a.trans ? j * KD + k : k * VD + j]; });
-        } else {
-            const float* src = a.slots + (bh * (geo.NS - 1) + (REV ? sc : sc - 1)) * geo.P * KD * VD;
-            if (a.trans) each_state_element<KD>([&](int T, int r, int k, int j) { S[T][r] = src[slot_at(j, k, KD)]; });
-            else each_state_element<KD>([&](int T, int r, int k, int j) { S[T][r] = src[slot_at(k, j, VD)]; });
+        for (int T = 0; T < KT; ++T)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) S[hh][T][r] = 0.0f;
+        if constexpr (!AGG) {
+            const bool first = REV ? sc == geo.NS - 1 : sc == 0;
+            if (first) {
+                const float* src = a.init + (bh + hh) * KD * VD;
+                if (a.init)
+                    each_state_element<KD>(
+                        [&](int T, int r, int k, int j) { S[hh][T][r] = src[a.trans ? j * KD + k : k * VD + j]; });
+            } else {
+                const float* src = a.slots + ((bh + hh) * (geo.NS - 1) + (REV ? sc : sc - 1)) * geo.P * KD * VD;
+                if (a.trans)
+                    each_state_element<KD>([&](int T, int r, int k, int j) { S[hh][T][r] = src[slot_at(j, k, KD)]; });
+                else each_state_element<KD>([&](int T, int r, int k, int j) { S[hh][T][r] = src[slot_at(k, j, VD)]; });
+            }
         }
     }
 
     // W[x]: weight of row j of x3 in the state's update; forwards lam^(n-1-j) = W[j + 64 - n],
     // backwards lam^(j+1) = W[j]; times kv_scale
     lds_f32* wt = reinterpret_cast<lds_f32*>(lds + Ld::W);
-    for (int x = tid; x < 128; x += NT) wt[x] = x < kC ? power(REV ? x + 1 : kC - 1 - x) * a.kv_scale : 0.0f;
+#pragma unroll
+    for (int hh = 0; hh < R; ++hh)
+        for (int x = tid; x < 128; x += NT)
+            wt[hh * 128 + x] = x < kC ? power(hh, REV ? x + 1 : kC - 1 - x) * a.kv_scale : 0.0f;
     // The scores' tiles that count are (J, I) = (0, 0) and (1, 1) on the diagonal and one off
     // it, (0, 1) forwards, (1, 0) backwards. Each is computed by one wave, decayed (this
     // lane's 16 factors: row i = 32 I + c, column j = 32 J + 16 (r / 8) + 8 hf + r % 8),
@@ -449,15 +475,29 @@ __device__ __forceinline__ void run_chunks(const Mix& a, const Geom& geo, lds_t*
     // which the first passes on.
     const bool off_diag = NT == 256 && wave == 2;
     const int Ja = off_diag ? (REV ? 1 : 0) : wave & 1 & (wave >> 1 ^ 1), Ia = off_diag ? (REV ? 0 : 1) : Ja;
-    f32x16 d_a, d_b;
-    if constexpr (!AGG) {
+    auto factor = [&](int hh, bool off, int r) {
+        const int j = 16 * (r >> 3) + 8 * hf + (r & 7), lag = REV ? j - c : c - j;
+        return (off ? power(hh, 32 + lag) : lag >= 0 ? power(hh, lag) : 0.0f) * (a.kv_scale * a.out_scale);
+    };
+    f32x16 d_a, d_b;  // in registers for one head, in LDS for more ([head][on, off][4][lane])
+    lds_f32x4* tab = reinterpret_cast<lds_f32x4*>(lds + Ld::D);
+    if constexpr (!AGG && R == 1) {
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
-            const int j = 16 * (r >> 3) + 8 * hf + (r & 7), lag = REV ? j - c : c - j;
-            const float f = a.kv_scale * a.out_scale, on = lag >= 0 ? power(lag) * f : 0.0f, off = power(32 + lag) * f;
-            d_a[r] = off_diag ? off : on;
-            d_b[r] = off;
+            d_a[r] = factor(0, off_diag, r);
+            d_b[r] = factor(0, true, r);
         }
+    } else if constexpr (!AGG) {
+        if (wave < 2)
+#pragma unroll
+            for (int hh = 0; hh < R; ++hh)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    f32x4 x;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[e] = factor(hh, wave, 4 * q + e);
+                    tab[((hh * 2 + wave) * 4 + q) * 64 + lane] = x;
+                }
     }
 
     // outputs of this wave's 32 columns of row block I (rows t0 + 32 I + c); rows past the
@@ -465,11 +505,12 @@ __device__ __forceinline__ void run_chunks(const Mix& a, const Geom& geo, lds_t*
     // A lane holds 32 (or, fp32, 64) bytes of one row in pieces of 16; pieces are exchanged
     // between lanes 16 apart so that a store covers 64 consecutive bytes of 16 rows and not
     // 32 of 32.
-    const uint32_t orow = (uint32_t)a.H * VD * (BF16 && !a.out_f32 ? 2 : 4);
+    const int ho = h / R, no = a.H / R;  // the output's head of so many
+    const uint32_t orow = (uint32_t)no * VD * (BF16 && !a.out_f32 ? 2 : 4);
     auto put = [&](int t0, int I, const f32x16& acc) {
         const int es = BF16 && !a.out_f32 ? 2 : 4;
         const int nr = min(kC, a.L - t0);
-        const auto out = make_rsrc(static_cast<char*>(a.out) + (((size_t)b * a.L + t0) * a.H + h) * (size_t)(VD * es),
+        const auto out = make_rsrc(static_cast<char*>(a.out) + (((size_t)b * a.L + t0) * no + ho) * (size_t)(VD * es),
                                    (uint32_t)(nr - 1) * orow + VD * es);
         // pieces x and y of this lane's row; col: where the piece this lane then has begins
         auto pair = [&](u32x4 x, u32x4 y, uint32_t col) {
@@ -507,11 +548,11 @@ __device__ __forceinline__ void run_chunks(const Mix& a, const Geom& geo, lds_t*
                 if (ch * kC < a.L) put(ch * kC, I, zero);
     }
 
-    // chunk u's tiles complete and visible to every wave. A chunk's stores of outputs are
+    // step u's tiles complete and visible to every wave. A chunk's stores of outputs are
     // issued after the loads of the next one's rows and need not be waited for (vmcnt
     // counts both in the order of issue; every wave issues 4 of bf16, 8 of fp32).
     auto stage = [&](int u, bool stores) {
-        const int n = min(kC, len - chunk_at(u) * kC);
+        const int n = min(kC, len - chunk_at(u / R) * kC);
         lds_t* x1 = lds + Ld::X1 + u % Ld::N13 * Ld::BK;
         lds_t* x2 = lds + Ld::X2 + u % Ld::N2 * Ld::BK;
         lds_t* x3 = lds + Ld::X3 + u % Ld::N13 * Ld::BV;
@@ -522,20 +563,27 @@ __device__ __forceinline__ void run_chunks(const Mix& a, const Geom& geo, lds_t*
             __syncthreads();
             if constexpr (!AGG) RowsK::clear(x1, n);
             RowsK::clear(x2, n);
-            RowsV::clear(x3, n);
+            if (u % R == 0) RowsV::clear(x3, n);
         }
         __syncthreads();
     };
 
-    ChunkDecay full(la * (float)kC);
+    ChunkDecay full[R];
+#pragma unroll
+    for (int hh = 0; hh < R; ++hh) full[hh].set(la[hh] * (float)kC);
     if (nch > 0) stage(0, false);
-    for (int u = 0; u < nch; ++u) {
-        const int t0 = chunk_at(u) * kC, n = min(kC, len - t0);
+    for (int cu = 0; cu < nch; ++cu) {
+        const int t0 = chunk_at(cu) * kC, n = min(kC, len - t0);
+        Op v[4];
+        f32x16 out[2];
+#pragma unroll
+        for (int hh = 0; hh < R; ++hh) {
+        const int u = cu * R + hh;
+        const bool more = u + 1 < nch * R;
         const lds_t* x1 = lds + Ld::X1 + u % Ld::N13 * Ld::BK;
         const lds_t* x2 = lds + Ld::X2 + u % Ld::N2 * Ld::BK;
         const lds_t* x3 = lds + Ld::X3 + u % Ld::N13 * Ld::BV;
-        if (Ld::FULL && u + 1 < nch) load(u + 1);
-        Op v[4];
+        if (Ld::FULL && more) load(u + 1);
         auto read_v = [&]() {
 #pragma unroll
             for (int s = 0; s < 4; ++s) v[s] = Ty::template col8<VD>(x3, 16 * s, 32 * wave);
@@ -563,7 +611,7 @@ __device__ __forceinline__ void run_chunks(const Mix& a, const Geom& geo, lds_t*
             for (int ks = 0; ks < KS; ++ks) {
                 const Op p0 = q0, p1 = q1, pa = NT == 256 ? qa : (wave ? q1 : q0), la_ = ka, lb = kb;
                 if (ks + 1 < KS) fetch(ks + 1);
-                const Formed sf = Ty::form(half_of(S[ks >> 1], ks & 1));
+                const Formed sf = Ty::form(half_of(S[hh][ks >> 1], ks & 1));
                 ma = Ty::mma(la_, pa, ma);
                 acc[0] = Ty::template part<0>(sf, p0, acc[0]);
                 acc[1] = Ty::template part<0>(sf, p1, acc[1]);
@@ -588,17 +636,27 @@ __device__ __forceinline__ void run_chunks(const Mix& a, const Geom& geo, lds_t*
                     to[64] = q[1];
                 }
             };
-            if (wave < 3) pass(ma, d_a, wave);
-            if (NT != 256 && wave == 0) pass(mb, d_b, 2);
-            read_v();
+            auto factors = [&](bool off) {
+                f32x16 d;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const f32x4 x = tab[((hh * 2 + off) * 4 + q) * 64 + lane];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) d[4 * q + e] = x[e];
+                }
+                return d;
+            };
+            if (wave < 3) pass(ma, R == 1 ? d_a : factors(off_diag), wave);
+            if (NT != 256 && wave == 0) pass(mb, R == 1 ? d_b : factors(true), 2);
+            if (hh == 0) read_v();
             __syncthreads();  // the scores visible; x1 and x3 read
-            if (!Ld::FULL && u + 1 < nch) load(u + 1);
-            const float w0 = power(REV ? max(n - 1 - c, 0) : c + 1) * a.out_scale;
-            const float w1 = power(REV ? max(n - 33 - c, 0) : c + 33) * a.out_scale;
+            if (!Ld::FULL && more) load(u + 1);
+            const float w0 = power(hh, REV ? max(n - 1 - c, 0) : c + 1) * a.out_scale;
+            const float w1 = power(hh, REV ? max(n - 33 - c, 0) : c + 33) * a.out_scale;
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
-                acc[0][r] *= w0;
-                acc[1][r] *= w1;
+                out[0][r] = hh == 0 ? acc[0][r] * w0 : __builtin_fmaf(acc[0][r], w0, out[0][r]);
+                out[1][r] = hh == 0 ? acc[1][r] * w1 : __builtin_fmaf(acc[1][r], w1, out[1][r]);
             }
             auto formed = [&](int slot, int s) {
                 const lds_u32x4* m = reinterpret_cast<const lds_u32x4*>(lds + Ld::M + (2 * slot + s) * 2048) + lane;
@@ -610,7 +668,7 @@ __device__ __forceinline__ void run_chunks(const Mix& a, const Geom& geo, lds_t*
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
                 const Formed f0 = formed(0, s), f1 = formed(1, s), fx = formed(2, s);
-                f32x16 &ax = acc[REV ? 0 : 1], &ay = acc[REV ? 1 : 0];
+                f32x16 &ax = out[REV ? 0 : 1], &ay = out[REV ? 1 : 0];
                 const Formed &gx = REV ? f0 : f1, &gy = REV ? f1 : f0;
                 const Op vx = v[REV ? s : 2 + s], vy = v[REV ? 2 + s : s];
                 ax = Ty::template part<0>(vx, gx, ax);
@@ -622,19 +680,21 @@ __device__ __forceinline__ void run_chunks(const Mix& a, const Geom& geo, lds_t*
                     ax = Ty::template part<1>(vy, fx, ax);
                 }
             }
-            if (n < kC) {  // rows of padding are 0 whatever the state holds
+            if (hh == R - 1) {
+                if (n < kC) {  // rows of padding are 0 whatever the state holds
 #pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    if (c >= n) acc[0][r] = 0.0f;
-                    if (32 + c >= n) acc[1][r] = 0.0f;
+                    for (int r = 0; r < 16; ++r) {
+                        if (c >= n) out[0][r] = 0.0f;
+                        if (32 + c >= n) out[1][r] = 0.0f;
+                    }
                 }
+                put(t0, 0, out[0]);
+                put(t0, 1, out[1]);
             }
-            put(t0, 0, acc[0]);
-            put(t0, 1, acc[1]);
         }
-        if (AGG || u + 1 < nch || a.final_state) {
+        if (AGG || cu + 1 < nch || (R == 1 && a.final_state)) {
             // the operands of step s + 1 are read and formed while those of step s multiply
-            const lds_f32* w0 = wt + 8 * hf + (REV ? 0 : kC - n);
+            const lds_f32* w0 = wt + hh * 128 + 8 * hf + (REV ? 0 : kC - n);
             Op k[KT];
             f32x8 w;
             auto fetch = [&](int s) {
@@ -653,11 +713,11 @@ __device__ __forceinline__ void run_chunks(const Mix& a, const Geom& geo, lds_t*
                 return f;
             };
             fetch(0);
-            const float m = n == kC ? full.next() : expf(la * (float)n);  // at most one chunk is shorter
+            const float m = n == kC ? full[hh].next() : expf(la[hh] * (float)n);  // at most one chunk is shorter
 #pragma unroll
             for (int T = 0; T < KT; ++T)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) S[T][r] *= m;
+                for (int r = 0; r < 16; ++r) S[hh][T][r] *= m;
             Formed wv = weighted(0);
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
@@ -666,45 +726,56 @@ __device__ __forceinline__ void run_chunks(const Mix& a, const Geom& geo, lds_t*
                 for (int T = 0; T < KT; ++T) kn[T] = k[T];
                 if (s < 3) fetch(s + 1);
 #pragma unroll
-                for (int T = 0; T < KT; ++T) S[T] = Ty::template part<0>(kn[T], wv, S[T]);
+                for (int T = 0; T < KT; ++T) S[hh][T] = Ty::template part<0>(kn[T], wv, S[hh][T]);
                 const Op third = rest;
                 const Formed next = s < 3 ? weighted(s + 1) : wv;
                 if constexpr (Ty::PARTS == 2)
 #pragma unroll
-                    for (int T = 0; T < KT; ++T) S[T] = Ty::template part<1>(kn[T], wv, S[T]);
+                    for (int T = 0; T < KT; ++T) S[hh][T] = Ty::template part<1>(kn[T], wv, S[hh][T]);
                 if constexpr (BF16 && EXACT)
 #pragma unroll
-                    for (int T = 0; T < KT; ++T) S[T] = Ty::mma(kn[T], third, S[T]);
+                    for (int T = 0; T < KT; ++T) S[hh][T] = Ty::mma(kn[T], third, S[hh][T]);
                 wv = next;
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
-        if (u + 1 < nch) stage(u + 1, !AGG);
+        if (more) stage(u + 1, !AGG && hh == R - 1);
+        }
     }
 
     if constexpr (AGG) {
         float* dst = a.slots + ((bh * (geo.NS - 1) + (REV ? sc - 1 : sc)) * geo.P + piece) * KD * VD;
-        if (a.trans) each_state_element<KD>([&](int T, int r, int k, int j) { dst[slot_at(j, k, KD)] = S[T][r]; });
-        else each_state_element<KD>([&](int T, int r, int k, int j) { dst[slot_at(k, j, VD)] = S[T][r]; });
+        if (a.trans) each_state_element<KD>([&](int T, int r, int k, int j) { dst[slot_at(j, k, KD)] = S[0][T][r]; });
+        else each_state_element<KD>([&](int T, int r, int k, int j) { dst[slot_at(k, j, VD)] = S[0][T][r]; });
     } else if (a.final_state && (REV ? sc == 0 : sc == geo.NS - 1)) {
         float* dst = a.final_state + bh * KD * VD;
-        each_state_element<KD>([&](int T, int r, int k, int j) { dst[k * VD + j] = S[T][r]; });
+        each_state_element<KD>([&](int T, int r, int k, int j) { dst[k * VD + j] = S[0][T][r]; });
     }
 }
 
 template <int KD, int VD, bool BF16, bool AGG>
 __global__ void __launch_bounds__(2 * VD) __attribute__((amdgpu_waves_per_eu(BF16 ? 2 : 1, BF16 ? 2 : 1)))
 mix_chunks(Jobs jobs, Geom geo) {
-    __shared__ __attribute__((aligned(16))) char lds[Lds<KD, VD, BF16, AGG>::TOTAL];
+    __shared__ __attribute__((aligned(16))) char lds[Lds<KD, VD, BF16, AGG, 1>::TOTAL];
     const int j = blockIdx.y;
     const Mix& m = jobs.m[j];
     if (BF16 && m.exact) {
-        if (jobs.rev[j]) run_chunks<KD, VD, BF16, true, AGG, true>(m, geo, (lds_t*)lds);
-        else run_chunks<KD, VD, BF16, false, AGG, true>(m, geo, (lds_t*)lds);
+        if (jobs.rev[j]) run_chunks<KD, VD, BF16, true, AGG, true, 1>(m, geo, (lds_t*)lds);
+        else run_chunks<KD, VD, BF16, false, AGG, true, 1>(m, geo, (lds_t*)lds);
     } else {
-        if (jobs.rev[j]) run_chunks<KD, VD, BF16, true, AGG, false>(m, geo, (lds_t*)lds);
-        else run_chunks<KD, VD, BF16, false, AGG, false>(m, geo, (lds_t*)lds);
+        if (jobs.rev[j]) run_chunks<KD, VD, BF16, true, AGG, false, 1>(m, geo, (lds_t*)lds);
+        else run_chunks<KD, VD, BF16, false, AGG, false, 1>(m, geo, (lds_t*)lds);
     }
+}
+
+// dq and dk of R heads that share a group
+template <int VD, int R>
+__global__ void __launch_bounds__(2 * VD) __attribute__((amdgpu_waves_per_eu(1, 1)))
+mix_chunks_shared(Jobs jobs, Geom geo) {
+    __shared__ __attribute__((aligned(16))) char lds[Lds<64, VD, true, false, R>::TOTAL];
+    const int j = blockIdx.y;
+    if (jobs.rev[j]) run_chunks<64, VD, true, true, false, false, R>(jobs.m[j], geo, (lds_t*)lds);
+    else run_chunks<64, VD, true, false, false, false, R>(jobs.m[j], geo, (lds_t*)lds);
 }
 
 // Aggregates -> entering states, in the run's direction: what super-chunk s adds, plus
@@ -797,6 +868,16 @@ hipError_t run_carry(const Jobs& jobs, const Geom& g, int KD, int VD, bool bf16,
     return hipGetLastError();
 }
 
+hipError_t run_shared(const Jobs& jobs, const Geom& g, int r, int K, hipStream_t st) {
+    const Mix& m = jobs.m[0];
+    const dim3 grid((unsigned)m.B * (m.H / r) * g.NS, (unsigned)jobs.n), block(2 * K);
+    if (K == 64 && r == 2) launch((mix_chunks_shared<64, 2>), grid, block, 0, st, jobs, g);
+    else if (K == 64) launch((mix_chunks_shared<64, 3>), grid, block, 0, st, jobs, g);
+    else if (r == 2) launch((mix_chunks_shared<128, 2>), grid, block, 0, st, jobs, g);
+    else launch((mix_chunks_shared<128, 3>), grid, block, 0, st, jobs, g);
+    return hipGetLastError();
+}
+
 size_t slot_bytes(int B, int H, int K, int V, const Geom& g) { return (size_t)B * H * (g.NS - 1) * g.P * K * V * 4; }
 
 }  // namespace
@@ -810,7 +891,8 @@ size_t linattn_workspace_bytes(int B, int L, int H, int G, int K, int V, bool bf
 
 // those of both directions, and fp32 dq and dk per head where heads share a group
 size_t linattn_bwd_workspace_bytes(int B, int L, int H, int G, int K, int V, bool bf16) {
-    return 2 * slot_bytes(B, H, K, V, geom(B, L, H, G, K, V, bf16, true)) + (H == G ? 0 : 2 * (size_t)B * L * H * K * 4);
+    return 2 * slot_bytes(B, H, K, V, geom(B, L, H, G, K, V, bf16, true)) + 
+           (H == G || shared_heads(H / G, V, bf16) ? 0 : 2 * (size_t)B * L * H * K * 4);
 }
 
 hipError_t launch_linattn_fwd(const LinattnArgs& a, hipStream_t st) {
@@ -825,7 +907,7 @@ hipError_t launch_linattn_fwd(const LinattnArgs& a, hipStream_t st) {
 hipError_t launch_linattn_bwd(const LinattnBwdArgs& a, hipStream_t st) {
     const Geom g = geom(a.B, a.L, a.H, a.G, a.K, a.V, a.bf16, true);
     const int r = a.H / a.G;
-    const bool shared = r > 1;
+    const bool together = shared_heads(r, a.V, a.bf16), shared = r > 1 && !together;
     const size_t ng = (size_t)a.B * a.L * a.G * a.K, ns = slot_bytes(a.B, a.H, a.K, a.V, g) / 4;
     float* slots = static_cast<float*>(a.ws);
     float* heads = slots + 2 * ns;
@@ -842,6 +924,10 @@ hipError_t launch_linattn_bwd(const LinattnBwdArgs& a, hipStream_t st) {
     // that one launch does both
     if ((e = run_carry(Jobs{{mq, mk}, {0, 1}, 2}, g, a.V, a.K, a.bf16, st)) != hipSuccess) return e;
     mk.exact = 0;  // its own state is no output
+    if (together) {
+        if ((e = run_shared(Jobs{{mq, mk}, {0, 1}, 2}, g, r, a.K, st)) != hipSuccess) return e;
+        return run(Jobs{{mv}, {1}, 1}, g, a.K, a.V, a.bf16, false, st);
+    }
     if (a.K == a.V) {
         if ((e = run(Jobs{{mq, mk, mv}, {0, 1, 1}, 3}, g, a.V, a.K, a.bf16, false, st)) != hipSuccess) return e;
     } else {  // other workgroup sizes

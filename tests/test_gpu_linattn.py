@@ -58,7 +58,7 @@ SHAPES = [
     (1, 1, 1, 1, 64, 64), (2, 2, 2, 1, 128, 64), (1, 31, 2, 2, 64, 128), (2, 63, 3, 1, 128, 128),
     (1, 64, 2, 2, 128, 128), (1, 65, 4, 2, 64, 64), (3, 127, 2, 2, 128, 128), (1, 128, 3, 3, 64, 128),
     (2, 129, 6, 2, 128, 64), (1, 700, 5, 5, 128, 128), (2, 1500, 2, 1, 64, 64), (1, 2500, 1, 1, 128, 128),
-    (5, 257, 7, 7, 64, 64),
+    (5, 257, 7, 7, 64, 64), (2, 300, 3, 1, 64, 64), (1, 1300, 6, 2, 128, 64), (3, 70, 8, 2, 64, 64),
 ]
 
 
