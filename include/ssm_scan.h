@@ -434,12 +434,14 @@ int ssm_ssd_step(int B, int H, int P, int N, ssm_dtype_t io,
  *               on the stored o viewed as [B L, 1, H V] with H groups (padding
  *               rows: what that gives for a row of zeros)
  *   workspace : at least ssm_linattn_workspace_size(B, L, H, G, K, V, io) bytes
- * Arithmetic: products of io values are exact in fp32 accumulators; the state and
- * the decayed score matrix, formed in fp32, enter the matrix cores as pairs of
- * bf16 numbers (about 17 significant bits) when io = SSM_BF16, as fp32 when
- * io = SSM_F32.
- * Supported: K, V in {64, 128}; B, H <= 65535; B * H <= 2^24. Every pointer must be
- * 16-byte aligned; h_final must not be h0. Errors as for ssm_scan_fwd.
+ * Arithmetic: fp32 state and accumulators. With io = SSM_BF16 the matrix cores take
+ * the stored values exactly and what is formed in fp32 (the state, the decayed scores)
+ * as pairs of bf16 numbers (about 17 significant bits, below the rounding of o); what
+ * enters the state itself as triples (24 bits) where h_final is given, as pairs where
+ * not, so o may differ in its last bit between the two. With io = SSM_F32 every product
+ * is fp32.
+ * Supported: K, V in {64, 128}; B, H <= 65535; B * H <= 2^24; L <= 2^30. Every pointer
+ * must be 16-byte aligned; h_final must not be h0. Errors as for ssm_scan_fwd.
  * ------------------------------------------------------------------------- */
 typedef struct {
     const float* weight; /* [H * V] fp32 or NULL (ones) */
@@ -477,7 +479,7 @@ int ssm_linattn_fwd(int B, int L, int H, int G, int K, int V, ssm_dtype_t io,
  *   dh0      : [B, H, K, V]  fp32 out, or NULL (not written); must not be dh_final
  *   workspace: at least ssm_linattn_bwd_workspace_size(B, L, H, G, K, V, io) bytes
  * States are recomputed, not read from a forward call; reductions run in a fixed
- * order. Supported sizes, alignment and errors as for ssm_linattn_fwd.
+ * order. Arithmetic as in ssm_linattn_fwd (triples for dh0's state). Supported sizes, alignment and errors as for ssm_linattn_fwd.
  * ------------------------------------------------------------------------- */
 size_t ssm_linattn_bwd_workspace_size(int B, int L, int H, int G, int K, int V, ssm_dtype_t io);
 

@@ -427,6 +427,7 @@ int linattn_dims(const char* fn, int B, int L, int H, int G, int K, int V, int i
     if (!ssm::linattn_supported_dim(K) || !ssm::linattn_supported_dim(V))
         return fail(SSM_ERR_UNSUPPORTED, fn, "K and V must be 64 or 128");
     if (B > 65535 || H > 65535) return fail(SSM_ERR_UNSUPPORTED, fn, "B and H must be <= 65535");
+    if (L > (1 << 30)) return fail(SSM_ERR_UNSUPPORTED, fn, "L must be <= 2^30");
     if ((long long)B * H > (1LL << 24)) return fail(SSM_ERR_UNSUPPORTED, fn, "B * H must be <= 2^24");
     if (!product_ok({B, L, H, std::max(K, V)}, 1LL << 40) || !product_ok({B, H, K, V}, 1LL << 40))
         return fail(SSM_ERR_INVALID_ARG, fn, "tensor sizes overflow");
@@ -434,7 +435,7 @@ int linattn_dims(const char* fn, int B, int L, int H, int G, int K, int V, int i
 }
 
 bool linattn_dims_ok(int B, int L, int H, int G, int K, int V, int io) {
-    return B >= 1 && L >= 0 && H >= 1 && G >= 1 && H % G == 0 && B <= 65535 && H <= 65535 &&
+    return B >= 1 && L >= 0 && L <= (1 << 30) && H >= 1 && G >= 1 && H % G == 0 && B <= 65535 && H <= 65535 &&
            (long long)B * H <= (1LL << 24) && (io == SSM_F32 || io == SSM_BF16) && ssm::linattn_supported_dim(K) &&
            ssm::linattn_supported_dim(V) && product_ok({B, L, H, std::max(K, V)}, 1LL << 40) &&
            product_ok({B, H, K, V}, 1LL << 40);

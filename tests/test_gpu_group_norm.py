@@ -233,3 +233,23 @@ def test_nothing_is_written_outside_the_outputs():
         torch.cuda.synchronize()
         for buf in bufs:
             assert (buf[:1024] == 7).all() and (buf[-1024:] == 7).all()
+
+
+@pytest.mark.parametrize("S", [1, 700000])
+def test_offsets_beyond_32_bits(S):
+    """More than 2^31 elements: the last sample is what a call on it alone gives."""
+    C, G = 1536, 24
+    M = 2 if S > 1 else 1400003
+    gen = torch.Generator(device=DEV).manual_seed(3)
+    x = torch.randn((M, S, C), generator=gen, device=DEV, dtype=BF16)
+    assert x.numel() > 2 ** 31
+    w = torch.randn(C, generator=gen, device=DEV)
+    y, mean, rstd = ssa.ssm_group_norm_fwd(x, G, w, act="silu")
+    y2, mean2, rstd2 = ssa.ssm_group_norm_fwd(x[-1:], G, w, act="silu")
+    # (a sample alone may be cut into other ranges: statistics within rounding, y a bf16 step)
+    assert torch.allclose(mean[-1:], mean2, atol=1e-6) and torch.allclose(rstd[-1:], rstd2, rtol=1e-6)
+    assert float((y[-1:].float() - y2.float()).abs().max()) <= 2.0 ** -7 * float(y2.float().abs().max())
+    g = ssa.ssm_group_norm_bwd(x, G, mean, rstd, y, w, act="silu", want_affine=False)
+    g2 = ssa.ssm_group_norm_bwd(x[-1:], G, mean[-1:].contiguous(), rstd[-1:].contiguous(), y[-1:], w, act="silu",
+                                want_affine=False)
+    assert float((g["dx"][-1:].float() - g2["dx"].float()).abs().max()) <= 2.0 ** -7 * float(g2["dx"].float().abs().max())

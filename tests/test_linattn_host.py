@@ -73,7 +73,7 @@ def _norm(weight=None, bias=None, z=None, eps=1e-5):
 # every case has exactly one defect, so no call reaches a launch
 DIMS = [(dict(B=0), 1), (dict(L=-1), 1), (dict(H=0), 1), (dict(G=0), 1), (dict(G=3), 1), (dict(io=4), 1),
         (dict(K=32), 2), (dict(V=96), 2), (dict(K=256), 2), (dict(B=70000), 2), (dict(H=65536, G=1), 2),
-        (dict(B=65535, H=1024, G=1024), 2)]
+        (dict(B=65535, H=1024, G=1024), 2), (dict(L=(1 << 30) + 1, B=1, H=1, G=1), 2)]
 
 
 @pytest.mark.parametrize("kw,status", DIMS + [
