@@ -440,8 +440,11 @@ int ssm_ssd_step(int B, int H, int P, int N, ssm_dtype_t io,
  * enters the state itself as triples (24 bits) where h_final is given, as pairs where
  * not, so o may differ in its last bit between the two. With io = SSM_F32 every product
  * is fp32.
- * Supported: K, V in {64, 128}; B, H <= 65535; B * H <= 2^24; L <= 2^30. Every pointer
- * must be 16-byte aligned; h_final must not be h0. Errors as for ssm_scan_fwd.
+ * A row that is not finite reaches the rows from its own on, and may reach the rows
+ * before it in its chunk of 64 (a product with a zero weight); padding rows reach none.
+ * Supported: K, V in {64, 128}; B, H <= 65535; B * H <= 2^22; L <= 2^30; with norm H * V
+ * <= 65536 and B * L * H <= 2^30. Every pointer must be 16-byte aligned. Outputs must not
+ * alias inputs or each other (the same address is refused). Errors as for ssm_scan_fwd.
  * ------------------------------------------------------------------------- */
 typedef struct {
     const float* weight; /* [H * V] fp32 or NULL (ones) */
@@ -476,10 +479,11 @@ int ssm_linattn_fwd(int B, int L, int H, int G, int K, int V, ssm_dtype_t io,
  *   dh_final : [B, H, K, V]  fp32 or NULL (zeros)
  *   dq, dk   : [B, L, G, K]  io dtype out (0 at padding)
  *   dv       : [B, L, H, V]  io dtype out (0 at padding)
- *   dh0      : [B, H, K, V]  fp32 out, or NULL (not written); must not be dh_final
+ *   dh0      : [B, H, K, V]  fp32 out, or NULL (not written)
  *   workspace: at least ssm_linattn_bwd_workspace_size(B, L, H, G, K, V, io) bytes
  * States are recomputed, not read from a forward call; reductions run in a fixed
- * order. Arithmetic as in ssm_linattn_fwd (triples for dh0's state). Supported sizes, alignment and errors as for ssm_linattn_fwd.
+ * order. Arithmetic as in ssm_linattn_fwd (triples for dh0's state). Supported sizes,
+ * alignment, aliasing and errors as for ssm_linattn_fwd.
  * ------------------------------------------------------------------------- */
 size_t ssm_linattn_bwd_workspace_size(int B, int L, int H, int G, int K, int V, ssm_dtype_t io);
 
@@ -497,8 +501,9 @@ int ssm_linattn_bwd(int B, int L, int H, int G, int K, int V, ssm_dtype_t io,
  *   q, k  : [B, G, K]     io dtype;  v, o : [B, H, V]  io dtype
  *   norm  : as for ssm_linattn_fwd (z: [B, H, V]); here the norm takes o before it
  *           is rounded to the io dtype
- * Supported: K, V in {64, 128}; B * H <= 2^24. Every pointer must be 16-byte
- * aligned. Errors as for ssm_step.
+ * Supported: K, V in {64, 128}; B, H <= 65535; B * H <= 2^22. Every pointer must be
+ * 16-byte aligned; o and state must not alias each other or another argument. Errors as
+ * for ssm_step.
  * ------------------------------------------------------------------------- */
 int ssm_linattn_step(int B, int H, int G, int K, int V, ssm_dtype_t io,
                      float* state, const void* q, const void* k, const void* v,
@@ -524,8 +529,9 @@ int ssm_linattn_step(int B, int H, int G, int K, int V, ssm_dtype_t io,
  *   workspace    : at least ssm_group_norm_workspace_size(M, S, C, G, io) bytes
  * Statistics are fp32, from squared distances to a mean (no difference of large
  * sums). Supported: C >= 1 a multiple of G, C <= 65536; M >= 0 and S >= 1 (M = 0 does
- * nothing); M * S * C <= 2^38, M * S < 2^31. Every pointer must be 16-byte
- * aligned. Errors as for ssm_scan_fwd.
+ * nothing); M * S * C <= 2^38, M * S <= 2^30, M * G <= 2^30. Every pointer must be
+ * 16-byte aligned. But for y and x, outputs must not alias inputs or each other (the
+ * same address is refused). Errors as for ssm_scan_fwd.
  * ------------------------------------------------------------------------- */
 typedef enum { SSM_ACT_NONE = 0, SSM_ACT_SILU = 1, SSM_ACT_INT_RANGE_ = 0x7fffffff } ssm_act_t;
 

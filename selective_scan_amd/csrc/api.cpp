@@ -7,6 +7,7 @@
 #include <algorithm>
 #include <cstdint>
 #include <cstdio>
+#include <initializer_list>
 #include <limits>
 #include <string>
 
@@ -358,7 +359,7 @@ int ssm_ssd_fwd(int B, int L, int H, int P, int N, int chunk, ssm_dtype_t io,
     const char* why = ssm::ssd_unsupported_reason(L, H, P, N, Q, io == SSM_BF16);
     if (why[0] != '\0') return fail(SSM_ERR_UNSUPPORTED, fn, why);
     if (B > 65535) return fail(SSM_ERR_UNSUPPORTED, fn, "B must be <= 65535");
-    if ((long long)B * H > (1LL << 24)) return fail(SSM_ERR_UNSUPPORTED, fn, "B * H must be <= 2^24");
+    if ((long long)B * H > (1LL << 22)) return fail(SSM_ERR_UNSUPPORTED, fn, "B * H must be <= 2^22");
     if (!product_ok({B, L, H, P}, 1LL << 40) || !product_ok({B, H, N, P}, 1LL << 40))
         return fail(SSM_ERR_INVALID_ARG, fn, "tensor sizes overflow");
     if (!A) return fail(SSM_ERR_INVALID_ARG, fn, "A is NULL");
@@ -428,7 +429,7 @@ int linattn_dims(const char* fn, int B, int L, int H, int G, int K, int V, int i
         return fail(SSM_ERR_UNSUPPORTED, fn, "K and V must be 64 or 128");
     if (B > 65535 || H > 65535) return fail(SSM_ERR_UNSUPPORTED, fn, "B and H must be <= 65535");
     if (L > (1 << 30)) return fail(SSM_ERR_UNSUPPORTED, fn, "L must be <= 2^30");
-    if ((long long)B * H > (1LL << 24)) return fail(SSM_ERR_UNSUPPORTED, fn, "B * H must be <= 2^24");
+    if ((long long)B * H > (1LL << 22)) return fail(SSM_ERR_UNSUPPORTED, fn, "B * H must be <= 2^22");
     if (!product_ok({B, L, H, std::max(K, V)}, 1LL << 40) || !product_ok({B, H, K, V}, 1LL << 40))
         return fail(SSM_ERR_INVALID_ARG, fn, "tensor sizes overflow");
     return SSM_OK;
@@ -436,9 +437,18 @@ int linattn_dims(const char* fn, int B, int L, int H, int G, int K, int V, int i
 
 bool linattn_dims_ok(int B, int L, int H, int G, int K, int V, int io) {
     return B >= 1 && L >= 0 && L <= (1 << 30) && H >= 1 && G >= 1 && H % G == 0 && B <= 65535 && H <= 65535 &&
-           (long long)B * H <= (1LL << 24) && (io == SSM_F32 || io == SSM_BF16) && ssm::linattn_supported_dim(K) &&
+           (long long)B * H <= (1LL << 22) && (io == SSM_F32 || io == SSM_BF16) && ssm::linattn_supported_dim(K) &&
            ssm::linattn_supported_dim(V) && product_ok({B, L, H, std::max(K, V)}, 1LL << 40) &&
            product_ok({B, H, K, V}, 1LL << 40);
+}
+
+// Whether an output is an input or another output (the same address).
+bool shared_buffer(std::initializer_list<const void*> outs, std::initializer_list<const void*> ins) {
+    for (auto o = outs.begin(); o != outs.end(); ++o) {
+        if (*o && (std::find(ins.begin(), ins.end(), *o) != ins.end() || std::find(o + 1, outs.end(), *o) != outs.end()))
+            return true;
+    }
+    return false;
 }
 
 int linattn_norm_args(const char* fn, const ssm_linattn_norm_t* n, ssm::LinattnNorm* out) {
@@ -460,14 +470,15 @@ int group_norm_dims(const char* fn, int M, int S, int C, int G, int io, int act)
         return fail(SSM_ERR_INVALID_ARG, fn, "act must be SSM_ACT_NONE or SSM_ACT_SILU");
     if (C % G != 0) return fail(SSM_ERR_INVALID_ARG, fn, "G must divide C");
     if (C > 65536) return fail(SSM_ERR_UNSUPPORTED, fn, "C must be <= 65536");
-    if (!product_ok({M, S}, 0x7fffffffLL)) return fail(SSM_ERR_UNSUPPORTED, fn, "M * S must be < 2^31");
+    if (!product_ok({M, S}, 1LL << 30)) return fail(SSM_ERR_UNSUPPORTED, fn, "M * S must be <= 2^30");
+    if (!product_ok({M, G}, 1LL << 30)) return fail(SSM_ERR_UNSUPPORTED, fn, "M * G must be <= 2^30");
     if (!product_ok({M, S, C}, 1LL << 38)) return fail(SSM_ERR_INVALID_ARG, fn, "tensor sizes overflow");
     return SSM_OK;
 }
 
 bool group_norm_dims_ok(int M, int S, int C, int G, int io) {
     return M >= 0 && S >= 1 && C >= 1 && C <= 65536 && G >= 1 && C % G == 0 && (io == SSM_F32 || io == SSM_BF16) &&
-           product_ok({M, S}, 0x7fffffffLL) && product_ok({M, S, C}, 1LL << 38);
+           product_ok({M, S}, 1LL << 30) && product_ok({M, G}, 1LL << 30) && product_ok({M, S, C}, 1LL << 38);
 }
 
 }  // namespace
@@ -493,14 +504,15 @@ int ssm_linattn_fwd(int B, int L, int H, int G, int K, int V, ssm_dtype_t io,
     const void* ptrs[] = {q, k, v, log_decay, seqlens, h0, o, h_final, workspace};
     for (const void* p : ptrs)
         if (!aligned16(p)) return fail(SSM_ERR_INVALID_ARG, fn, "every pointer must be 16-byte aligned");
-    if (h0 && h0 == h_final) return fail(SSM_ERR_INVALID_ARG, fn, "h_final must not be h0");
     ssm::LinattnNorm nm;
     if ((s = linattn_norm_args(fn, norm, &nm)) != SSM_OK) return s;
-    if (nm.on && ((long long)H * V > 65536 || !product_ok({B, L}, 0x7fffffffLL) || !product_ok({B, L, H, V}, 1LL << 38)))
-        return fail(SSM_ERR_UNSUPPORTED, fn, "norm: H * V must be <= 65536, B * L < 2^31 and B * L * H * V <= 2^38");
+    if (nm.on && ((long long)H * V > 65536 || !product_ok({B, L, H}, 1LL << 30)))
+        return fail(SSM_ERR_UNSUPPORTED, fn, "norm: H * V must be <= 65536 and B * L * H <= 2^30");
     const size_t need = ssm::linattn_workspace_bytes(B, L, H, G, K, V, io == SSM_BF16);
     if (need > 0 && (workspace == nullptr || workspace_bytes < need))
         return fail(SSM_ERR_WORKSPACE, fn, "workspace missing or smaller than ssm_linattn_workspace_size()");
+    if (shared_buffer({o, h_final}, {q, k, v, log_decay, seqlens, h0, nm.weight, nm.bias, nm.z}))
+        return fail(SSM_ERR_INVALID_ARG, fn, "an output must not be an input or another output");
     const hipStream_t st = static_cast<hipStream_t>(stream);
     ssm::LinattnArgs a{B, L, H, G, K, V, io == SSM_BF16, q, k, v, log_decay, scale, seqlens, h0, o, h_final, workspace};
     const hipError_t e = ssm::launch_linattn_fwd(a, st);
@@ -531,10 +543,11 @@ int ssm_linattn_bwd(int B, int L, int H, int G, int K, int V, ssm_dtype_t io,
     const void* ptrs[] = {q, k, v, log_decay, seqlens, h0, dout, dh_final, dq, dk, dv, dh0, workspace};
     for (const void* p : ptrs)
         if (!aligned16(p)) return fail(SSM_ERR_INVALID_ARG, fn, "every pointer must be 16-byte aligned");
-    if (dh0 && dh0 == dh_final) return fail(SSM_ERR_INVALID_ARG, fn, "dh0 must not be dh_final");
     const size_t need = ssm::linattn_bwd_workspace_bytes(B, L, H, G, K, V, io == SSM_BF16);
     if (need > 0 && (workspace == nullptr || workspace_bytes < need))
         return fail(SSM_ERR_WORKSPACE, fn, "workspace missing or smaller than ssm_linattn_bwd_workspace_size()");
+    if (shared_buffer({dq, dk, dv, dh0}, {q, k, v, log_decay, seqlens, h0, dout, dh_final}))
+        return fail(SSM_ERR_INVALID_ARG, fn, "an output must not be an input or another output");
     ssm::LinattnBwdArgs a{B, L, H, G, K, V, io == SSM_BF16, q, k, v, log_decay, scale, seqlens, h0, dout, dh_final,
                           dq, dk, dv, dh0, workspace};
     return hip_status(ssm::launch_linattn_bwd(a, static_cast<hipStream_t>(stream)), fn);
@@ -554,6 +567,8 @@ int ssm_linattn_step(int B, int H, int G, int K, int V, ssm_dtype_t io,
         if (!aligned16(p)) return fail(SSM_ERR_INVALID_ARG, fn, "every pointer must be 16-byte aligned");
     ssm::LinattnNorm nm;
     if ((s = linattn_norm_args(fn, norm, &nm)) != SSM_OK) return s;
+    if (shared_buffer({state, o}, {q, k, v, log_decay, nm.weight, nm.bias, nm.z}))
+        return fail(SSM_ERR_INVALID_ARG, fn, "an output must not be an input or another output");
     ssm::LinattnStepArgs a{B, H, G, K, V, io == SSM_BF16, state, q, k, v, log_decay, scale, nm, o};
     return hip_status(ssm::launch_linattn_step(a, static_cast<hipStream_t>(stream)), fn);
 }
@@ -581,6 +596,8 @@ int ssm_group_norm_fwd(int M, int S, int C, int G, ssm_dtype_t io, ssm_act_t act
     const size_t need = ssm::group_norm_workspace_bytes(M, S, C, G, io == SSM_BF16);
     if (need > 0 && (workspace == nullptr || workspace_bytes < need))
         return fail(SSM_ERR_WORKSPACE, fn, "workspace missing or smaller than ssm_group_norm_workspace_size()");
+    if (shared_buffer({mean, rstd, y}, {weight, bias, z}) || shared_buffer({mean, rstd}, {x}))
+        return fail(SSM_ERR_INVALID_ARG, fn, "an output must not be an input or another output");
     ssm::GroupNormArgs a{M, S, C, G, io == SSM_BF16, act, x, weight, bias, z, eps, y, mean, rstd, workspace};
     return hip_status(ssm::launch_group_norm_fwd(a, static_cast<hipStream_t>(stream)), fn);
 }
@@ -608,6 +625,8 @@ int ssm_group_norm_bwd(int M, int S, int C, int G, ssm_dtype_t io, ssm_act_t act
     const size_t need = ssm::group_norm_bwd_workspace_bytes(M, S, C, G, io == SSM_BF16);
     if (need > 0 && (workspace == nullptr || workspace_bytes < need))
         return fail(SSM_ERR_WORKSPACE, fn, "workspace missing or smaller than ssm_group_norm_bwd_workspace_size()");
+    if (shared_buffer({dx, dweight, dbias, dz}, {x, weight, bias, z, mean, rstd, dy}))
+        return fail(SSM_ERR_INVALID_ARG, fn, "an output must not be an input or another output");
     ssm::GroupNormBwdArgs a{M, S, C, G, io == SSM_BF16, act, x, weight, bias, z, mean, rstd, dy, dx, dweight, dbias,
                             dz, workspace};
     return hip_status(ssm::launch_group_norm_bwd(a, static_cast<hipStream_t>(stream)), fn);

@@ -538,7 +538,7 @@ def ssm_linattn_fwd(q, k, v, log_decay, *, scale=None, seqlens=None, h0=None, no
         workspace, wp, wbytes = _space(need, workspace, dev)
     op, hp = _fits(o, "o", ov, io, dev), _fits(h_final, "h_final", st, torch.float32, dev, False)
     with _Launch(dev, stream) as s:
-        rc = lib().ssm_linattn_fwd(B, L, H, G, K, V, code, *p, K ** -0.5 if scale is None else scale, lens, h0p, norm,
+        rc = lib().ssm_linattn_fwd(B, L, H, G, K, V, code, *p, max(K, 1) ** -0.5 if scale is None else scale, lens, h0p, norm,
                                    op, hp, wp, wbytes, s)
     if rc != SSM_OK:
         _raise("ssm_linattn_fwd", rc)
@@ -576,7 +576,7 @@ def ssm_linattn_bwd(q, k, v, log_decay, dout, *, scale=None, seqlens=None, h0=No
             gp.append(_fits(g[n], n, shape, dt, dev, n != "dh0"))
         workspace, wp, wbytes = _space(need, workspace, dev)
     with _Launch(dev, stream) as s:
-        rc = lib().ssm_linattn_bwd(B, L, H, G, K, V, code, *p, K ** -0.5 if scale is None else scale, lens, h0p, dp, tp,
+        rc = lib().ssm_linattn_bwd(B, L, H, G, K, V, code, *p, max(K, 1) ** -0.5 if scale is None else scale, lens, h0p, dp, tp,
                                    *gp, wp, wbytes, s)
     if rc != SSM_OK:
         _raise("ssm_linattn_bwd", rc)
@@ -604,7 +604,7 @@ def ssm_linattn_step(state, q, k, v, log_decay, *, scale=None, norm_eps=None, no
             o = torch.empty(ov, dtype=io, device=dev)
     op = _fits(o, "o", ov, io, dev)
     with _Launch(dev, stream) as s:
-        rc = lib().ssm_linattn_step(B, H, G, K, V, code, *p, K ** -0.5 if scale is None else scale, norm, op, s)
+        rc = lib().ssm_linattn_step(B, H, G, K, V, code, *p, max(K, 1) ** -0.5 if scale is None else scale, norm, op, s)
     if rc != SSM_OK:
         _raise("ssm_linattn_step", rc)
     return o

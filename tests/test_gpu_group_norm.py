@@ -253,3 +253,25 @@ def test_offsets_beyond_32_bits(S):
     g2 = ssa.ssm_group_norm_bwd(x[-1:], G, mean[-1:].contiguous(), rstd[-1:].contiguous(), y[-1:], w, act="silu",
                                 want_affine=False)
     assert float((g["dx"][-1:].float() - g2["dx"].float()).abs().max()) <= 2.0 ** -7 * float(g2["dx"].float().abs().max())
+
+
+@pytest.mark.parametrize("M,S,C,dtype", [
+    ((1 << 22) + 5, 2, 32, BF16),   # a workgroup per sample
+    ((1 << 22) + 5, 2, 33, BF16),   # tiles
+    ((1 << 24) + 21, 1, 33, BF16),  # a wave per row
+])
+def test_more_workgroups_than_a_grid_dimension_takes(M, S, C, dtype):
+    """The samples on both sides of the fold, and the last, are what calls on them alone give."""
+    gen = torch.Generator(device=DEV).manual_seed(11)
+    x = torch.randn((M, S, C), generator=gen, device=DEV, dtype=dtype)
+    w, b = (torch.randn(C, generator=gen, device=DEV) for _ in range(2))
+    y, mean, rstd = ssa.ssm_group_norm_fwd(x, 1, w, b, act="silu")
+    g = ssa.ssm_group_norm_bwd(x, 1, mean, rstd, y, w, b, act="silu", want_affine=False)["dx"]
+    for lo, hi in ((0, 3), (M // 2, M // 2 + 3), ((1 << 22) - 2, (1 << 22) + 5), (M - 6, M)):
+        y2, mean2, rstd2 = ssa.ssm_group_norm_fwd(x[lo:hi].clone(), 1, w, b, act="silu")
+        g2 = ssa.ssm_group_norm_bwd(x[lo:hi].clone(), 1, mean[lo:hi].clone(), rstd[lo:hi].clone(), y[lo:hi].clone(), w, b,
+                                    act="silu", want_affine=False)["dx"]
+        # (few samples alone may be cut into other ranges: statistics within rounding, y a bf16 step)
+        assert torch.allclose(mean[lo:hi], mean2, atol=1e-6) and torch.allclose(rstd[lo:hi], rstd2, rtol=1e-5)
+        assert float((y[lo:hi].float() - y2.float()).abs().max()) <= 2.0 ** -7 * float(y2.float().abs().max())
+        assert float((g[lo:hi].float() - g2.float()).abs().max()) <= 2.0 ** -7 * float(g2.float().abs().max())

@@ -73,7 +73,8 @@ def _norm(weight=None, bias=None, z=None, eps=1e-5):
 # every case has exactly one defect, so no call reaches a launch
 DIMS = [(dict(B=0), 1), (dict(L=-1), 1), (dict(H=0), 1), (dict(G=0), 1), (dict(G=3), 1), (dict(io=4), 1),
         (dict(K=32), 2), (dict(V=96), 2), (dict(K=256), 2), (dict(B=70000), 2), (dict(H=65536, G=1), 2),
-        (dict(B=65535, H=1024, G=1024), 2), (dict(L=(1 << 30) + 1, B=1, H=1, G=1), 2)]
+        (dict(B=65535, H=1024, G=1024), 2), (dict(L=(1 << 30) + 1, B=1, H=1, G=1), 2),
+        (dict(B=4096, H=1025, G=1), 2)]
 
 
 @pytest.mark.parametrize("kw,status", DIMS + [
@@ -116,7 +117,8 @@ def test_linattn_step_rejects(kw, status):
 
 
 NDIMS = [(dict(M=-1), 1), (dict(S=0), 1), (dict(C=0), 1), (dict(G=0), 1), (dict(G=5), 1), (dict(io=2), 1),
-         (dict(act=2), 1), (dict(C=65600, G=1), 2), (dict(M=1 << 20, S=1 << 20), 2)]
+         (dict(act=2), 1), (dict(C=65600, G=1), 2), (dict(M=1 << 20, S=1 << 20), 2),
+         (dict(M=1, S=(1 << 30) + 1, C=1, G=1), 2), (dict(M=1 << 21, S=1, C=1024, G=1024), 2)]
 
 
 @pytest.mark.parametrize("kw,status", NDIMS + [
@@ -142,6 +144,33 @@ def test_group_norm_bwd_rejects(kw, status):
                                         a["z"], a["mean"], a["rstd"], a["dy"], a["dx"], a["dw"], a["db"], a["dz"], P,
                                         1 << 40, None) == status
     assert ops.lib().ssm_last_error().startswith(b"ssm_group_norm_bwd: ")
+
+
+def _refused(status):
+    assert status == 1
+    assert b"an output must not be" in ops.lib().ssm_last_error()
+
+
+def test_outputs_that_are_inputs_or_each_other_are_refused():
+    L, n = ops.lib(), [0x10000 * (i + 1) for i in range(16)]
+    dims = (2, 8, 2, 2, 64, 64, 1)
+    for o, hf, h0, z in ((n[2], None, None, None), (n[0], None, None, None), (n[4], n[5], n[5], None),
+                         (n[4], n[4], None, None), (n[4], None, None, n[4])):
+        _refused(L.ssm_linattn_fwd(*dims, *n[:4], 1.0, None, h0, _norm(z=z) if z else None, o, hf, n[9], 1 << 40, None))
+    for at in range(4):
+        outs = n[8:12]
+        for other in (n[0], n[5], outs[(at + 1) % 4]):
+            _refused(L.ssm_linattn_bwd(*dims, *n[:4], 1.0, None, None, n[4], n[5],
+                                       *(other if i == at else x for i, x in enumerate(outs)), n[15], 1 << 40, None))
+    for o, z in ((n[3], None), (n[0], None), (n[6], n[6])):
+        _refused(L.ssm_linattn_step(2, 2, 2, 64, 64, 1, n[0], n[1], n[2], n[3], n[4], 1.0, _norm(z=z), o, None))
+    for y, mean, rstd in ((n[3], n[5], n[6]), (n[4], n[5], n[5]), (n[4], n[0], n[6]), (n[4], n[4], n[6])):
+        _refused(L.ssm_group_norm_fwd(2, 3, 24, 4, 1, 0, n[0], n[1], n[2], n[3], 1e-5, y, mean, rstd, n[9], 1 << 40, None))
+    for at in range(4):
+        outs = n[8:12]
+        for other in (n[0], n[6], outs[(at + 1) % 4]):
+            _refused(L.ssm_group_norm_bwd(2, 3, 24, 4, 1, 0, *n[:7],
+                                          *(other if i == at else x for i, x in enumerate(outs)), n[15], 1 << 40, None))
 
 
 def test_workspace_sizes_of_refused_shapes_are_zero():
