@@ -17,12 +17,16 @@
 //              S    <- lam^n S + sum_j lam^(j+1) x2_j (x) x3_j
 // Every power has an exponent >= 0, so none can overflow.
 //
-// Kernels. A sequence is cut into super-chunks (runs of chunks), one workgroup per
-// (batch, head, super-chunk):
-//   mix_chunks<AGG>   every super-chunk but the last in the run's direction: its state
-//                     from a zero start
+// Launches. A sequence is cut into super-chunks (runs of chunks), one workgroup per
+// (batch, head, super-chunk); runs that need no other's result share a launch:
+//   mix_chunks<AGG>   every super-chunk but the last in the run's direction: what it adds to
+//                     the state, from a zero start (in pieces where that pays)
 //   mix_carry         per state element, over the super-chunks: the state entering each
-//   mix_chunks        the outputs, from that state
+//   mix_chunks        the outputs, from that state (mix_chunks_shared: dq and dk of two or
+//                     three heads that share a group, their sum in registers)
+//   sum_heads         dq and dk of other shared groups, from fp32 planes per head
+// With one super-chunk only the third runs. All are deterministic.
+//
 // One wave owns 32 columns of the state (all KD rows, fp32, in its accumulators) and
 // the same columns of the output. The state never leaves the registers: an
 // accumulator tile of v_mfma_f32_32x32x16_bf16 holds column c = lane % 32 and, per half
@@ -35,8 +39,24 @@
 // columns of one row: 16-byte stores.
 // Operands stored in bf16 enter exactly; those formed in fp32 (state, decayed scores,
 // weighted x3) enter as hi = bf16(x) and lo = bf16(x - hi), two products, about 17
-// significant bits (one bf16 rounding would cost 1e-3 of the result). With fp32
-// storage every product is v_mfma_f32_32x32x2_f32.
+// significant bits: one bf16 rounding would cost 1e-3 of the result, two are far below
+// the rounding of a bf16 output. Where the state itself is an output (fp32), weighted x3
+// enters it with a third part, 24 bits: the final state is then 3e-7 off and not 2e-6,
+// for 2% of the time (8% at V = 64). With fp32 storage every product is
+// v_mfma_f32_32x32x2_f32.
+// The scores are computed once per workgroup (a 32 x 32 tile a wave) and passed on through
+// LDS as finished operands; each wave computing all of them was 16 of 100 products and 130
+// vector instructions a chunk more. Rows go straight into LDS (no registers between: these
+// cost 50 to 80, spills at V = 64, 235 -> 173 us at B4 L8000 H24 K128 V64).
+//
+// What bounds it (bf16, K = V = 128). A chunk's 84 products of 32 cycles are 1.1 us at
+// 2.4 GHz; with the splits, decays and waits a workgroup alone on its CU takes 3.3 us a
+// chunk (6900 cycles: 1700 scores and x1 S, 400 passing, 900 barrier and loads' issue, 740
+// scores times x3, 650 stores, 2000 state, 430 waiting for rows), one of two on a CU 5.2 us.
+// B4 L4096 H16 (one super-chunk, dq, dk and dv side by side): 231 us, 470 MB that have to
+// move (92 us at a copy's rate), 800 MB moved. Tried and not kept: both buffers for x1 and
+// x3 as well at K = V = 128 (one workgroup a CU; 246 us either way), the state's first
+// operands before the read-out (spills), more than 256 registers (AGPR copies: 275 us).
 #include "common.h"
 #include "launch.h"
 #include "linattn.h"
@@ -578,168 +598,168 @@ __device__ __forceinline__ void run_chunks(const Mix& a, const Geom& geo, lds_t*
         f32x16 out[2];
 #pragma unroll
         for (int hh = 0; hh < R; ++hh) {
-        const int u = cu * R + hh;
-        const bool more = u + 1 < nch * R;
-        const lds_t* x1 = lds + Ld::X1 + u % Ld::N13 * Ld::BK;
-        const lds_t* x2 = lds + Ld::X2 + u % Ld::N2 * Ld::BK;
-        const lds_t* x3 = lds + Ld::X3 + u % Ld::N13 * Ld::BV;
-        if (Ld::FULL && more) load(u + 1);
-        auto read_v = [&]() {
+            const int u = cu * R + hh;
+            const bool more = u + 1 < nch * R;
+            const lds_t* x1 = lds + Ld::X1 + u % Ld::N13 * Ld::BK;
+            const lds_t* x2 = lds + Ld::X2 + u % Ld::N2 * Ld::BK;
+            const lds_t* x3 = lds + Ld::X3 + u % Ld::N13 * Ld::BV;
+            if (Ld::FULL && more) load(u + 1);
+            auto read_v = [&]() {
 #pragma unroll
-            for (int s = 0; s < 4; ++s) v[s] = Ty::template col8<VD>(x3, 16 * s, 32 * wave);
-        };
-        if constexpr (AGG) {
-            read_v();
-        } else {
-            // scores (rows j in the order pi, columns i) and x1 S (rows: columns of S); the
-            // operands of step ks + 1 are read while those of ks multiply
-            f32x16 acc[2], ma, mb;
-#pragma unroll
-            for (int r = 0; r < 16; ++r) acc[0][r] = acc[1][r] = ma[r] = mb[r] = 0.0f;
-            const lds_t* xj = x2 + Ja * (Ld::BK / 2);
-            const lds_t* xi = x1 + Ia * (Ld::BK / 2);
-            Op q0, q1, qa{}, ka, kb{};
-            auto fetch = [&](int ks) {
-                q0 = Ty::template row8<KD>(x1, c, ks);
-                q1 = Ty::template row8<KD>(x1, 32 + c, ks);
-                ka = Ty::template row8<KD>(xj, pi(c), ks);
-                if constexpr (NT == 256) qa = Ty::template row8<KD>(xi, c, ks);
-                else kb = Ty::template row8<KD>(x2, (REV ? 32 : 0) + pi(c), ks);
+                for (int s = 0; s < 4; ++s) v[s] = Ty::template col8<VD>(x3, 16 * s, 32 * wave);
             };
-            fetch(0);
+            if constexpr (AGG) {
+                read_v();
+            } else {
+                // scores (rows j in the order pi, columns i) and x1 S (rows: columns of S); the
+                // operands of step ks + 1 are read while those of ks multiply
+                f32x16 acc[2], ma, mb;
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
-                const Op p0 = q0, p1 = q1, pa = NT == 256 ? qa : (wave ? q1 : q0), la_ = ka, lb = kb;
-                if (ks + 1 < KS) fetch(ks + 1);
-                const Formed sf = Ty::form(half_of(S[hh][ks >> 1], ks & 1));
-                ma = Ty::mma(la_, pa, ma);
-                acc[0] = Ty::template part<0>(sf, p0, acc[0]);
-                acc[1] = Ty::template part<0>(sf, p1, acc[1]);
-                if constexpr (NT != 256) mb = Ty::mma(lb, REV ? p0 : p1, mb);
-                if constexpr (Ty::PARTS == 2) {
-                    acc[0] = Ty::template part<1>(sf, p0, acc[0]);
-                    acc[1] = Ty::template part<1>(sf, p1, acc[1]);
+                for (int r = 0; r < 16; ++r) acc[0][r] = acc[1][r] = ma[r] = mb[r] = 0.0f;
+                const lds_t* xj = x2 + Ja * (Ld::BK / 2);
+                const lds_t* xi = x1 + Ia * (Ld::BK / 2);
+                Op q0, q1, qa{}, ka, kb{};
+                auto fetch = [&](int ks) {
+                    q0 = Ty::template row8<KD>(x1, c, ks);
+                    q1 = Ty::template row8<KD>(x1, 32 + c, ks);
+                    ka = Ty::template row8<KD>(xj, pi(c), ks);
+                    if constexpr (NT == 256) qa = Ty::template row8<KD>(xi, c, ks);
+                    else kb = Ty::template row8<KD>(x2, (REV ? 32 : 0) + pi(c), ks);
+                };
+                fetch(0);
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks) {
+                    const Op p0 = q0, p1 = q1, pa = NT == 256 ? qa : (wave ? q1 : q0), la_ = ka, lb = kb;
+                    if (ks + 1 < KS) fetch(ks + 1);
+                    const Formed sf = Ty::form(half_of(S[hh][ks >> 1], ks & 1));
+                    ma = Ty::mma(la_, pa, ma);
+                    acc[0] = Ty::template part<0>(sf, p0, acc[0]);
+                    acc[1] = Ty::template part<0>(sf, p1, acc[1]);
+                    if constexpr (NT != 256) mb = Ty::mma(lb, REV ? p0 : p1, mb);
+                    if constexpr (Ty::PARTS == 2) {
+                        acc[0] = Ty::template part<1>(sf, p0, acc[0]);
+                        acc[1] = Ty::template part<1>(sf, p1, acc[1]);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
                 }
-                __builtin_amdgcn_sched_barrier(0);
-            }
-            auto pass = [&](const f32x16& m, const f32x16& d, int slot) {
-                f32x16 x;
+                auto pass = [&](const f32x16& m, const f32x16& d, int slot) {
+                    f32x16 x;
 #pragma unroll
-                for (int r = 0; r < 16; ++r) x[r] = m[r] * d[r];
+                    for (int r = 0; r < 16; ++r) x[r] = m[r] * d[r];
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
+                        const Formed f = Ty::form(half_of(x, s));
+                        u32x4 q[2];
+                        __builtin_memcpy(q, &f, 32);
+                        lds_u32x4* to = reinterpret_cast<lds_u32x4*>(lds + Ld::M + (2 * slot + s) * 2048) + lane;
+                        to[0] = q[0];
+                        to[64] = q[1];
+                    }
+                };
+                auto factors = [&](bool off) {
+                    f32x16 d;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const f32x4 x = tab[((hh * 2 + off) * 4 + q) * 64 + lane];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) d[4 * q + e] = x[e];
+                    }
+                    return d;
+                };
+                if (wave < 3) pass(ma, R == 1 ? d_a : factors(off_diag), wave);
+                if (NT != 256 && wave == 0) pass(mb, R == 1 ? d_b : factors(true), 2);
+                if (hh == 0) read_v();
+                __syncthreads();  // the scores visible; x1 and x3 read
+                if (!Ld::FULL && more) load(u + 1);
+                const float w0 = power(hh, REV ? max(n - 1 - c, 0) : c + 1) * a.out_scale;
+                const float w1 = power(hh, REV ? max(n - 33 - c, 0) : c + 33) * a.out_scale;
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    out[0][r] = hh == 0 ? acc[0][r] * w0 : __builtin_fmaf(acc[0][r], w0, out[0][r]);
+                    out[1][r] = hh == 0 ? acc[1][r] * w1 : __builtin_fmaf(acc[1][r], w1, out[1][r]);
+                }
+                auto formed = [&](int slot, int s) {
+                    const lds_u32x4* m = reinterpret_cast<const lds_u32x4*>(lds + Ld::M + (2 * slot + s) * 2048) + lane;
+                    const u32x4 q[2] = {m[0], m[64]};
+                    Formed f;
+                    __builtin_memcpy(&f, q, 32);
+                    return f;
+                };
 #pragma unroll
                 for (int s = 0; s < 2; ++s) {
-                    const Formed f = Ty::form(half_of(x, s));
-                    u32x4 q[2];
-                    __builtin_memcpy(q, &f, 32);
-                    lds_u32x4* to = reinterpret_cast<lds_u32x4*>(lds + Ld::M + (2 * slot + s) * 2048) + lane;
-                    to[0] = q[0];
-                    to[64] = q[1];
-                }
-            };
-            auto factors = [&](bool off) {
-                f32x16 d;
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const f32x4 x = tab[((hh * 2 + off) * 4 + q) * 64 + lane];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) d[4 * q + e] = x[e];
-                }
-                return d;
-            };
-            if (wave < 3) pass(ma, R == 1 ? d_a : factors(off_diag), wave);
-            if (NT != 256 && wave == 0) pass(mb, R == 1 ? d_b : factors(true), 2);
-            if (hh == 0) read_v();
-            __syncthreads();  // the scores visible; x1 and x3 read
-            if (!Ld::FULL && more) load(u + 1);
-            const float w0 = power(hh, REV ? max(n - 1 - c, 0) : c + 1) * a.out_scale;
-            const float w1 = power(hh, REV ? max(n - 33 - c, 0) : c + 33) * a.out_scale;
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                out[0][r] = hh == 0 ? acc[0][r] * w0 : __builtin_fmaf(acc[0][r], w0, out[0][r]);
-                out[1][r] = hh == 0 ? acc[1][r] * w1 : __builtin_fmaf(acc[1][r], w1, out[1][r]);
-            }
-            auto formed = [&](int slot, int s) {
-                const lds_u32x4* m = reinterpret_cast<const lds_u32x4*>(lds + Ld::M + (2 * slot + s) * 2048) + lane;
-                const u32x4 q[2] = {m[0], m[64]};
-                Formed f;
-                __builtin_memcpy(&f, q, 32);
-                return f;
-            };
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                const Formed f0 = formed(0, s), f1 = formed(1, s), fx = formed(2, s);
-                f32x16 &ax = out[REV ? 0 : 1], &ay = out[REV ? 1 : 0];
-                const Formed &gx = REV ? f0 : f1, &gy = REV ? f1 : f0;
-                const Op vx = v[REV ? s : 2 + s], vy = v[REV ? 2 + s : s];
-                ax = Ty::template part<0>(vx, gx, ax);
-                ay = Ty::template part<0>(vy, gy, ay);
-                ax = Ty::template part<0>(vy, fx, ax);
-                if constexpr (Ty::PARTS == 2) {
-                    ay = Ty::template part<1>(vy, gy, ay);
-                    ax = Ty::template part<1>(vx, gx, ax);
-                    ax = Ty::template part<1>(vy, fx, ax);
-                }
-            }
-            if (hh == R - 1) {
-                if (n < kC) {  // rows of padding are 0 whatever the state holds
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) {
-                        if (c >= n) out[0][r] = 0.0f;
-                        if (32 + c >= n) out[1][r] = 0.0f;
+                    const Formed f0 = formed(0, s), f1 = formed(1, s), fx = formed(2, s);
+                    f32x16 &ax = out[REV ? 0 : 1], &ay = out[REV ? 1 : 0];
+                    const Formed &gx = REV ? f0 : f1, &gy = REV ? f1 : f0;
+                    const Op vx = v[REV ? s : 2 + s], vy = v[REV ? 2 + s : s];
+                    ax = Ty::template part<0>(vx, gx, ax);
+                    ay = Ty::template part<0>(vy, gy, ay);
+                    ax = Ty::template part<0>(vy, fx, ax);
+                    if constexpr (Ty::PARTS == 2) {
+                        ay = Ty::template part<1>(vy, gy, ay);
+                        ax = Ty::template part<1>(vx, gx, ax);
+                        ax = Ty::template part<1>(vy, fx, ax);
                     }
                 }
-                put(t0, 0, out[0]);
-                put(t0, 1, out[1]);
+                if (hh == R - 1) {
+                    if (n < kC) {  // rows of padding are 0 whatever the state holds
+#pragma unroll
+                        for (int r = 0; r < 16; ++r) {
+                            if (c >= n) out[0][r] = 0.0f;
+                            if (32 + c >= n) out[1][r] = 0.0f;
+                        }
+                    }
+                    put(t0, 0, out[0]);
+                    put(t0, 1, out[1]);
+                }
             }
-        }
-        if (AGG || cu + 1 < nch || (R == 1 && a.final_state)) {
-            // the operands of step s + 1 are read and formed while those of step s multiply
-            const lds_f32* w0 = wt + hh * 128 + 8 * hf + (REV ? 0 : kC - n);
-            Op k[KT];
-            f32x8 w;
-            auto fetch = [&](int s) {
+            if (AGG || cu + 1 < nch || (R == 1 && a.final_state)) {
+                // the operands of step s + 1 are read and formed while those of step s multiply
+                const lds_f32* w0 = wt + hh * 128 + 8 * hf + (REV ? 0 : kC - n);
+                Op k[KT];
+                f32x8 w;
+                auto fetch = [&](int s) {
 #pragma unroll
-                for (int T = 0; T < KT; ++T) k[T] = Ty::template col8<KD>(x2, 16 * s, 32 * T);
+                    for (int T = 0; T < KT; ++T) k[T] = Ty::template col8<KD>(x2, 16 * s, 32 * T);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) w[e] = w0[16 * s + e];
-            };
-            Op rest{};
-            auto weighted = [&](int s) {
-                f32x8 x = Ty::widen(v[s]);
+                    for (int e = 0; e < 8; ++e) w[e] = w0[16 * s + e];
+                };
+                Op rest{};
+                auto weighted = [&](int s) {
+                    f32x8 x = Ty::widen(v[s]);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] *= w[e];
-                const Formed f = Ty::form(x);
-                if constexpr (BF16 && EXACT) rest = Ty::rest(x, f);
-                return f;
-            };
-            fetch(0);
-            const float m = n == kC ? full[hh].next() : expf(la[hh] * (float)n);  // at most one chunk is shorter
+                    for (int e = 0; e < 8; ++e) x[e] *= w[e];
+                    const Formed f = Ty::form(x);
+                    if constexpr (BF16 && EXACT) rest = Ty::rest(x, f);
+                    return f;
+                };
+                fetch(0);
+                const float m = n == kC ? full[hh].next() : expf(la[hh] * (float)n);  // at most one chunk is shorter
 #pragma unroll
-            for (int T = 0; T < KT; ++T)
+                for (int T = 0; T < KT; ++T)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) S[hh][T][r] *= m;
-            Formed wv = weighted(0);
+                    for (int r = 0; r < 16; ++r) S[hh][T][r] *= m;
+                Formed wv = weighted(0);
 #pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                Op kn[KT];
+                for (int s = 0; s < 4; ++s) {
+                    Op kn[KT];
 #pragma unroll
-                for (int T = 0; T < KT; ++T) kn[T] = k[T];
-                if (s < 3) fetch(s + 1);
+                    for (int T = 0; T < KT; ++T) kn[T] = k[T];
+                    if (s < 3) fetch(s + 1);
 #pragma unroll
-                for (int T = 0; T < KT; ++T) S[hh][T] = Ty::template part<0>(kn[T], wv, S[hh][T]);
-                const Op third = rest;
-                const Formed next = s < 3 ? weighted(s + 1) : wv;
-                if constexpr (Ty::PARTS == 2)
+                    for (int T = 0; T < KT; ++T) S[hh][T] = Ty::template part<0>(kn[T], wv, S[hh][T]);
+                    const Op third = rest;
+                    const Formed next = s < 3 ? weighted(s + 1) : wv;
+                    if constexpr (Ty::PARTS == 2)
 #pragma unroll
-                    for (int T = 0; T < KT; ++T) S[hh][T] = Ty::template part<1>(kn[T], wv, S[hh][T]);
-                if constexpr (BF16 && EXACT)
+                        for (int T = 0; T < KT; ++T) S[hh][T] = Ty::template part<1>(kn[T], wv, S[hh][T]);
+                    if constexpr (BF16 && EXACT)
 #pragma unroll
-                    for (int T = 0; T < KT; ++T) S[hh][T] = Ty::mma(kn[T], third, S[hh][T]);
-                wv = next;
-                __builtin_amdgcn_sched_barrier(0);
+                        for (int T = 0; T < KT; ++T) S[hh][T] = Ty::mma(kn[T], third, S[hh][T]);
+                    wv = next;
+                    __builtin_amdgcn_sched_barrier(0);
+                }
             }
-        }
-        if (more) stage(u + 1, !AGG && hh == R - 1);
+            if (more) stage(u + 1, !AGG && hh == R - 1);
         }
     }
 

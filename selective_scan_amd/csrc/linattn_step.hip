@@ -7,6 +7,9 @@
 // load issued before the first store; a wave's load covers whole rows of V values.
 // o is summed over the row groups through LDS, so the workgroup has a head's V values
 // and the norm needs no other launch.
+// Measured: B64 H24 K128 V64 bf16 with norm and gate 17.3 us a call (101 MB, 5.9 TB/s, the
+// state partly in the memory-side cache; a copy of that size reaches 5.5), B1 H16
+// K = V = 128 4.4 us (latency; the call's host side takes 9).
 #include "common.h"
 #include "launch.h"
 #include "linattn.h"
