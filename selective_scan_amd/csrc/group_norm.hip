@@ -21,7 +21,7 @@
 // 64 x 64 x 512 bf16 in 32 groups with SiLU 49-54 us (tiles: 18 + 31; 134 MB that have to
 // move, 27 us at a copy's rate, 201 MB moved); gradient of 32768 x 1536 bf16 in 24 groups
 // with gate 112 us a call (rows: 503 MB, 4.5 TB/s), of 8 x 1025 x 320 fp32 in 32 groups
-// 24 us (tiles: 11 + 11 + 4, each a launch of little work).
+// 20 us (tiles, two launches of little work each: latency).
 #include "common.h"
 #include "group_norm.h"
 #include "launch.h"
@@ -56,6 +56,15 @@ __device__ __forceinline__ void load(const void* p, size_t i, float (&x)[V]) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) x[k] = __uint_as_float(q[k]);
     }
+}
+
+// f(i, U) for i, i + U step, ... below end with U = N while N rows are left, then one by one:
+// f loads its U rows before it stores any (the compiler moves no load above a store to an
+// output that might be an input).
+template <int N, typename F>
+__device__ __forceinline__ void in_batches(int i, int end, int step, F f) {
+    for (; i + (N - 1) * step < end; i += N * step) f(i, std::integral_constant<int, N>{});
+    for (; i < end; i += step) f(i, std::integral_constant<int, 1>{});
 }
 
 template <bool BF16, int V>
@@ -580,11 +589,39 @@ __global__ void __launch_bounds__(kT) gn_bwd_sums(GroupNormBwdArgs a, Tiles t, f
     }
 }
 
+// dweight and dbias from n parts [n][2][C]: 16 of the 2 C sums per workgroup (a 64-byte line
+// of a part), sixteen lanes each.
+__device__ __forceinline__ void sum_parts(const float* __restrict__ part, int n, int C, unsigned wg, float* dweight,
+                                          float* dbias) {
+    __shared__ float s[16][17];
+    const int i = threadIdx.x & 15, r = threadIdx.x >> 4, e = wg * 16 + i;
+    float v = 0.0f;
+    if (e < 2 * C)
+#pragma unroll 8
+        for (int k = r; k < n; k += 16) v += part[(size_t)k * 2 * C + e];
+    s[r][i] = v;
+    __syncthreads();
+    if (r != 0 || e >= 2 * C) return;
+    for (int k = 1; k < 16; ++k) v += s[k][i];
+    if (e < C) {
+        if (dweight) dweight[e] = v;
+    } else if (dbias) {
+        dbias[e - C] = v;
+    }
+}
+
+// dx and dz; the workgroups behind the last sample's sum the n parts of dw and db (n = 0: none),
+// which saves a launch: 8 x 1025 x 320 fp32 takes 24 us on the GPU and not 27.
 template <bool BF16, int V, bool GATE>
-__global__ void __launch_bounds__(kT) gn_bwd_apply(GroupNormBwdArgs a, Tiles t, const float2* stat) {
+__global__ void __launch_bounds__(kT) gn_bwd_apply(GroupNormBwdArgs a, Tiles t, const float2* stat,
+                                                   const float* part, int n) {
     extern __shared__ float2 gs[];  // [groups of the tile]: mean of dn, mean of dn xhat
     const unsigned wg = folded(), sample = wg / t.tiles;
-    if (sample >= (unsigned)a.M) return;
+    if (sample >= (unsigned)a.M) {
+        const unsigned at = (wg - t.tiles * (unsigned)a.M) * gridDim.y + blockIdx.y;
+        if (n > 0 && at * 16 < 2 * (unsigned)a.C) sum_parts(part, n, a.C, at, a.dweight, a.dbias);
+        return;
+    }
     const int tile = wg % t.tiles, m = sample, split = blockIdx.y;
     const Place<V> p(t, a.S, a.C, tile, split);
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
@@ -611,22 +648,30 @@ __global__ void __launch_bounds__(kT) gn_bwd_apply(GroupNormBwdArgs a, Tiles t, 
         m1[v] = s.y;
     }
     const size_t base = (size_t)m * a.S * a.C + p.c0 + p.col;
-#pragma unroll 2
-    for (int i = p.s0 + p.row; i < p.s1; i += p.rl) {
-        float x[V], d[V], z[V];
-        load<BF16, V>(a.x, base + (size_t)i * a.C, x);
-        load<BF16, V>(a.dy, base + (size_t)i * a.C, d);
-        if constexpr (GATE) load<BF16, V>(a.z, base + (size_t)i * a.C, z);
+    in_batches<4>(p.s0 + p.row, p.s1, p.rl, [&](int i, auto n) {
+        constexpr int U = decltype(n)::value;
+        float x[U][V], d[U][V], z[U][V];
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const float xhat = (x[v] - c.mean[v]) * c.rstd[v];
-            const float u = __builtin_fmaf(xhat, c.w[v], c.b[v]);
-            const float dn = gate_du<GATE>(d[v], u, GATE ? z[v] : 0.0f, a.act, &z[v]) * c.w[v];
-            x[v] = c.rstd[v] * (dn - m0[v] - xhat * m1[v]);
+        for (int k = 0; k < U; ++k) {
+            const size_t e = base + (size_t)(i + k * p.rl) * a.C;
+            load<BF16, V>(a.x, e, x[k]);
+            load<BF16, V>(a.dy, e, d[k]);
+            if constexpr (GATE) load<BF16, V>(a.z, e, z[k]);
         }
-        store<BF16, V>(a.dx, base + (size_t)i * a.C, x);
-        if constexpr (GATE) store<BF16, V>(a.dz, base + (size_t)i * a.C, z);
-    }
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const size_t e = base + (size_t)(i + k * p.rl) * a.C;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const float xhat = (x[k][v] - c.mean[v]) * c.rstd[v];
+                const float u = __builtin_fmaf(xhat, c.w[v], c.b[v]);
+                const float dn = gate_du<GATE>(d[k][v], u, GATE ? z[k][v] : 0.0f, a.act, &z[k][v]) * c.w[v];
+                x[k][v] = c.rstd[v] * (dn - m0[v] - xhat * m1[v]);
+            }
+            store<BF16, V>(a.dx, e, x[k]);
+            if constexpr (GATE) store<BF16, V>(a.dz, e, z[k]);
+        }
+    });
 }
 
 // dw and db of a range of rows (sample and position), every lane on channels of its own;
@@ -664,25 +709,9 @@ __global__ void __launch_bounds__(kT) gn_bwd_affine(GroupNormBwdArgs a, long lon
     }
 }
 
-// dweight and dbias from n parts [n][2][C]: 16 of the 2 C sums per workgroup (a 64-byte line
-// of a part), sixteen lanes each.
 __global__ void __launch_bounds__(kT) gn_sum_parts(const float* __restrict__ part, int n, int C, float* dweight,
                                                    float* dbias) {
-    __shared__ float s[16][17];
-    const int i = threadIdx.x & 15, r = threadIdx.x >> 4, e = blockIdx.x * 16 + i;
-    float v = 0.0f;
-    if (e < 2 * C)
-#pragma unroll 8
-        for (int k = r; k < n; k += 16) v += part[(size_t)k * 2 * C + e];
-    s[r][i] = v;
-    __syncthreads();
-    if (r != 0 || e >= 2 * C) return;
-    for (int k = 1; k < 16; ++k) v += s[k][i];
-    if (e < C) {
-        if (dweight) dweight[e] = v;
-    } else if (dbias) {
-        dbias[e - C] = v;
-    }
+    sum_parts(part, n, C, blockIdx.x, dweight, dbias);
 }
 
 // ------------------------------------------------------------------ choices
@@ -769,6 +798,9 @@ Path bwd_path(int S, int C, int G, bool bf16) {
 // range's rows (6 or more bytes a channel and row).
 bool parts_by_range(const Tiles& t) { return t.rows >= 8; }
 
+// Workgroups that sum the parts of dw and db.
+int sum_groups(int C) { return (2 * C + 15) / 16; }
+
 int row_parts(long long rows) { return (int)std::min<long long>(kParts, std::max<long long>(1, (rows + 7) / 8)); }
 
 template <bool BF16, int V>
@@ -830,8 +862,11 @@ hipError_t tiles_bwd(const GroupNormBwdArgs& a, const Tiles& t, float* part, hip
     launch((gn_bwd_sums<BF16, V, GATE>), grid, dim3(kT), 0, st, a, t, stat, parts_by_range(t) ? part : nullptr);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    launch((gn_bwd_apply<BF16, V, GATE>), grid, dim3(kT), (uint32_t)(t.gt * sizeof(float2)), st, a, t, stat);
-    if ((e = hipGetLastError()) != hipSuccess || !part || parts_by_range(t)) return e;
+    const bool sums = part && parts_by_range(t);
+    const dim3 more = fold((long long)t.tiles * a.M + (sums ? (sum_groups(a.C) + t.splits - 1) / t.splits : 0), t.splits);
+    launch((gn_bwd_apply<BF16, V, GATE>), more, dim3(kT), (uint32_t)(t.gt * sizeof(float2)), st, a, t, stat, part,
+           sums ? a.M * t.splits : 0);
+    if ((e = hipGetLastError()) != hipSuccess || !part || sums) return e;
     const long long rows = (long long)a.M * a.S;
     const dim3 ga((unsigned)((a.C / V + kT - 1) / kT), (unsigned)row_parts(rows));
     launch((gn_bwd_affine<BF16, V, GATE>), ga, dim3(kT), 0, st, a, rows, a.C / a.G, part);
@@ -873,6 +908,7 @@ hipError_t launch_group_norm_bwd(const GroupNormBwdArgs& a, hipStream_t st) {
     const bool affine = a.dweight || a.dbias, gate = a.z != nullptr;
     float* part = nullptr;
     int n = 0;
+    bool summed = false;
     hipError_t e = hipSuccess;
     if (a.M > 0 && bwd_path(a.S, a.C, a.G, a.bf16) == kRows) {
         n = row_parts(a.M);
@@ -887,15 +923,16 @@ hipError_t launch_group_norm_bwd(const GroupNormBwdArgs& a, hipStream_t st) {
         const Tiles t = tiles_of(a.M, a.S, a.C, a.G, a.bf16, &V);
         if (affine) {
             part = reinterpret_cast<float*>(static_cast<char*>(a.ws) + stat_bytes(a.M, a.G, t));
-            n = parts_by_range(t) ? a.M * t.splits : row_parts((long long)a.M * a.S);
+            n = row_parts((long long)a.M * a.S);
+            summed = parts_by_range(t);
         }
         if (a.bf16 && V == 8) e = gate ? tiles_bwd<true, 8, true>(a, t, part, st) : tiles_bwd<true, 8, false>(a, t, part, st);
         else if (a.bf16) e = gate ? tiles_bwd<true, 1, true>(a, t, part, st) : tiles_bwd<true, 1, false>(a, t, part, st);
         else if (V == 4) e = gate ? tiles_bwd<false, 4, true>(a, t, part, st) : tiles_bwd<false, 4, false>(a, t, part, st);
         else e = gate ? tiles_bwd<false, 1, true>(a, t, part, st) : tiles_bwd<false, 1, false>(a, t, part, st);
     }
-    if (e != hipSuccess || !affine) return e;
-    launch(gn_sum_parts, dim3((unsigned)((2 * a.C + 15) / 16)), dim3(kT), 0, st, part, n, a.C, a.dweight, a.dbias);
+    if (e != hipSuccess || !affine || summed) return e;
+    launch(gn_sum_parts, dim3((unsigned)sum_groups(a.C)), dim3(kT), 0, st, part, n, a.C, a.dweight, a.dbias);
     return hipGetLastError();
 }
 
