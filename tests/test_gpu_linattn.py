@@ -403,3 +403,27 @@ def test_offsets_beyond_32_bits():
     assert float((d / (o2.float().abs() + o2.float().square().mean().sqrt())).max()) < 2.0 ** -6
     assert float((d > 0).float().mean()) < 0.05
     assert float((hf - hf2).norm() / hf.norm()) < 1e-6
+
+
+@pytest.mark.parametrize("L", [70, 500])
+@pytest.mark.parametrize("name", ["q", "k", "v"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_a_row_that_is_not_finite_leaves_the_chunks_before_it_and_the_other_rows_alone(L, name, bad):
+    B, H, t = 2, 3, L - 5
+    gen = torch.Generator(device=DEV).manual_seed(4)
+    x = dict(q=torch.randn((B, L, H, 64), generator=gen, device=DEV).to(BF16),
+             k=torch.randn((B, L, H, 64), generator=gen, device=DEV).to(BF16),
+             v=torch.randn((B, L, H, 64), generator=gen, device=DEV).to(BF16))
+    a = torch.tensor([0.0, -0.05, -1.0], device=DEV)
+    want, hw = ssa.ssm_linattn_fwd(**x, log_decay=a)
+    x[name][1, t, 2] = bad
+    got, hg = ssa.ssm_linattn_fwd(**x, log_decay=a)
+    before = t // 64 * 64
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1, :, :2], want[1, :, :2])
+    assert torch.equal(got[1, :before, 2], want[1, :before, 2])
+    assert not torch.isfinite(got[1, t, 2]).all()
+    assert torch.equal(hg[0], hw[0]) and torch.equal(hg[1, :2], hw[1, :2])
+    if name == "q":
+        assert torch.equal(hg, hw)
+    else:
+        assert not torch.isfinite(hg[1, 2]).all()
