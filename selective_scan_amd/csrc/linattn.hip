@@ -327,9 +327,12 @@ struct Rows {
         for (int k = 0; k < N; ++k) {
             const int rr = tid / P + k * (NT / P);
             const uint32_t off = (uint32_t)rr * row + (((tid % P) ^ Ti::swz(rr)) << 4);
-            uint32_t m0;  // the LDS address goes through m0, which is left as it was
-            asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\tbuffer_load_dwordx4 %2, %3, 0 offen lds\n\t"
-                         "s_mov_b32 m0, %0"
+            // The LDS address goes through m0, which is left as it was. A load into LDS may come no
+            // sooner than one wait state after a scalar write of m0, which the compiler sees to
+            // only outside asm: hence the s_nop.
+            uint32_t m0;
+            asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\t"
+                         "buffer_load_dwordx4 %2, %3, 0 offen lds\n\ts_mov_b32 m0, %0"
                          : "=&s"(m0)
                          : "s"(to + k * NT * 16), "v"(off), "s"(r)
                          : "memory");
