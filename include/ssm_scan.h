@@ -345,7 +345,7 @@ int ssm_scan_bwd(int B, int L, int D, int N, ssm_dtype_t io,
  *             by 32 rows, so a chunk that is not a multiple of 32 costs the work
  *             of the next multiple.
  * Supported: io = SSM_BF16; N in {64, 128}; P = 64; B, H <= 65535;
- * B * H <= 2^24; L * H * P * 2 < 2^31.
+ * B * H < 2^23 (512 lanes each, in one grid dimension); L * H * P * 2 < 2^31.
  * ------------------------------------------------------------------------- */
 size_t ssm_ssd_workspace_size(int B, int L, int H, int P, int N, int chunk);
 
