@@ -577,11 +577,17 @@ int ssm_group_norm_bwd(int M, int S, int C, int G, ssm_dtype_t io, ssm_act_t act
  *   kernel that only reads and writes an array of the decode state's size reaches.
  * ssm_diag_copy: dst[i] = src[i] (n a multiple of 4): the byte reference that
  *   scales HBM byte counters.
- * Pointers are device pointers, 16-byte aligned. Errors as for the entry points.
+ * ssm_diag_linattn_plan: how ssm_linattn_fwd (gradient = 0) or ssm_linattn_bwd
+ *   (gradient = 1) cuts a sequence; no GPU call. plan[0] chunks of 64 steps,
+ *   plan[1] super-chunks of plan[2] chunks each (one workgroup each), plan[3] pieces
+ *   of plan[4] chunks each that what a super-chunk adds to the state is formed in,
+ *   plan[5] heads that share a workgroup in dq and dk.
+ * Pointers are device pointers (but for plan), 16-byte aligned. Errors as for the entry points.
  * ------------------------------------------------------------------------- */
 int ssm_diag_valu_rate(int mode, int blocks, int iters, float* out, void* stream);
 int ssm_diag_stream_scale(float* p, size_t n, float s, void* stream);
 int ssm_diag_copy(const float* src, float* dst, size_t n, void* stream);
+int ssm_diag_linattn_plan(int B, int L, int H, int G, int K, int V, ssm_dtype_t io, int gradient, int plan[6]);
 
 #ifdef __cplusplus
 }

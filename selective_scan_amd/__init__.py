@@ -12,6 +12,7 @@ from .ops import (  # noqa: F401
     SsmError,
     lib,
     ssm_diag_copy,
+    ssm_diag_linattn_plan,
     ssm_diag_stream_scale,
     ssm_diag_valu_rate,
     ssm_group_norm_bwd,

@@ -656,4 +656,13 @@ int ssm_diag_copy(const float* src, float* dst, size_t n, void* stream) {
     return hip_status(ssm::launch_copy(src, dst, n, static_cast<hipStream_t>(stream)), fn);
 }
 
+int ssm_diag_linattn_plan(int B, int L, int H, int G, int K, int V, ssm_dtype_t io, int gradient, int plan[6]) {
+    const char* fn = "ssm_diag_linattn_plan";
+    const int s = linattn_dims(fn, B, L, H, G, K, V, io);
+    if (s != SSM_OK) return s;
+    if (!plan) return fail(SSM_ERR_INVALID_ARG, fn, "plan is NULL");
+    ssm::linattn_plan(B, L, H, G, K, V, io == SSM_BF16, gradient != 0, plan);
+    return ok();
+}
+
 }  // extern "C"

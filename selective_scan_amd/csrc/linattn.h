@@ -82,6 +82,8 @@ struct LinattnStepArgs {
 };
 
 bool linattn_supported_dim(int d);
+// chunks, super-chunks, chunks of one, pieces, chunks of one, heads that share a workgroup
+void linattn_plan(int B, int L, int H, int G, int K, int V, bool bf16, bool bwd, int plan[6]);
 size_t linattn_workspace_bytes(int B, int L, int H, int G, int K, int V, bool bf16);
 size_t linattn_bwd_workspace_bytes(int B, int L, int H, int G, int K, int V, bool bf16);
 hipError_t launch_linattn_fwd(const LinattnArgs& a, hipStream_t stream);

@@ -907,6 +907,12 @@ size_t slot_bytes(int B, int H, int K, int V, const Geom& g) { return (size_t)B 
 
 bool linattn_supported_dim(int d) { return d == 64 || d == 128; }
 
+void linattn_plan(int B, int L, int H, int G, int K, int V, bool bf16, bool bwd, int plan[6]) {
+    const Geom g = geom(B, L, H, G, K, V, bf16, bwd);
+    const int p[6] = {g.NC, g.NS, g.cps, g.P, g.cpp, bwd && shared_heads(H / G, V, bf16) ? H / G : 1};
+    std::copy(p, p + 6, plan);
+}
+
 // entering states of the super-chunks
 size_t linattn_workspace_bytes(int B, int L, int H, int G, int K, int V, bool bf16) {
     return slot_bytes(B, H, K, V, geom(B, L, H, G, K, V, bf16, false));

@@ -80,6 +80,7 @@ def lib():
     L.ssm_group_norm_bwd.restype = i
     L.ssm_diag_valu_rate.argtypes, L.ssm_diag_valu_rate.restype = [i, i, i, vp, vp], i
     L.ssm_diag_stream_scale.argtypes, L.ssm_diag_stream_scale.restype = [vp, sz, ctypes.c_float, vp], i
+    L.ssm_diag_linattn_plan.argtypes, L.ssm_diag_linattn_plan.restype = [i] * 8 + [ctypes.POINTER(i)], i
     L.ssm_diag_copy.argtypes, L.ssm_diag_copy.restype = [vp, vp, sz, vp], i
     _lib = L
     return _lib
@@ -714,3 +715,13 @@ def ssm_diag_copy(src, dst, stream=None):
     st = lib().ssm_diag_copy(_ptr(src), _ptr(dst), src.numel(), _stream(src.device, stream))
     if st != SSM_OK:
         _raise("ssm_diag_copy", st)
+
+
+def ssm_diag_linattn_plan(B, L, H, G, K, V, io=SSM_BF16, gradient=False):
+    """How ``ssm_linattn_fwd`` or its gradient cuts a sequence: dict(chunks, supers, per_super,
+    pieces, per_piece, together); counts of 64-step chunks, see ``include/ssm_scan.h``."""
+    plan = (ctypes.c_int * 6)()
+    st = lib().ssm_diag_linattn_plan(B, L, H, G, K, V, io, int(gradient), plan)
+    if st != SSM_OK:
+        _raise("ssm_diag_linattn_plan", st)
+    return dict(zip(("chunks", "supers", "per_super", "pieces", "per_piece", "together"), plan))

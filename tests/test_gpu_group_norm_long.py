@@ -50,3 +50,23 @@ def test_statistics_over_many_positions(S, C, G, dtype, rl, first, offset):
         xh = (t - mean[m].double().cpu()[:, None]) * rstd[m].double().cpu()[:, None]
         lim = torch.finfo(dtype).eps / 2 * xh.abs() + 4 * U * (t.abs() + want.abs()[:, None]) * r[:, None] + 1e-30
         assert bool(((y[m].double().cpu().reshape(S, G, cg) - xh).abs() <= 1.01 * lim).all()), f"y of sample {m}"
+
+
+@pytest.mark.parametrize("M,S,C,G", [((1 << 22) + 5, 8, 32, 2), ((1 << 22) + 5, 9, 9, 3), (70000, 40, 64, 8),
+                                     (3, 100001, 24, 4), ((1 << 22) + 5, 1, 64, 1)])
+def test_sums_over_many_samples_are_exact(M, S, C, G):
+    """dweight and dbias where the workgroups that add up their parts come behind more samples than one
+    grid dimension takes, and on the ways beside it. Small whole numbers, statistics 0 and 1: every
+    product and every partial sum (far below 2^24) is exact in 32 bits, and so are the results."""
+    gen = torch.Generator(device=DEV).manual_seed(7)
+    x, dy = (torch.randint(-2, 3, (M, S, C), generator=gen, device=DEV, dtype=torch.int8) for _ in range(2))
+    mean, rstd = torch.zeros((M, G), device=DEV), torch.ones((M, G), device=DEV)
+    g = ssa.ssm_group_norm_bwd(x.to(BF16), G, mean, rstd, dy.to(BF16))
+    torch.cuda.synchronize()
+    db, dw = (torch.zeros(C, dtype=torch.int64, device=DEV) for _ in range(2))
+    for a in range(0, M, 1 << 18):
+        p, q = x[a:a + (1 << 18)].reshape(-1, C), dy[a:a + (1 << 18)].reshape(-1, C)
+        db += q.sum(0, dtype=torch.int64)
+        dw += (p * q).sum(0, dtype=torch.int64)
+    assert float(max(db.abs().max(), dw.abs().max())) < 2 ** 22
+    assert torch.equal(g["dbias"].double(), db.double()) and torch.equal(g["dweight"].double(), dw.double())
