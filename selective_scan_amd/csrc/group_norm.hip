@@ -18,7 +18,7 @@
 //           is read twice, the second time largely from the cache behind the L2s.
 // Rows whose channels are not whole 16-byte pieces are taken value by value.
 // Measured: 64 x 2048 bf16 in 16 groups with gate 3.5 us (rows; latency); 16 samples of
-// 64 x 64 x 512 bf16 in 32 groups with SiLU 49-54 us (tiles: 18 + 31; 134 MB that have to
+// 64 x 64 x 512 bf16 in 32 groups with SiLU 50-55 us (tiles: 20 + 31; 134 MB that have to
 // move, 27 us at a copy's rate, 201 MB moved); gradient of 32768 x 1536 bf16 in 24 groups
 // with gate 112 us a call (rows: 503 MB, 4.5 TB/s), of 8 x 1025 x 320 fp32 in 32 groups
 // 20 us (tiles, two launches of little work each: latency).
@@ -384,7 +384,8 @@ struct Place {
 // row of the data would lose digits for all rows far from that row (a border of zeros, one large
 // position). The running mean is kept in 64 bits, 3 of some 40 operations a batch: 2000 merges
 // rounded to 32 leave it 4e-6 of the spread off and the variance 5e-7, 64 bits 4e-8 and 2e-7
-// (16384 x 33 fp32, a zero row before 300 +- 1).
+// (16384 x 33 fp32, a zero row before 300 +- 1). 16 x 4096 x 512 bf16: 19.6 us, where the
+// distances to one row alone take 18.7.
 template <bool BF16, int V>
 __global__ void __launch_bounds__(kT) gn_stats(GroupNormArgs a, Tiles t, float2* stat) {
     __shared__ float sm[kT * V], sq[kT * V];
@@ -776,7 +777,7 @@ Tiles tiles_of(int M, int S, int C, int G, bool bf16, int* V) {
         *V = 1;
     }
     // three workgroups a CU, but at least eight rows a lane (16 samples of 64 x 64 x 512 bf16:
-    // 53 us with 512 workgroups, 49 with 768, 53 with 1024, 67 with 2048)
+    // 52 us with 512 workgroups, 49.5 with 768, 52 with 1024, 64 with 2048)
     const int rl = std::max(1, kT / (t.width / *V));
     const long want = std::max<long>(1, 768 / std::max<long>(1, (long)M * t.tiles));
     const long most = std::max<long>(1, (S + 8L * rl - 1) / (8L * rl));
@@ -806,8 +807,11 @@ Path bwd_path(int S, int C, int G, bool bf16) {
     return S == 1 && rows_shape(cg, V, 4, &T, &R) ? kRows : kTiles;
 }
 
-// Whether a part of dw and db per sample and range (8 bytes a channel) is small against the
-// range's rows (6 or more bytes a channel and row).
+// Whether gn_bwd_sums leaves dw and db in a part per sample and range (8 bytes a channel, against
+// 6 or more a channel and row of the range), or gn_bwd_affine reads x and dy again for 1024 parts
+// at most. M x S x C bf16, parts against reading again: 4096 x 8 x 64 53 us and 102, 4096 x 8 x 1024
+// 91 and 136, 262144 x 8 x 64 3.6 ms and 6.5, 4096 x 512 x 320 1.3 ms and 4.1. The parts grow with
+// M all the same; only short ranges of C taken value by value lose (16384 x 8 x 33: 113 and 94).
 bool parts_by_range(const Tiles& t) { return t.rows >= 8; }
 
 // Workgroups that sum the parts of dw and db.

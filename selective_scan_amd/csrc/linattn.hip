@@ -401,8 +401,9 @@ struct ChunkDecay {
 };
 
 // The tiles of a workgroup in LDS. Two buffers where they are filled while the other is
-// read: of x2, and, if full, of x1 and x3 as well; where two workgroups would not fit a CU
-// with that, x1 and x3 have one, filled once the chunk's scores and x1 S are done.
+// read: of x2, and, if full, of x1 and x3 as well, where that leaves as many workgroups on a
+// CU (two, of KD = 64 and VD = 128). Elsewhere it would be one of two, or, at 64 x 64, two of
+// three: x1 and x3 have one buffer, filled once the chunk's scores and x1 S are done.
 template <int KD, int VD, bool BF16, bool AGG, int R>
 struct Lds {
     static constexpr int BK = Tile<KD, BF16>::BYTES, BV = Tile<VD, BF16>::BYTES;
@@ -920,7 +921,7 @@ size_t linattn_workspace_bytes(int B, int L, int H, int G, int K, int V, bool bf
 
 // those of both directions, and fp32 dq and dk per head where heads share a group
 size_t linattn_bwd_workspace_bytes(int B, int L, int H, int G, int K, int V, bool bf16) {
-    return 2 * slot_bytes(B, H, K, V, geom(B, L, H, G, K, V, bf16, true)) + 
+    return 2 * slot_bytes(B, H, K, V, geom(B, L, H, G, K, V, bf16, true)) +
            (H == G || shared_heads(H / G, V, bf16) ? 0 : 2 * (size_t)B * L * H * K * 4);
 }
 
