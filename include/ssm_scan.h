@@ -18,6 +18,13 @@
  *   ssm_linattn_step its one-token decode step, optionally with the group norm and gate
  *   ssm_group_norm_fwd, ssm_group_norm_bwd
  *                    group norm, channels last, with activation and/or silu(z) gate
+ *   ssm_glr_fwd      gated linear recurrence: a decay per token and channel, one state a
+ *                    channel (prefill; padded batches)
+ *   ssm_glr_bwd      its gradient
+ *   ssm_glr_step     its one-token decode step
+ *   ssm_add_norm_fwd, ssm_add_norm_bwd
+ *                    residual add with dropout, then layer norm or RMS norm
+ *   ssm_dropout      dropout from a counter, forward and gradient
  *
  * The operation (selective SSM of Gu & Dao, "Mamba: Linear-Time Sequence
  * Modeling with Selective State Spaces", 2023, and the SSD form of Dao & Gu,
@@ -563,6 +570,179 @@ int ssm_group_norm_bwd(int M, int S, int C, int G, ssm_dtype_t io, ssm_act_t act
                        const float* mean, const float* rstd, const void* dy,
                        void* dx, float* dweight, float* dbias, void* dz,
                        void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * ssm_glr_fwd -- gated linear recurrence (prefill): a state per channel whose decay
+ * is gated by the input of every token. Per (b, d), from h = h0[b, d] (or 0), for
+ * t = 0 .. len_b - 1, with sigma the logistic function:
+ *   SSM_GLR_DECAY    a = exp(A[d] sigma(r[b,t,d])),  u = sqrt(1 - a^2) sigma(i[b,t,d]) x[b,t,d]
+ *                    (the real-gated linear recurrent unit of De et al., "Griffin", 2024;
+ *                    the factor keeps the state's variance that of the gated input)
+ *   SSM_GLR_CONVEX   a = 1 - sigma(r[b,t,d]),        u = sigma(r[b,t,d]) x[b,t,d]
+ *                    (the minimal gated unit of Feng et al., "Were RNNs all we needed?", 2024)
+ *   h = a h + u
+ *   y[b,t,d] = h * silu(z[b,t,d])
+ *   h_final[b, d] = h after step len_b - 1.
+ * Rows t >= len_b are padding: their inputs are not used, their y is 0.
+ *
+ *   x, r, i, z : [B, L, D]  io dtype, rows ld[0..3] elements apart (i: given exactly with
+ *                SSM_GLR_DECAY; z may be NULL: no gate)
+ *   A          : [D]        fp32, finite and <= 0 (SSM_GLR_DECAY; else NULL)
+ *   ld         : HOST array of the row strides of x, r, i, z in elements (slices of one
+ *                projection's rows; row t of batch b at (b L + t) ld), or NULL: D each. The
+ *                entry of an absent tensor is not read.
+ *   seqlens    : [B] int32 or NULL (every length L); a value outside [0, L] is taken as
+ *                the nearest of the two
+ *   h0         : [B, D]     fp32 or NULL (zeros)
+ *   y          : [B, L, D]  io dtype out
+ *   h_final    : [B, D]     fp32 out, or NULL
+ *   states     : [B, ceil(L / SSM_GLR_STATE_STEPS), D] fp32 out, or NULL: the state entering
+ *                every SSM_GLR_STATE_STEPS-th step, which ssm_glr_bwd takes
+ *   workspace  : at least ssm_glr_workspace_size(B, L, D) bytes, for one call at a time
+ * Arithmetic: fp32; 1 - a^2 by a series where a is close to 1.
+ * A value that is not finite stays in its channel and sequence, from its own step on.
+ * Supported: B <= 65535; L <= 2^30; D <= 2^18; ld in [D, 2^20]; B ceil(L / 128) ceil(D / 64)
+ * <= 2^30. x, r, i and z must be aligned to their element, every other pointer to 16 bytes.
+ * Outputs must not alias inputs or each other (the same address is refused). Errors as for
+ * ssm_scan_fwd.
+ * ------------------------------------------------------------------------- */
+#define SSM_GLR_STATE_STEPS 128
+typedef enum { SSM_GLR_DECAY = 0, SSM_GLR_CONVEX = 1, SSM_GLR_INT_RANGE_ = 0x7fffffff } ssm_glr_form_t;
+
+size_t ssm_glr_workspace_size(int B, int L, int D);
+
+int ssm_glr_fwd(int B, int L, int D, ssm_dtype_t io, ssm_glr_form_t form,
+                const void* x, const void* r, const void* i, const float* A, const void* z,
+                const int* ld, const int* seqlens, const float* h0,
+                void* y, float* h_final, float* states,
+                void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * ssm_glr_bwd -- gradient of ssm_glr_fwd.
+ *
+ * For the loss  l = sum(dy * y) + sum(dh_final * h_final)  every output is dl/d(the input of
+ * the same name). With g_t the gradient of h_t (from the right: g_t = dy_t silu(z_t) +
+ * a_{t+1} g_{t+1}, the last step's plus dh_final):
+ *   SSM_GLR_DECAY    m = sqrt(1 - a^2), s = sigma(r), q = sigma(i):
+ *                    dx = g m q,  di = g m x q (1 - q),  w = g (a h_{t-1} - a^2 q x / m),
+ *                    dr = w A s (1 - s),  dA = sum over b, t of w s
+ *                    (where m rounds to 0 the term with 1 / m is 0, its limit in dr)
+ *   SSM_GLR_CONVEX   k = sigma(r):  dx = g k,  dr = g (x - h_{t-1}) k (1 - k)
+ *   dz = dy h silu'(z),  dh0 = a_0 g_0.
+ *
+ *   inputs     : x, r, i, A, z, ld, seqlens as given to ssm_glr_fwd; states: its output
+ *   dy         : [B, L, D]  io dtype (rows t >= len_b are not used)
+ *   dh_final   : [B, D]     fp32 or NULL (zeros)
+ *   dx, dr, di, dz : [B, L, D] io dtype out, 0 at padding; di is given exactly when i is, dz
+ *                exactly when z is
+ *   dA         : [D]        fp32 out; given exactly when A is
+ *   dh0        : [B, D]     fp32 out, or NULL (not written)
+ *   workspace  : at least ssm_glr_bwd_workspace_size(B, L, D) bytes, for one call at a time
+ * Sums over b and t run in a fixed order. Sizes, alignment, aliasing and errors as for
+ * ssm_glr_fwd. L = 0 writes dh0 = dh_final and dA = 0.
+ * ------------------------------------------------------------------------- */
+size_t ssm_glr_bwd_workspace_size(int B, int L, int D);
+
+int ssm_glr_bwd(int B, int L, int D, ssm_dtype_t io, ssm_glr_form_t form,
+                const void* x, const void* r, const void* i, const float* A, const void* z,
+                const int* ld, const int* seqlens, const float* states,
+                const void* dy, const float* dh_final,
+                void* dx, void* dr, void* di, float* dA, void* dz, float* dh0,
+                void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * ssm_glr_step -- one-token decode step of ssm_glr_fwd, state in place.
+ *
+ *   state      : [B, D]  fp32, updated in place
+ *   x, r, i, z : [B, D]  io dtype, rows ld[0..3] elements apart (ld NULL: D each)
+ *   y          : [B, D]  io dtype out
+ * Supported: B * D <= 2^30. Sizes, alignment and errors otherwise as for ssm_glr_fwd; y and
+ * state must not alias each other or another argument.
+ * ------------------------------------------------------------------------- */
+int ssm_glr_step(int B, int D, ssm_dtype_t io, ssm_glr_form_t form,
+                 float* state, const void* x, const void* r, const void* i, const float* A,
+                 const void* z, const int* ld, void* y, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * ssm_add_norm_fwd -- what stands between two layers of a residual network: the last
+ * layer's output x is dropped out, added to the residual stream, and the sum normed for the
+ * next layer. Per row m, over its C channels:
+ *   s = residual + dropout(x)
+ *   SSM_NORM_LAYER   y = (s - mean) * rstd * weight + bias,  rstd = 1 / sqrt(var + eps) (biased)
+ *   SSM_NORM_RMS     y = s * rstd * weight + bias,           rstd = 1 / sqrt(mean of s^2 + eps)
+ *
+ *   x, y          : [M, C]  io dtype; y may be x
+ *   residual, sum : [M, C]  res dtype (SSM_F32, or that of io); residual may be NULL (zero);
+ *                   sum (s, rounded to res once; y is made from s before that) may be NULL
+ *                   (not written) or residual
+ *   weight, bias  : [C]     fp32, each may be NULL (ones, zeros)
+ *   mean, rstd    : [M]     fp32 out, each may be NULL; mean must be NULL with SSM_NORM_RMS
+ *   p, rng        : dropout probability and generator as for ssm_dropout (p = 0: none, rng
+ *                   may be NULL)
+ *   eps           : > 0
+ * Statistics are fp32, the variance from squared distances to the mean. Supported: 1 <= C <=
+ * 16384; M >= 0, M * C <= 2^38, M <= 2^30. Every pointer must be 16-byte aligned. But for y
+ * and x, sum and residual, outputs must not alias inputs or each other (the same address is
+ * refused). Errors as for ssm_scan_fwd.
+ * ------------------------------------------------------------------------- */
+typedef enum { SSM_NORM_LAYER = 0, SSM_NORM_RMS = 1, SSM_NORM_INT_RANGE_ = 0x7fffffff } ssm_norm_t;
+
+int ssm_add_norm_fwd(int M, int C, ssm_dtype_t io, ssm_dtype_t res, ssm_norm_t norm,
+                     const void* x, const void* residual, const float* weight, const float* bias,
+                     float eps, double p, const unsigned long long* rng,
+                     void* y, void* sum, float* mean, float* rstd, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * ssm_add_norm_bwd -- gradient of ssm_add_norm_fwd.
+ *
+ *   sum, mean, rstd : its outputs (x with res = io where there was neither residual nor
+ *                     dropout; mean NULL with SSM_NORM_RMS)
+ *   weight, p, rng  : as given to it
+ *   dy              : [M, C]  io dtype
+ *   dsum            : [M, C]  res dtype, what else the sum's gradient holds (the residual
+ *                     stream's from later layers), or NULL
+ *   dresidual       : [M, C]  res dtype out, or NULL: the gradient of s; may be dsum
+ *   dx              : [M, C]  io dtype out, or NULL: dropout of the gradient of s. One of the
+ *                     two is given at least.
+ *   dweight, dbias  : [C]     fp32 out, each may be NULL (not written); given or not whether
+ *                     weight and bias were
+ *   workspace       : at least ssm_add_norm_bwd_workspace_size(M, C, io, res) bytes, for one
+ *                     call at a time
+ * Sums over rows run in a fixed order. But for dresidual and dsum, outputs must not alias
+ * inputs or each other. M = 0 writes dweight = dbias = 0. Sizes and errors as for
+ * ssm_add_norm_fwd.
+ * ------------------------------------------------------------------------- */
+size_t ssm_add_norm_bwd_workspace_size(int M, int C, ssm_dtype_t io, ssm_dtype_t res);
+
+int ssm_add_norm_bwd(int M, int C, ssm_dtype_t io, ssm_dtype_t res, ssm_norm_t norm,
+                     const void* sum, const float* weight, const float* mean, const float* rstd,
+                     const void* dy, const void* dsum, double p, const unsigned long long* rng,
+                     void* dx, void* dresidual, float* dweight, float* dbias,
+                     void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * ssm_dropout -- dropout whose mask is drawn from a counter and never stored. The same call
+ * on dy with the same rng is its gradient.
+ *   y[m,c] = x[m,c] * scale where the element is kept, else 0
+ *
+ *   p        : in [0, 1); least = p * 65536 rounded to the nearest whole number (ties to even)
+ *              must be below 65536. An element is kept where its 16 bits are >= least, and
+ *              scale = 65536 / (65536 - least): the mean is exact for the rounded p.
+ *   rng      : DEVICE array {seed, offset}, read when the kernel runs, so that a captured graph
+ *              draws anew when the caller advances it; may be NULL where least = 0
+ *   The bits : row m's channels 8k .. 8k + 7 share block offset + m * ceil(C / 8) + k (mod 2^64),
+ *              whose number (low word first, then two zero words) is encrypted by Philox-4x32-10
+ *              (Salmon et al., "Parallel random numbers: as easy as 1, 2, 3", 2011) under the
+ *              seed's two words (low first); channel 8k + j takes half j % 2 (0: the low one) of
+ *              word j / 2. A call uses ssm_dropout_blocks(M, C) = M * ceil(C / 8) blocks: the
+ *              next offset is that much further.
+ *   x, y     : [M, C]  io dtype; y may be x
+ * Sizes as for ssm_add_norm_fwd but C <= 2^24; every pointer must be 16-byte aligned.
+ * ------------------------------------------------------------------------- */
+unsigned long long ssm_dropout_blocks(int M, int C);
+
+int ssm_dropout(int M, int C, ssm_dtype_t io, const void* x, double p, const unsigned long long* rng,
+                void* y, void* stream);
 
 /* ---------------------------------------------------------------------------
  * Diagnostics for benchmarks (not part of the method; asynchronous on `stream`,

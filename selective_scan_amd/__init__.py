@@ -11,10 +11,20 @@ module raises.
 from .ops import (  # noqa: F401
     SsmError,
     lib,
+    ssm_add_norm_bwd,
+    ssm_add_norm_bwd_workspace_size,
+    ssm_add_norm_fwd,
     ssm_diag_copy,
     ssm_diag_linattn_plan,
     ssm_diag_stream_scale,
     ssm_diag_valu_rate,
+    ssm_dropout,
+    ssm_dropout_blocks,
+    ssm_glr_bwd,
+    ssm_glr_bwd_workspace_size,
+    ssm_glr_fwd,
+    ssm_glr_step,
+    ssm_glr_workspace_size,
     ssm_group_norm_bwd,
     ssm_group_norm_bwd_workspace_size,
     ssm_group_norm_fwd,

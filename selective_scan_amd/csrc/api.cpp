@@ -5,13 +5,16 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstdint>
 #include <cstdio>
 #include <initializer_list>
 #include <limits>
 #include <string>
 
+#include "add_norm.h"
 #include "extras.h"
+#include "glr.h"
 #include "group_norm.h"
 #include "launch.h"
 #include "linattn.h"
@@ -482,6 +485,71 @@ bool group_norm_dims_ok(int M, int S, int C, int G, int io) {
            product_ok({M, S}, 1LL << 30) && product_ok({M, G}, 1LL << 30) && product_ok({M, S, C}, 1LL << 38);
 }
 
+// Sizes and inputs of the gated linear recurrence; SSM_OK with *in filled, or the failure.
+bool glr_dims_ok(int B, int L, int D) {
+    return B >= 1 && B <= 65535 && L >= 0 && L <= (1 << 30) && D >= 1 && D <= (1 << 18) &&
+           product_ok({B, ((long long)L + 127) / 128, (D + 63) / 64}, 1LL << 30);
+}
+
+int glr_inputs(const char* fn, int B, int L, int D, int io, int form, const void* x, const void* r, const void* i,
+               const float* A, const void* z, const int* ld, const int* seqlens, ssm::GlrIn* in) {
+    if (B < 1 || L < 0 || D < 1) return fail(SSM_ERR_INVALID_ARG, fn, "B, D must be >= 1 and L >= 0");
+    if (io != SSM_F32 && io != SSM_BF16) return fail(SSM_ERR_INVALID_ARG, fn, "io must be SSM_F32 or SSM_BF16");
+    if (form != SSM_GLR_DECAY && form != SSM_GLR_CONVEX)
+        return fail(SSM_ERR_INVALID_ARG, fn, "form must be SSM_GLR_DECAY or SSM_GLR_CONVEX");
+    if (B > 65535 || L > (1 << 30) || D > (1 << 18))
+        return fail(SSM_ERR_UNSUPPORTED, fn, "B must be <= 65535, L <= 2^30 and D <= 2^18");
+    if (!glr_dims_ok(B, L, D))
+        return fail(SSM_ERR_UNSUPPORTED, fn, "B * ceil(L / 128) * ceil(D / 64) must be <= 2^30");
+    if (L > 0 && (!x || !r)) return fail(SSM_ERR_INVALID_ARG, fn, "x and r are required");
+    if ((form == SSM_GLR_DECAY) != (A != nullptr))
+        return fail(SSM_ERR_INVALID_ARG, fn, "A must be given exactly with SSM_GLR_DECAY");
+    if (L > 0 && (form == SSM_GLR_DECAY) != (i != nullptr))
+        return fail(SSM_ERR_INVALID_ARG, fn, "i must be given exactly with SSM_GLR_DECAY");
+    const uintptr_t es = io == SSM_BF16 ? 2 : 4;
+    const void* rows[] = {x, r, i, z};
+    int strides[4] = {D, D, D, D};
+    for (int k = 0; k < 4; ++k) {
+        if (!rows[k]) continue;
+        if (reinterpret_cast<uintptr_t>(rows[k]) % es != 0)
+            return fail(SSM_ERR_INVALID_ARG, fn, "x, r, i and z must be aligned to their element");
+        if (!ld) continue;
+        if (ld[k] < D) return fail(SSM_ERR_INVALID_ARG, fn, "a row stride must be >= D");
+        if (ld[k] > (1 << 20)) return fail(SSM_ERR_UNSUPPORTED, fn, "a row stride must be <= 2^20");
+        strides[k] = ld[k];
+    }
+    if (!aligned16(A) || !aligned16(seqlens))
+        return fail(SSM_ERR_INVALID_ARG, fn, "every pointer but x, r, i and z must be 16-byte aligned");
+    for (int k : strides)
+        if (!product_ok({B, L, k}, 1LL << 40)) return fail(SSM_ERR_INVALID_ARG, fn, "tensor sizes overflow");
+    *in = ssm::GlrIn{B, L, D, io == SSM_BF16, form, x, r, i, A, z, strides[0], strides[1], strides[2], strides[3],
+                     seqlens};
+    return SSM_OK;
+}
+
+// Sizes and types of the residual add with norm; SSM_OK or the failure.
+int add_norm_dims(const char* fn, int M, int C, int io, int res, int norm) {
+    if (M < 0 || C < 1) return fail(SSM_ERR_INVALID_ARG, fn, "M must be >= 0 and C >= 1");
+    if (io != SSM_F32 && io != SSM_BF16) return fail(SSM_ERR_INVALID_ARG, fn, "io must be SSM_F32 or SSM_BF16");
+    if (res != SSM_F32 && res != io) return fail(SSM_ERR_INVALID_ARG, fn, "res must be SSM_F32 or that of io");
+    if (norm != SSM_NORM_LAYER && norm != SSM_NORM_RMS)
+        return fail(SSM_ERR_INVALID_ARG, fn, "norm must be SSM_NORM_LAYER or SSM_NORM_RMS");
+    if (C > 16384) return fail(SSM_ERR_UNSUPPORTED, fn, "C must be <= 16384");
+    if (M > (1 << 30)) return fail(SSM_ERR_UNSUPPORTED, fn, "M must be <= 2^30");
+    if (!product_ok({M, C}, 1LL << 38)) return fail(SSM_ERR_INVALID_ARG, fn, "tensor sizes overflow");
+    return SSM_OK;
+}
+
+int dropout_args(const char* fn, double p, const unsigned long long* rng, ssm::Dropout* d) {
+    if (!(p >= 0.0 && p < 1.0)) return fail(SSM_ERR_INVALID_ARG, fn, "p must be in [0, 1)");
+    const double least = std::nearbyint(p * 65536.0);
+    if (least > 65535.0) return fail(SSM_ERR_INVALID_ARG, fn, "p * 65536 must round to less than 65536");
+    if (least > 0.0 && !rng) return fail(SSM_ERR_INVALID_ARG, fn, "rng is required with p > 0");
+    if (!aligned16(rng)) return fail(SSM_ERR_INVALID_ARG, fn, "every pointer must be 16-byte aligned");
+    *d = ssm::Dropout{(unsigned)least, (float)(65536.0 / (65536.0 - least)), rng};
+    return SSM_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -631,6 +699,177 @@ int ssm_group_norm_bwd(int M, int S, int C, int G, ssm_dtype_t io, ssm_act_t act
     ssm::GroupNormBwdArgs a{M, S, C, G, io == SSM_BF16, act, x, weight, bias, z, mean, rstd, dy, dx, dweight, dbias,
                             dz, workspace};
     return hip_status(ssm::launch_group_norm_bwd(a, static_cast<hipStream_t>(stream)), fn);
+}
+
+// ------------------------------------------------------------------ gated linear recurrence
+size_t ssm_glr_workspace_size(int B, int L, int D) {
+    return glr_dims_ok(B, L, D) ? ssm::glr_workspace_bytes(B, L, D) : 0;
+}
+
+int ssm_glr_fwd(int B, int L, int D, ssm_dtype_t io, ssm_glr_form_t form,
+                const void* x, const void* r, const void* i, const float* A, const void* z,
+                const int* ld, const int* seqlens, const float* h0,
+                void* y, float* h_final, float* states,
+                void* workspace, size_t workspace_bytes, void* stream) {
+    const char* fn = "ssm_glr_fwd";
+    ssm::GlrArgs a{};
+    const int s = glr_inputs(fn, B, L, D, io, form, x, r, i, A, z, ld, seqlens, &a.in);
+    if (s != SSM_OK) return s;
+    if (L > 0 && !y) return fail(SSM_ERR_INVALID_ARG, fn, "y is required");
+    const void* ptrs[] = {h0, y, h_final, states, workspace};
+    for (const void* p : ptrs)
+        if (!aligned16(p))
+            return fail(SSM_ERR_INVALID_ARG, fn, "every pointer but x, r, i and z must be 16-byte aligned");
+    const size_t need = ssm::glr_workspace_bytes(B, L, D);
+    if (need > 0 && (workspace == nullptr || workspace_bytes < need))
+        return fail(SSM_ERR_WORKSPACE, fn, "workspace missing or smaller than ssm_glr_workspace_size()");
+    if (shared_buffer({y, h_final, states}, {x, r, i, A, z, seqlens, h0}))
+        return fail(SSM_ERR_INVALID_ARG, fn, "an output must not be an input or another output");
+    a.h0 = h0;
+    a.y = y;
+    a.h_final = h_final;
+    a.states = states;
+    a.ws = workspace;
+    return hip_status(ssm::launch_glr_fwd(a, static_cast<hipStream_t>(stream)), fn);
+}
+
+size_t ssm_glr_bwd_workspace_size(int B, int L, int D) {
+    return glr_dims_ok(B, L, D) ? ssm::glr_bwd_workspace_bytes(B, L, D) : 0;
+}
+
+int ssm_glr_bwd(int B, int L, int D, ssm_dtype_t io, ssm_glr_form_t form,
+                const void* x, const void* r, const void* i, const float* A, const void* z,
+                const int* ld, const int* seqlens, const float* states,
+                const void* dy, const float* dh_final,
+                void* dx, void* dr, void* di, float* dA, void* dz, float* dh0,
+                void* workspace, size_t workspace_bytes, void* stream) {
+    const char* fn = "ssm_glr_bwd";
+    ssm::GlrBwdArgs a{};
+    const int s = glr_inputs(fn, B, L, D, io, form, x, r, i, A, z, ld, seqlens, &a.in);
+    if (s != SSM_OK) return s;
+    if (L > 0 && (!states || !dy || !dx || !dr))
+        return fail(SSM_ERR_INVALID_ARG, fn, "states, dy, dx and dr are required");
+    if ((A != nullptr) != (dA != nullptr)) return fail(SSM_ERR_INVALID_ARG, fn, "dA must be given exactly when A is");
+    if (L > 0 && ((i != nullptr) != (di != nullptr) || (z != nullptr) != (dz != nullptr)))
+        return fail(SSM_ERR_INVALID_ARG, fn, "di must be given exactly when i is, dz exactly when z is");
+    const void* ptrs[] = {states, dy, dh_final, dx, dr, di, dA, dz, dh0, workspace};
+    for (const void* p : ptrs)
+        if (!aligned16(p))
+            return fail(SSM_ERR_INVALID_ARG, fn, "every pointer but x, r, i and z must be 16-byte aligned");
+    const size_t need = ssm::glr_bwd_workspace_bytes(B, L, D);
+    if (need > 0 && (workspace == nullptr || workspace_bytes < need))
+        return fail(SSM_ERR_WORKSPACE, fn, "workspace missing or smaller than ssm_glr_bwd_workspace_size()");
+    if (shared_buffer({dx, dr, di, dA, dz, dh0}, {x, r, i, A, z, seqlens, states, dy, dh_final}))
+        return fail(SSM_ERR_INVALID_ARG, fn, "an output must not be an input or another output");
+    a.states = states;
+    a.dy = dy;
+    a.dh_final = dh_final;
+    a.dx = dx;
+    a.dr = dr;
+    a.di = di;
+    a.dA = dA;
+    a.dz = dz;
+    a.dh0 = dh0;
+    a.ws = workspace;
+    return hip_status(ssm::launch_glr_bwd(a, static_cast<hipStream_t>(stream)), fn);
+}
+
+int ssm_glr_step(int B, int D, ssm_dtype_t io, ssm_glr_form_t form,
+                 float* state, const void* x, const void* r, const void* i, const float* A,
+                 const void* z, const int* ld, void* y, void* stream) {
+    const char* fn = "ssm_glr_step";
+    ssm::GlrStepArgs a{};
+    const int s = glr_inputs(fn, B, 1, D, io, form, x, r, i, A, z, ld, nullptr, &a.in);
+    if (s != SSM_OK) return s;
+    if (!state || !y) return fail(SSM_ERR_INVALID_ARG, fn, "state and y are required");
+    if (!product_ok({B, D}, 1LL << 30)) return fail(SSM_ERR_UNSUPPORTED, fn, "B * D must be <= 2^30");
+    if (!aligned16(state) || !aligned16(y))
+        return fail(SSM_ERR_INVALID_ARG, fn, "every pointer but x, r, i and z must be 16-byte aligned");
+    if (shared_buffer({state, y}, {x, r, i, A, z}))
+        return fail(SSM_ERR_INVALID_ARG, fn, "an output must not be an input or another output");
+    a.state = state;
+    a.y = y;
+    return hip_status(ssm::launch_glr_step(a, static_cast<hipStream_t>(stream)), fn);
+}
+
+// ------------------------------------------------------------------ residual add, norm, dropout
+int ssm_add_norm_fwd(int M, int C, ssm_dtype_t io, ssm_dtype_t res, ssm_norm_t norm,
+                     const void* x, const void* residual, const float* weight, const float* bias,
+                     float eps, double p, const unsigned long long* rng,
+                     void* y, void* sum, float* mean, float* rstd, void* stream) {
+    const char* fn = "ssm_add_norm_fwd";
+    int s = add_norm_dims(fn, M, C, io, res, norm);
+    if (s != SSM_OK) return s;
+    if (!(eps > 0.0f)) return fail(SSM_ERR_INVALID_ARG, fn, "eps must be > 0");
+    if (M > 0 && (!x || !y)) return fail(SSM_ERR_INVALID_ARG, fn, "x and y are required");
+    if (norm == SSM_NORM_RMS && mean) return fail(SSM_ERR_INVALID_ARG, fn, "mean must be NULL with SSM_NORM_RMS");
+    ssm::Dropout d;
+    if ((s = dropout_args(fn, p, rng, &d)) != SSM_OK) return s;
+    const void* ptrs[] = {x, residual, weight, bias, y, sum, mean, rstd};
+    for (const void* q : ptrs)
+        if (!aligned16(q)) return fail(SSM_ERR_INVALID_ARG, fn, "every pointer must be 16-byte aligned");
+    if (shared_buffer({y, sum, mean, rstd}, {weight, bias, rng}) || shared_buffer({y, mean, rstd}, {residual}) ||
+        shared_buffer({sum, mean, rstd}, {x}))
+        return fail(SSM_ERR_INVALID_ARG, fn, "an output must not be an input or another output");
+    ssm::AddNormArgs a{M, C, io == SSM_BF16, res == SSM_BF16, norm == SSM_NORM_RMS, x, residual, weight, bias, eps, d,
+                       y, sum, mean, rstd};
+    return hip_status(ssm::launch_add_norm_fwd(a, static_cast<hipStream_t>(stream)), fn);
+}
+
+size_t ssm_add_norm_bwd_workspace_size(int M, int C, ssm_dtype_t io, ssm_dtype_t res) {
+    if (M < 0 || M > (1 << 30) || C < 1 || C > 16384 || !product_ok({M, C}, 1LL << 38) ||
+        (io != SSM_F32 && io != SSM_BF16) || (res != SSM_F32 && res != io))
+        return 0;
+    return ssm::add_norm_bwd_workspace_bytes(M, C, io == SSM_BF16, res == SSM_BF16);
+}
+
+int ssm_add_norm_bwd(int M, int C, ssm_dtype_t io, ssm_dtype_t res, ssm_norm_t norm,
+                     const void* sum, const float* weight, const float* mean, const float* rstd,
+                     const void* dy, const void* dsum, double p, const unsigned long long* rng,
+                     void* dx, void* dresidual, float* dweight, float* dbias,
+                     void* workspace, size_t workspace_bytes, void* stream) {
+    const char* fn = "ssm_add_norm_bwd";
+    int s = add_norm_dims(fn, M, C, io, res, norm);
+    if (s != SSM_OK) return s;
+    if (M > 0 && (!sum || !rstd || !dy)) return fail(SSM_ERR_INVALID_ARG, fn, "sum, rstd and dy are required");
+    if (M > 0 && !dx && !dresidual) return fail(SSM_ERR_INVALID_ARG, fn, "dx or dresidual is required");
+    if (M > 0 && (norm == SSM_NORM_LAYER) != (mean != nullptr))
+        return fail(SSM_ERR_INVALID_ARG, fn, "mean must be given exactly with SSM_NORM_LAYER");
+    ssm::Dropout d;
+    if ((s = dropout_args(fn, p, rng, &d)) != SSM_OK) return s;
+    const void* ptrs[] = {sum, weight, mean, rstd, dy, dsum, dx, dresidual, dweight, dbias, workspace};
+    for (const void* q : ptrs)
+        if (!aligned16(q)) return fail(SSM_ERR_INVALID_ARG, fn, "every pointer must be 16-byte aligned");
+    const size_t need = ssm::add_norm_bwd_workspace_bytes(M, C, io == SSM_BF16, res == SSM_BF16);
+    if (need > 0 && (workspace == nullptr || workspace_bytes < need))
+        return fail(SSM_ERR_WORKSPACE, fn, "workspace missing or smaller than ssm_add_norm_bwd_workspace_size()");
+    if (shared_buffer({dx, dresidual, dweight, dbias}, {sum, weight, mean, rstd, dy, rng}) ||
+        shared_buffer({dx, dweight, dbias}, {dsum}))
+        return fail(SSM_ERR_INVALID_ARG, fn, "an output must not be an input or another output");
+    ssm::AddNormBwdArgs a{M, C, io == SSM_BF16, res == SSM_BF16, norm == SSM_NORM_RMS, sum, weight, mean, rstd, dy, dsum, d,
+                          dx, dresidual, dweight, dbias, workspace};
+    return hip_status(ssm::launch_add_norm_bwd(a, static_cast<hipStream_t>(stream)), fn);
+}
+
+unsigned long long ssm_dropout_blocks(int M, int C) {
+    return M < 0 || C < 1 ? 0 : (unsigned long long)M * (((unsigned)C + 7) / 8);
+}
+
+int ssm_dropout(int M, int C, ssm_dtype_t io, const void* x, double p, const unsigned long long* rng,
+                void* y, void* stream) {
+    const char* fn = "ssm_dropout";
+    if (M < 0 || C < 1) return fail(SSM_ERR_INVALID_ARG, fn, "M must be >= 0 and C >= 1");
+    if (io != SSM_F32 && io != SSM_BF16) return fail(SSM_ERR_INVALID_ARG, fn, "io must be SSM_F32 or SSM_BF16");
+    if (C > (1 << 24) || M > (1 << 30)) return fail(SSM_ERR_UNSUPPORTED, fn, "C must be <= 2^24 and M <= 2^30");
+    if (!product_ok({M, C}, 1LL << 38)) return fail(SSM_ERR_INVALID_ARG, fn, "tensor sizes overflow");
+    if (M > 0 && (!x || !y)) return fail(SSM_ERR_INVALID_ARG, fn, "x and y are required");
+    if (!aligned16(x) || !aligned16(y)) return fail(SSM_ERR_INVALID_ARG, fn, "every pointer must be 16-byte aligned");
+    ssm::Dropout d;
+    const int s = dropout_args(fn, p, rng, &d);
+    if (s != SSM_OK) return s;
+    if (shared_buffer({y}, {rng})) return fail(SSM_ERR_INVALID_ARG, fn, "an output must not be an input or another output");
+    ssm::DropoutArgs a{M, C, io == SSM_BF16, x, d, y};
+    return hip_status(ssm::launch_dropout(a, static_cast<hipStream_t>(stream)), fn);
 }
 
 // ------------------------------------------------------------------ diagnostics

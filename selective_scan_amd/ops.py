@@ -78,6 +78,23 @@ def lib():
     L.ssm_group_norm_bwd_workspace_size.argtypes, L.ssm_group_norm_bwd_workspace_size.restype = [i] * 5, sz
     L.ssm_group_norm_bwd.argtypes = [i] * 6 + [vp] * 11 + [vp, sz, vp]
     L.ssm_group_norm_bwd.restype = i
+    L.ssm_glr_workspace_size.argtypes, L.ssm_glr_workspace_size.restype = [i] * 3, sz
+    L.ssm_glr_fwd.argtypes = [i] * 5 + [vp] * 11 + [vp, sz, vp]
+    L.ssm_glr_fwd.restype = i
+    L.ssm_glr_bwd_workspace_size.argtypes, L.ssm_glr_bwd_workspace_size.restype = [i] * 3, sz
+    L.ssm_glr_bwd.argtypes = [i] * 5 + [vp] * 16 + [vp, sz, vp]
+    L.ssm_glr_bwd.restype = i
+    L.ssm_glr_step.argtypes = [i] * 4 + [vp] * 9
+    L.ssm_glr_step.restype = i
+    d = ctypes.c_double
+    L.ssm_add_norm_fwd.argtypes = [i] * 5 + [vp] * 4 + [f, d] + [vp] * 6
+    L.ssm_add_norm_fwd.restype = i
+    L.ssm_add_norm_bwd_workspace_size.argtypes, L.ssm_add_norm_bwd_workspace_size.restype = [i] * 4, sz
+    L.ssm_add_norm_bwd.argtypes = [i] * 5 + [vp] * 6 + [d] + [vp] * 5 + [vp, sz, vp]
+    L.ssm_add_norm_bwd.restype = i
+    L.ssm_dropout_blocks.argtypes, L.ssm_dropout_blocks.restype = [i, i], ctypes.c_ulonglong
+    L.ssm_dropout.argtypes = [i] * 3 + [vp, d] + [vp] * 3
+    L.ssm_dropout.restype = i
     L.ssm_diag_valu_rate.argtypes, L.ssm_diag_valu_rate.restype = [i, i, i, vp, vp], i
     L.ssm_diag_stream_scale.argtypes, L.ssm_diag_stream_scale.restype = [vp, sz, ctypes.c_float, vp], i
     L.ssm_diag_linattn_plan.argtypes, L.ssm_diag_linattn_plan.restype = [i] * 8 + [ctypes.POINTER(i)], i
@@ -686,6 +703,248 @@ def ssm_group_norm_bwd(x, groups, mean, rstd, dy, weight=None, bias=None, z=None
     if rc != SSM_OK:
         _raise("ssm_group_norm_bwd", rc)
     return g
+
+
+# ------------------------------------------------------------------ gated linear recurrence
+SSM_GLR_FORM = {"decay": 0, "convex": 1}
+SSM_GLR_STATE_STEPS = 128
+
+
+def _strided(t, name, shape, dtype, device, required=True):
+    """(address, row stride) of a tensor whose rows may be further apart than they are long (a
+    slice of a projection's output): [B, L, D] or [B, D] with neighbouring channels neighbours in
+    memory and every row as far from the next."""
+    D = shape[-1]
+    if t is None and not required:
+        return None, D
+    if type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and t.device == device:
+        if t.is_contiguous():
+            return t.data_ptr(), D
+        ld, rows, even = D, 1, D == 1 or t.stride(-1) == 1
+        for n, s in zip(reversed(shape[:-1]), reversed(t.stride()[:-1])):  # the inner rows first
+            if n > 1:
+                if rows == 1:
+                    ld = s
+                even, rows = even and s == ld * rows, rows * n
+        if even and ld >= D:
+            return t.data_ptr(), ld
+        if t.numel():
+            raise ValueError(f"{name} must have adjacent channels and evenly spaced rows, got strides {t.stride()}")
+    _check(t, name, shape, dtype, device, required)
+    return t.data_ptr(), D
+
+
+def _glr_inputs(x, r, i, A, z, form):
+    """(form code, io code, addresses of x, r, i, A, z and the row strides) after checks."""
+    form, code, dev, io, shape = SSM_GLR_FORM[form], _io_code(x), x.device, x.dtype, x.shape
+    if (form == 0) != (A is not None) or (form == 0) != (i is not None):
+        raise ValueError("i and A are given exactly with form 'decay'")
+    rows = [_strided(t, n, shape, io, dev, need) for t, n, need in
+            ((x, "x", True), (r, "r", True), (i, "i", form == 0), (z, "z", False))]
+    Ap = _fits(A, "A", shape[-1:], torch.float32, dev, form == 0)
+    (xp, lx), (rp, lr), (ip, li), (zp, lz) = rows
+    D = shape[-1]
+    ld = None if lx == lr == li == lz == D else (ctypes.c_int * 4)(lx, lr, li, lz)
+    return form, code, (xp, rp, ip, Ap, zp, ld)
+
+
+def ssm_glr_workspace_size(B, L, D):
+    return int(lib().ssm_glr_workspace_size(B, L, D))
+
+
+def ssm_glr_fwd(x, r, i=None, A=None, z=None, *, form="decay", seqlens=None, h0=None, y=None, h_final=None,
+                states=None, workspace=None, stream=None, want_final_state=True, want_states=False):
+    """Gated linear recurrence h_t = a_t h_{t-1} + u_t, y = h [silu(z)]. form "decay": a = exp(A
+    sigmoid(r)), u = sqrt(1 - a^2) sigmoid(i) x; "convex" (without i and A): a = 1 - sigmoid(r), u =
+    sigmoid(r) x. x, r, i, z: [B, L, D] bf16 or fp32, rows may be strided (slices of a projection);
+    A: [D] fp32, <= 0; seqlens: [B] int32, rows past a length are padding (y is 0 there); h0: [B, D]
+    fp32. Returns (y [B, L, D], h_final [B, D] fp32, states), the last with ``want_states``: the
+    state entering every 128th step, [B, ceil(L / 128), D] fp32, for ``ssm_glr_bwd``."""
+    if x.dim() != 3:
+        raise ValueError(f"x must be [B, L, D], got {tuple(x.shape)}")
+    B, L, D = x.shape
+    dev, io, f32 = x.device, x.dtype, torch.float32
+    form, code, p = _glr_inputs(x, r, i, A, z, form)
+    lens, h0p = _fits(seqlens, "seqlens", (B,), torch.int32, dev, False), _fits(h0, "h0", (B, D), f32, dev, False)
+    n = -(-L // SSM_GLR_STATE_STEPS)
+    need = lib().ssm_glr_workspace_size(B, L, D)
+    with _on(stream):
+        if y is None:
+            y = torch.empty((B, L, D), dtype=io, device=dev)
+        if want_final_state and h_final is None:
+            h_final = torch.empty((B, D), dtype=f32, device=dev)
+        if want_states and states is None:
+            states = torch.empty((B, n, D), dtype=f32, device=dev)
+        workspace, wp, wbytes = _space(need, workspace, dev)
+    out = (_fits(y, "y", (B, L, D), io, dev), _fits(h_final, "h_final", (B, D), f32, dev, False),
+           _fits(states, "states", (B, n, D), f32, dev, False))
+    with _Launch(dev, stream) as s:
+        rc = lib().ssm_glr_fwd(B, L, D, code, form, *p, lens, h0p, *out, wp, wbytes, s)
+    if rc != SSM_OK:
+        _raise("ssm_glr_fwd", rc)
+    return y, h_final, states
+
+
+def ssm_glr_bwd_workspace_size(B, L, D):
+    return int(lib().ssm_glr_bwd_workspace_size(B, L, D))
+
+
+def ssm_glr_bwd(x, r, states, dy, i=None, A=None, z=None, *, form="decay", seqlens=None, dh_final=None, want_dh0=True,
+                out=None, workspace=None, stream=None):
+    """Gradient of ``ssm_glr_fwd`` for l = sum(dy * y) + sum(dh_final * h_final), from its inputs
+    and the ``states`` it returned. dy: [B, L, D]; dh_final: [B, D] fp32 or None. Returns a dict
+    with dx, dr, di, dz [B, L, D] (0 at padding; di, dz None without i, z), dA [D] fp32 (None
+    without A) and dh0 [B, D] fp32 (None unless want_dh0). ``out`` may supply any of these."""
+    if x.dim() != 3:
+        raise ValueError(f"x must be [B, L, D], got {tuple(x.shape)}")
+    B, L, D = x.shape
+    dev, io, f32, shape = x.device, x.dtype, torch.float32, tuple(x.shape)
+    form, code, p = _glr_inputs(x, r, i, A, z, form)
+    lens = _fits(seqlens, "seqlens", (B,), torch.int32, dev, False)
+    ins = (_fits(states, "states", (B, -(-L // SSM_GLR_STATE_STEPS), D), f32, dev), _fits(dy, "dy", shape, io, dev),
+           _fits(dh_final, "dh_final", (B, D), f32, dev, False))
+    g, gp = dict(out or {}), []
+    need = lib().ssm_glr_bwd_workspace_size(B, L, D)
+    with _on(stream):
+        for n, sh, dt, wanted in (("dx", shape, io, True), ("dr", shape, io, True), ("di", shape, io, i is not None),
+                                  ("dA", (D,), f32, A is not None), ("dz", shape, io, z is not None),
+                                  ("dh0", (B, D), f32, want_dh0)):
+            if not wanted:
+                g[n] = None
+            elif g.get(n) is None:
+                g[n] = torch.empty(sh, dtype=dt, device=dev)
+            gp.append(_fits(g[n], n, sh, dt, dev, wanted))
+        workspace, wp, wbytes = _space(need, workspace, dev)
+    with _Launch(dev, stream) as s:
+        rc = lib().ssm_glr_bwd(B, L, D, code, form, *p, lens, *ins, *gp, wp, wbytes, s)
+    if rc != SSM_OK:
+        _raise("ssm_glr_bwd", rc)
+    return g
+
+
+def ssm_glr_step(state, x, r, i=None, A=None, z=None, *, form="decay", y=None, stream=None):
+    """One decode step of ``ssm_glr_fwd``. state: [B, D] fp32 (updated in place); x, r, i, z: [B, D],
+    rows may be strided; A: [D]. Returns y [B, D]."""
+    if x.dim() != 2:
+        raise ValueError(f"x must be [B, D], got {tuple(x.shape)}")
+    B, D = x.shape
+    dev, io = x.device, x.dtype
+    form, code, p = _glr_inputs(x, r, i, A, z, form)
+    sp = _fits(state, "state", (B, D), torch.float32, dev)
+    if y is None:
+        with _on(stream):
+            y = torch.empty((B, D), dtype=io, device=dev)
+    yp = _fits(y, "y", (B, D), io, dev)
+    with _Launch(dev, stream) as s:
+        rc = lib().ssm_glr_step(B, D, code, form, sp, *p, yp, s)
+    if rc != SSM_OK:
+        _raise("ssm_glr_step", rc)
+    return y
+
+
+# ------------------------------------------------------------------ residual add, norm, dropout
+SSM_NORM = {"layer": 0, "rms": 1}
+
+
+def _rows_dims(t, name):
+    """(M, C) of a tensor of rows [..., C]."""
+    if t.dim() < 1 or t.shape[-1] < 1:
+        raise ValueError(f"{name} must be [..., C], got shape {tuple(t.shape)}")
+    C = t.shape[-1]
+    return t.numel() // C, C
+
+
+def ssm_add_norm_fwd(x, residual=None, weight=None, bias=None, *, eps=1e-5, norm="layer", p=0.0, rng=None, y=None,
+                     sum=None, mean=None, rstd=None, want_sum=True, stream=None):
+    """s = residual + dropout(x), then y = norm(s) weight + bias over the last dimension: norm
+    "layer" ((s - mean) rstd) or "rms" (s rstd). x: [..., C] bf16 or fp32; residual: the same shape,
+    fp32 or x's type; weight, bias: [C] fp32; p, rng: as for ``ssm_dropout``. y may be x, sum may be
+    residual. Returns (y, sum, mean, rstd): sum in the residual's type (x itself where nothing is
+    added or dropped; None unless want_sum), mean (None for "rms") and rstd [...] fp32."""
+    M, C = _rows_dims(x, "x")
+    dev, io, f32, shape = x.device, x.dtype, torch.float32, x.shape
+    code, kind = _io_code(x), SSM_NORM[norm]
+    given = residual if residual is not None else sum
+    res = io if given is None else given.dtype
+    rcode = code if given is None else _io_code(given)
+    ins = (_fits(x, "x", shape, io, dev), _fits(residual, "residual", shape, res, dev, False),
+           _fits(weight, "weight", (C,), f32, dev, False), _fits(bias, "bias", (C,), f32, dev, False))
+    rp = _fits(rng, "rng", (2,), torch.int64, dev, p != 0.0)
+    same = sum is None and residual is None and p == 0.0
+    with _on(stream):
+        if y is None:
+            y = torch.empty(shape, dtype=io, device=dev)
+        if sum is None and want_sum and not same:
+            sum = torch.empty(shape, dtype=res, device=dev)
+        if mean is None and kind == 0:
+            mean = torch.empty(shape[:-1], dtype=f32, device=dev)
+        if rstd is None:
+            rstd = torch.empty(shape[:-1], dtype=f32, device=dev)
+    out = (_fits(y, "y", shape, io, dev), _fits(sum, "sum", shape, res, dev, False),
+           _fits(mean, "mean", shape[:-1], f32, dev, False), _fits(rstd, "rstd", shape[:-1], f32, dev))
+    with _Launch(dev, stream) as s:
+        rc = lib().ssm_add_norm_fwd(M, C, code, rcode, kind, *ins, eps, p, rp, *out, s)
+    if rc != SSM_OK:
+        _raise("ssm_add_norm_fwd", rc)
+    return y, (x if same and want_sum else sum), mean, rstd
+
+
+def ssm_add_norm_bwd_workspace_size(M, C, io=SSM_BF16, res=SSM_F32):
+    return int(lib().ssm_add_norm_bwd_workspace_size(M, C, io, res))
+
+
+def ssm_add_norm_bwd(sum, mean, rstd, dy, weight=None, dsum=None, *, norm="layer", p=0.0, rng=None, want_dx=True,
+                     want_dresidual=True, want_dweight=True, want_dbias=True, out=None, workspace=None, stream=None):
+    """Gradient of ``ssm_add_norm_fwd`` from the sum, mean and rstd it returned. dy: [..., C];
+    dsum: the gradient that the residual stream brings from later layers, in sum's type, or None.
+    Returns a dict with dx (dy's type), dresidual (sum's type; may be dsum), dweight and dbias [C]
+    fp32, None where not wanted. ``out`` may supply any of these tensors."""
+    M, C = _rows_dims(dy, "dy")
+    dev, io, f32, shape = dy.device, dy.dtype, torch.float32, dy.shape
+    code, kind, res, rcode = _io_code(dy), SSM_NORM[norm], sum.dtype, _io_code(sum)
+    ins = (_fits(sum, "sum", shape, res, dev), _fits(weight, "weight", (C,), f32, dev, False),
+           _fits(mean, "mean", shape[:-1], f32, dev, kind == 0), _fits(rstd, "rstd", shape[:-1], f32, dev),
+           _fits(dy, "dy", shape, io, dev), _fits(dsum, "dsum", shape, res, dev, False))
+    rp = _fits(rng, "rng", (2,), torch.int64, dev, p != 0.0)
+    g, gp = dict(out or {}), []
+    need = lib().ssm_add_norm_bwd_workspace_size(M, C, code, rcode)
+    with _on(stream):
+        for n, sh, dt, wanted in (("dx", shape, io, want_dx), ("dresidual", shape, res, want_dresidual),
+                                  ("dweight", (C,), f32, want_dweight), ("dbias", (C,), f32, want_dbias)):
+            if not wanted:
+                g[n] = None
+            elif g.get(n) is None:
+                g[n] = torch.empty(sh, dtype=dt, device=dev)
+            gp.append(_fits(g[n], n, sh, dt, dev, wanted))
+        workspace, wp, wbytes = _space(need, workspace, dev)
+    with _Launch(dev, stream) as s:
+        rc = lib().ssm_add_norm_bwd(M, C, code, rcode, kind, *ins, p, rp, *gp, wp, wbytes, s)
+    if rc != SSM_OK:
+        _raise("ssm_add_norm_bwd", rc)
+    return g
+
+
+def ssm_dropout_blocks(M, C):
+    """Counter values that dropout of [M, C] uses: the next call's offset is this much further."""
+    return int(lib().ssm_dropout_blocks(M, C))
+
+
+def ssm_dropout(x, p, rng=None, *, y=None, stream=None):
+    """Dropout of x [..., C] (bf16 or fp32) whose mask comes from a counter: each element is 0 with
+    probability p (a multiple of 2^-16), else scaled by 1 / (1 - p). rng: [2] int64 on x's device,
+    (seed, offset), read when the kernel runs. On dy with the same rng it is the gradient. y may be x."""
+    M, C = _rows_dims(x, "x")
+    dev, io, shape, code = x.device, x.dtype, x.shape, _io_code(x)
+    xp, rp = _fits(x, "x", shape, io, dev), _fits(rng, "rng", (2,), torch.int64, dev, p != 0.0)
+    if y is None:
+        with _on(stream):
+            y = torch.empty(shape, dtype=io, device=dev)
+    yp = _fits(y, "y", shape, io, dev)
+    with _Launch(dev, stream) as s:
+        rc = lib().ssm_dropout(M, C, code, xp, p, rp, yp, s)
+    if rc != SSM_OK:
+        _raise("ssm_dropout", rc)
+    return y
 
 
 # ------------------------------------------------------------------ diagnostics
