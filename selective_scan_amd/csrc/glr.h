@@ -69,7 +69,7 @@ struct Sigmoid {
     __device__ __forceinline__ explicit Sigmoid(float v) {
         const float e = exp2_fast(-v * kLog2e);
         s = rcp_fast(1.0f + e);
-        om = fminf(e, 8e37f) * s;
+        om = __builtin_fminf(e, 8e37f) * s;
     }
 };
 
@@ -81,7 +81,8 @@ __device__ __forceinline__ float one_minus_square(float t, float a) {
     q = __builtin_fmaf(t, q, 1.0f / 6.0f);
     q = __builtin_fmaf(t, q, 0.5f);
     q = __builtin_fmaf(t, q, 1.0f);
-    return t > -0.125f ? -t * q : __builtin_fmaf(-a, a, 1.0f);
+    const float series = -t * q, difference = __builtin_fmaf(-a, a, 1.0f);
+    return t > -0.125f ? series : difference;
 }
 
 // a and u of one element; FORM 0: A2 = A log2(e), At = 2 A.
@@ -100,15 +101,14 @@ __device__ __forceinline__ void glr_coefficients(float x, float r, float i, floa
 }
 
 // The gradient of one element from g, the state before it and its inputs; dl: what dA adds.
+// k: sigma(r), q: sigma(i).
 template <int FORM>
-__device__ __forceinline__ void glr_gradient(float g, float before, float x, float r, float i, float A, float A2,
-                                             float At, float* dx, float* dr, float* di, float* dl) {
-    const Sigmoid k(r);
+__device__ __forceinline__ void glr_gradient(float g, float before, float a, float x, const Sigmoid& k, const Sigmoid& q,
+                                             float A, float At, float* dx, float* dr, float* di, float* dl) {
     if constexpr (FORM == 0) {
-        const Sigmoid q(i);
-        const float a = exp2_fast(A2 * k.s), m2 = one_minus_square(At * k.s, a);
+        const float m2 = one_minus_square(At * k.s, a);
         // 1 / m; 0 where m is 0 (the limit of dr as the gate closes)
-        const float rm = m2 > kTiny ? __builtin_amdgcn_rsqf(m2) : 0.0f, gq = g * q.s, m = m2 * rm;
+        const float rs = __builtin_amdgcn_rsqf(m2), rm = m2 > kTiny ? rs : 0.0f, gq = g * q.s, m = m2 * rm;
         *dx = gq * m;
         *di = *dx * x * q.om;
         const float w = a * (g * before - a * rm * gq * x);  // d / d(A s)

@@ -47,18 +47,6 @@ struct Cut {
     float* part;      // [B][tiles][D]: dA's parts (gradient)
 };
 
-template <bool BF16>
-__device__ __forceinline__ float ld(const void* p, size_t i) {
-    if constexpr (BF16) return bf16_to_f32(static_cast<const uint16_t*>(p)[i]);
-    else return static_cast<const float*>(p)[i];
-}
-
-template <bool BF16>
-__device__ __forceinline__ void st(void* p, size_t i, float v) {
-    if constexpr (BF16) static_cast<uint16_t*>(p)[i] = f32_to_bf16(v);
-    else static_cast<float*>(p)[i] = v;
-}
-
 // a value's bits, never kAbsent
 __device__ __forceinline__ uint32_t present(float v) {
     const uint32_t b = __float_as_uint(v);
@@ -122,26 +110,110 @@ __device__ __forceinline__ bool take(const Cut& c, int* shared, unsigned* chain,
     return true;
 }
 
-// The rows of a wave's steps: where they start, how many are in the sequence and in the tensor.
+// How the lanes of a wave share its 16 steps of 64 channels: a lane has V neighbouring channels
+// (2 where rows hold whole pairs of bf16: one 32-bit access for both) and 16 / V steps, the lanes
+// of the wave's first half the earlier ones.
+template <int V>
+struct Share {
+    static constexpr int T = kSteps / V;
+    int late, d;  // whether the lane has the later steps; its first channel
+    __device__ __forceinline__ Share(int strip) {
+        const int lane = threadIdx.x & 63;
+        late = V == 1 ? 0 : lane >> 5;
+        d = strip * 64 + (V == 1 ? lane : 2 * (lane & 31));
+    }
+    // whether the lane has the first, or the last, of the wave's steps of its channels
+    __device__ __forceinline__ bool first() const { return V == 1 || !late; }
+    __device__ __forceinline__ bool last() const { return V == 1 || late; }
+    // The value of the lane with the other steps of the same channels.
+    __device__ __forceinline__ static float other(float v) { return __shfl_xor(v, 32); }
+};
+
+// A lane's elements of an io tensor's row as they are stored.
+template <bool BF16, int V>
+struct Raw {
+    uint32_t w;
+    __device__ __forceinline__ float operator[](int v) const {
+        if constexpr (!BF16) return __uint_as_float(w);
+        else return V == 2 && v == 1 ? bf16_hi(w) : bf16_lo(w);
+    }
+    // Forgets what was computed from the value: the compiler computes it again.
+    __device__ __forceinline__ void anew() { asm volatile("" : "+v"(w)); }
+};
+
+// A wave's rows of an io tensor through a buffer that ends behind the last of n rows: rows
+// further on read as 0 and are not written, and so does a lane whose channels do not exist (its
+// offset lies behind every buffer). One scalar addition a row.
+template <bool BF16, int V>
 struct Rows {
-    size_t first;
-    int live, stored;
-    __device__ __forceinline__ Rows(const GlrIn& in, int b, int t0) {
-        first = (size_t)b * in.L + t0;
-        live = min(max(glr_length(in.seqlens, b, in.L) - t0, 0), kSteps);
-        stored = min(max(in.L - t0, 0), kSteps);
+    static constexpr int T = Share<V>::T;
+    __amdgpu_buffer_rsrc_t buf;
+    uint32_t off, pitch;
+    __device__ __forceinline__ Rows(const void* p, int stride, int D, size_t first, int n, const Share<V>& me) {
+        constexpr uint32_t es = BF16 ? 2 : 4;
+        pitch = (uint32_t)stride * es;
+        // the same in every lane, said so that the buffer stays in scalar registers
+        const u64 at = (u64)p + (u64)first * pitch;
+        const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)at), hi = __builtin_amdgcn_readfirstlane((uint32_t)(at >> 32));
+        const uint32_t bytes = __builtin_amdgcn_readfirstlane(n > 0 ? (n - 1) * pitch + D * es : 0);
+        buf = make_rsrc(reinterpret_cast<const void*>((u64)hi << 32 | lo), bytes);
+        off = me.d < D ? (uint32_t)me.d * es + (me.late ? T * pitch : 0) : 0x80000000u;
+    }
+    __device__ __forceinline__ void load(Raw<BF16, V> (&v)[T]) const {
+#pragma unroll
+        for (int t = 0; t < T; ++t) {
+            if constexpr (BF16 && V == 1) v[t].w = __builtin_amdgcn_raw_buffer_load_b16(buf, (int)off, (int)(t * pitch), 0);
+            else v[t].w = __builtin_amdgcn_raw_buffer_load_b32(buf, (int)off, (int)(t * pitch), 0);
+        }
+    }
+    __device__ __forceinline__ void store(int t, const float (&v)[V]) const {
+        if constexpr (V == 2) {
+            const uint32_t w = f32_to_bf16(v[0]) | (uint32_t)f32_to_bf16(v[1]) << 16;
+            __builtin_amdgcn_raw_buffer_store_b32(w, buf, (int)off, (int)(t * pitch), 0);
+        } else {
+            store_io<BF16>(buf, off, t * pitch, v[0]);
+        }
     }
 };
 
-template <bool BF16>
-__device__ __forceinline__ void load_rows(const void* p, int stride, const Rows& rows, int d, float (&v)[kSteps]) {
+// Where a wave's steps are: the first one's row, and how many steps of the lane are in the
+// sequence (live) and how many rows of the wave in the sequence and in the tensor.
+template <int V>
+struct Steps {
+    size_t first;
+    int wave_live, wave_stored, live;
+    __device__ __forceinline__ Steps(const GlrIn& in, int b, int t0, const Share<V>& me) {
+        const int n = __builtin_amdgcn_readfirstlane(glr_length(in.seqlens, b, in.L));
+        first = (size_t)b * in.L + t0;
+        wave_live = min(max(n - t0, 0), kSteps);
+        wave_stored = min(max(in.L - t0, 0), kSteps);
+        live = wave_live - me.late * Share<V>::T;
+    }
+};
+
+// Keeps the compiler from computing more than a few steps side by side, whose intermediate
+// values would cost the registers of a workgroup a CU: computed() values exist at that place.
+__device__ __forceinline__ void few_at_once(int t) {
+    if (t % 2 == 1) __builtin_amdgcn_sched_barrier(0);
+}
+template <int V>
+__device__ __forceinline__ void computed(float (&v)[V]) {
 #pragma unroll
-    for (int t = 0; t < kSteps; ++t) v[t] = ld<BF16>(p, (rows.first + min(t, rows.live - 1)) * stride + d);
+    for (int k = 0; k < V; ++k) asm volatile("" : "+v"(v[k]));
+}
+
+// The state (or gradient) entering a tile: what enters its group, through the maps of the
+// tiles between, n of them.
+__device__ __forceinline__ float entering(const float (&start)[64], const float2 (&before)[kWaves][64], int n, int ch) {
+    float h = start[ch];
+    for (int q = 0; q * kPer < n; ++q) h = __builtin_fmaf(before[q][ch].x, h, before[q][ch].y);
+    return h;
 }
 
 // ------------------------------------------------------------------ forward
-template <bool BF16, int FORM, bool GATE>
-__global__ void __launch_bounds__(kThreads) glr_fwd_tiles(GlrArgs a, Cut c) {
+template <bool BF16, int V, int FORM, bool GATE>
+__global__ void __launch_bounds__(kThreads, 4) glr_fwd_tiles(GlrArgs a, Cut c) {
+    constexpr int T = Share<V>::T;
     __shared__ float2 own[kWaves][64], before[kWaves][64];
     __shared__ float start[64];
     __shared__ int shared;
@@ -149,44 +221,67 @@ __global__ void __launch_bounds__(kThreads) glr_fwd_tiles(GlrArgs a, Cut c) {
     unsigned chain;
     int tile;
     if (!take(c, &shared, &chain, &tile)) return;
-    const int b = (int)(chain / c.strips), lane = threadIdx.x & 63;
+    const int b = chain / c.strips, strip = chain % c.strips, lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int d = (int)(chain % c.strips) * 64 + lane, dc = min(d, in.D - 1);
-    const bool mine = d < in.D;
-    const Rows rows(in, b, tile * kTile + w * kSteps);
-    float ca[kSteps], cu[kSteps], z[kSteps];
-    float P = 1.0f, H = 0.0f;
-    if (rows.live > 0) {
-        float r[kSteps], i[kSteps];
-        load_rows<BF16>(in.x, in.ldx, rows, dc, cu);
-        load_rows<BF16>(in.r, in.ldr, rows, dc, r);
-        if constexpr (FORM == 0) load_rows<BF16>(in.i, in.ldi, rows, dc, i);
-        if constexpr (GATE) load_rows<BF16>(in.z, in.ldz, rows, dc, z);
-        const float A = FORM == 0 ? in.A[dc] : 0.0f, A2 = A * kLog2e, At = 2.0f * A;
+    const Share<V> me(strip);
+    const Steps<V> at(in, b, tile * kTile + w * kSteps, me);
+    const int ch = me.d - strip * 64;
+    const bool mine = me.d < in.D;
+    float ca[T][V], cu[T][V], P[V], H[V];
+    Raw<BF16, V> z[T];
+    {
+        Raw<BF16, V> x[T], r[T], i[T];
+        Rows<BF16, V>(in.x, in.ldx, in.D, at.first, at.wave_live, me).load(x);
+        Rows<BF16, V>(in.r, in.ldr, in.D, at.first, at.wave_live, me).load(r);
+        if constexpr (FORM == 0) Rows<BF16, V>(in.i, in.ldi, in.D, at.first, at.wave_live, me).load(i);
+        if constexpr (GATE) Rows<BF16, V>(in.z, in.ldz, in.D, at.first, at.wave_live, me).load(z);
+        float A[V];
 #pragma unroll
-        for (int t = 0; t < kSteps; ++t) {
-            glr_coefficients<FORM>(cu[t], r[t], FORM == 0 ? i[t] : 0.0f, A2, At, &ca[t], &cu[t]);
-            if (t >= rows.live) {
-                ca[t] = 1.0f;
-                cu[t] = 0.0f;
-            }
-            P *= ca[t];
-            H = __builtin_fmaf(ca[t], H, cu[t]);
-        }
-    } else {
+        for (int v = 0; v < V; ++v) A[v] = FORM == 0 ? in.A[min(me.d + v, in.D - 1)] : 0.0f;
 #pragma unroll
-        for (int t = 0; t < kSteps; ++t) {
-            ca[t] = 1.0f;
-            cu[t] = z[t] = 0.0f;
+        for (int t = 0; t < T; ++t) {
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                glr_coefficients<FORM>(x[t][v], r[t][v], FORM == 0 ? i[t][v] : 0.0f, A[v] * kLog2e, 2.0f * A[v], &ca[t][v],
+                                       &cu[t][v]);
+            computed(ca[t]);
+            computed(cu[t]);
+            few_at_once(t);
         }
     }
-    own[w][lane] = make_float2(P, H);
+    if (at.wave_live < kSteps)  // padding has u = 0 (x = 0); its state stays
+#pragma unroll
+        for (int t = 0; t < T; ++t)
+#pragma unroll
+            for (int v = 0; v < V; ++v) ca[t][v] = t >= at.live ? 1.0f : ca[t][v];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        P[v] = ca[0][v];
+        H[v] = cu[0][v];
+#pragma unroll
+        for (int t = 1; t < T; ++t) {
+            P[v] *= ca[t][v];
+            H[v] = __builtin_fmaf(ca[t][v], H[v], cu[t][v]);
+        }
+    }
+    float Po[V], Ho[V];  // of the lane with the other steps
+    if constexpr (V == 1) {
+        own[w][lane] = make_float2(P[0], H[0]);
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            Po[v] = me.other(P[v]);
+            Ho[v] = me.other(H[v]);
+            if (me.first()) own[w][ch + v] = make_float2(P[v] * Po[v], __builtin_fmaf(Po[v], H[v], Ho[v]));
+        }
+    }
     __syncthreads();
 
     const int group = tile / kGroup, first = group * kGroup;
+    const int dl = strip * 64 + lane, dc = min(dl, in.D - 1);  // a lane a channel
     if (c.tiles > 1) {
         const size_t slot = (size_t)b * c.tiles * in.D + dc;
-        if (w == kWaves - 1 && tile + 1 < c.tiles && mine) {
+        if (w == kWaves - 1 && tile + 1 < c.tiles && dl < in.D) {
             float p = 1.0f, h = 0.0f;
 #pragma unroll
             for (int q = 0; q < kWaves; ++q) {
@@ -204,28 +299,47 @@ __global__ void __launch_bounds__(kThreads) glr_fwd_tiles(GlrArgs a, Cut c) {
                                  : await_state(c.ends + ((size_t)b * c.groups + group - 1) * in.D + dc);
     __syncthreads();
 
-    float h = start[lane];
-    for (int q = 0; q * kPer < tile - first; ++q) h = __builtin_fmaf(before[q][lane].x, h, before[q][lane].y);
-    if (w == 0 && a.states && mine && rows.stored > 0)
-        a.states[((size_t)b * c.tiles + tile) * in.D + d] = h;
-    for (int q = 0; q < w; ++q) h = __builtin_fmaf(own[q][lane].x, h, own[q][lane].y);
-    if (w == kWaves - 1 && tile + 1 < c.tiles && tile + 1 == first + kGroup && mine)
-        __hip_atomic_store(c.ends + ((size_t)b * c.groups + group) * in.D + d, present(__builtin_fmaf(P, h, H)),
-                           __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    float h[V];
 #pragma unroll
-    for (int t = 0; t < kSteps; ++t) {
-        h = __builtin_fmaf(ca[t], h, cu[t]);
-        if (t < rows.stored && mine)
-            st<BF16>(a.y, (rows.first + t) * in.D + d, t >= rows.live ? 0.0f : GATE ? h * silu(z[t]) : h);
+    for (int v = 0; v < V; ++v) {
+        h[v] = entering(start, before, tile - first, ch + v);
+        if (w == 0 && a.states && mine && me.first() && at.wave_stored > 0)
+            a.states[((size_t)b * c.tiles + tile) * in.D + me.d + v] = h[v];
+        for (int q = 0; q < w; ++q) h[v] = __builtin_fmaf(own[q][ch + v].x, h[v], own[q][ch + v].y);
+        if constexpr (V == 2) h[v] = me.late ? __builtin_fmaf(Po[v], h[v], Ho[v]) : h[v];
+        if (w == kWaves - 1 && tile + 1 < c.tiles && tile + 1 == first + kGroup && mine && me.last())
+            __hip_atomic_store(c.ends + ((size_t)b * c.groups + group) * in.D + me.d + v,
+                               present(__builtin_fmaf(P[v], h[v], H[v])), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
-    if (a.h_final && tile + 1 == c.tiles && w == kWaves - 1 && mine) a.h_final[(size_t)b * in.D + d] = h;
+    const Rows<BF16, V> out(a.y, in.D, in.D, at.first, at.wave_stored, me);
+    auto sweep = [&](auto whole) {
+#pragma unroll
+        for (int t = 0; t < T; ++t) {
+            float y[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                h[v] = __builtin_fmaf(ca[t][v], h[v], cu[t][v]);
+                y[v] = GATE ? h[v] * silu(z[t][v]) : h[v];
+                if (!decltype(whole)::value) y[v] = t < at.live ? y[v] : 0.0f;
+            }
+            out.store(t, y);
+            few_at_once(t);
+        }
+    };
+    if (at.wave_live == kSteps) sweep(std::true_type{});
+    else sweep(std::false_type{});
+    if (a.h_final && tile + 1 == c.tiles && w == kWaves - 1 && mine && me.last())
+#pragma unroll
+        for (int v = 0; v < V; ++v) a.h_final[(size_t)b * in.D + me.d + v] = h[v];
 }
 
 // ------------------------------------------------------------------ gradient
-// Tiles are taken from the last to the first. own: P, H (forward) and C (what the wave's own dy
-// leaves for the step before it).
-template <bool BF16, int FORM, bool GATE>
-__global__ void __launch_bounds__(kThreads) glr_bwd_tiles(GlrBwdArgs a, Cut c) {
+// Tiles are taken from the last to the first. The map of a piece on the gradient leaving it at
+// its end to that at its start is g -> P g + C. The gates are computed twice: what a step needs
+// of them across the wait, held in registers, would cost the second workgroup of a CU.
+template <bool BF16, int V, int FORM, bool GATE>
+__global__ void __launch_bounds__(kThreads, 4) glr_bwd_tiles(GlrBwdArgs a, Cut c) {
+    constexpr int T = Share<V>::T;
     __shared__ float ownP[kWaves][64], ownH[kWaves][64], ownC[kWaves][64];
     __shared__ float2 after[kWaves][64];
     __shared__ float start[64];
@@ -235,43 +349,89 @@ __global__ void __launch_bounds__(kThreads) glr_bwd_tiles(GlrBwdArgs a, Cut c) {
     int k;
     if (!take(c, &shared, &chain, &k)) return;
     const int tile = c.tiles - 1 - k;
-    const int b = (int)(chain / c.strips), lane = threadIdx.x & 63;
+    const int b = chain / c.strips, strip = chain % c.strips, lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int d = (int)(chain % c.strips) * 64 + lane, dc = min(d, in.D - 1);
-    const bool mine = d < in.D;
-    const Rows rows(in, b, tile * kTile + w * kSteps);
-    float x[kSteps], r[kSteps], i[kSteps], z[kSteps], e[kSteps], ca[kSteps], cu[kSteps];
-    const float A = FORM == 0 ? in.A[dc] : 0.0f, A2 = A * kLog2e, At = 2.0f * A;
-    float P = 1.0f, H = 0.0f, C = 0.0f;
-    if (rows.live > 0) {
-        load_rows<BF16>(in.x, in.ldx, rows, dc, x);
-        load_rows<BF16>(in.r, in.ldr, rows, dc, r);
-        if constexpr (FORM == 0) load_rows<BF16>(in.i, in.ldi, rows, dc, i);
-        load_rows<BF16>(a.dy, in.D, rows, dc, e);
-        if constexpr (GATE) load_rows<BF16>(in.z, in.ldz, rows, dc, z);
+    const Share<V> me(strip);
+    const Steps<V> at(in, b, tile * kTile + w * kSteps, me);
+    const int ch = me.d - strip * 64;
+    const bool mine = me.d < in.D;
+    Raw<BF16, V> x[T], r[T], i[T];
+    float e[T][V], f[T][V], ca[T][V], cu[T][V], A[V], P[V], H[V], C[V];  // dz of a step is f h
+    {
+        Raw<BF16, V> dy[T], z[T];
+        Rows<BF16, V>(in.x, in.ldx, in.D, at.first, at.wave_live, me).load(x);
+        Rows<BF16, V>(in.r, in.ldr, in.D, at.first, at.wave_live, me).load(r);
+        if constexpr (FORM == 0) Rows<BF16, V>(in.i, in.ldi, in.D, at.first, at.wave_live, me).load(i);
+        Rows<BF16, V>(a.dy, in.D, in.D, at.first, at.wave_live, me).load(dy);
+        if constexpr (GATE) Rows<BF16, V>(in.z, in.ldz, in.D, at.first, at.wave_live, me).load(z);
 #pragma unroll
-        for (int t = 0; t < kSteps; ++t) {
-            glr_coefficients<FORM>(x[t], r[t], FORM == 0 ? i[t] : 0.0f, A2, At, &ca[t], &cu[t]);
-            if (t >= rows.live) {
-                ca[t] = 1.0f;
-                cu[t] = e[t] = 0.0f;
-                if constexpr (GATE) z[t] = 0.0f;
+        for (int v = 0; v < V; ++v) A[v] = FORM == 0 ? in.A[min(me.d + v, in.D - 1)] : 0.0f;
+#pragma unroll
+        for (int t = 0; t < T; ++t) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                glr_coefficients<FORM>(x[t][v], r[t][v], FORM == 0 ? i[t][v] : 0.0f, A[v] * kLog2e, 2.0f * A[v], &ca[t][v],
+                                       &cu[t][v]);
+                e[t][v] = dy[t][v];
+                if constexpr (GATE) {
+                    const Sigmoid s(z[t][v]);
+                    const float es = e[t][v] * s.s;
+                    e[t][v] = z[t][v] * es;
+                    f[t][v] = __builtin_fmaf(e[t][v], s.om, es);
+                }
             }
-            P *= ca[t];
-            H = __builtin_fmaf(ca[t], H, cu[t]);
+            computed(ca[t]);
+            computed(cu[t]);
+            if constexpr (GATE) {
+                computed(e[t]);
+                computed(f[t]);
+            }
+            few_at_once(t);
         }
-#pragma unroll
-        for (int t = kSteps - 1; t >= 0; --t) C = ca[t] * (C + (GATE ? e[t] * silu(z[t]) : e[t]));
     }
-    ownP[w][lane] = P;
-    ownH[w][lane] = H;
-    ownC[w][lane] = C;
+    if (at.wave_live < kSteps)  // padding has u = 0 and dy = 0; state and gradient stay
+#pragma unroll
+        for (int t = 0; t < T; ++t)
+#pragma unroll
+            for (int v = 0; v < V; ++v) ca[t][v] = t >= at.live ? 1.0f : ca[t][v];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        P[v] = ca[0][v];
+        H[v] = cu[0][v];
+#pragma unroll
+        for (int t = 1; t < T; ++t) {
+            P[v] *= ca[t][v];
+            H[v] = __builtin_fmaf(ca[t][v], H[v], cu[t][v]);
+        }
+        C[v] = 0.0f;
+#pragma unroll
+        for (int t = T - 1; t >= 0; --t) C[v] = ca[t][v] * (C[v] + e[t][v]);
+    }
+    float Po[V], Ho[V], Co[V];  // of the lane with the other steps
+    if constexpr (V == 1) {
+        ownP[w][lane] = P[0];
+        ownH[w][lane] = H[0];
+        ownC[w][lane] = C[0];
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            Po[v] = me.other(P[v]);
+            Ho[v] = me.other(H[v]);
+            Co[v] = me.other(C[v]);
+            if (me.first()) {
+                ownP[w][ch + v] = P[v] * Po[v];
+                ownH[w][ch + v] = __builtin_fmaf(Po[v], H[v], Ho[v]);
+                ownC[w][ch + v] = __builtin_fmaf(P[v], Co[v], C[v]);
+            }
+        }
+    }
     __syncthreads();
 
     const int group = k / kGroup, first = group * kGroup;
+    const int dl = strip * 64 + lane, dc = min(dl, in.D - 1);  // a lane a channel
     if (c.tiles > 1) {
         const size_t slot = (size_t)b * c.tiles * in.D + dc;
-        if (w == 0 && k + 1 < c.tiles && mine) {
+        if (w == 0 && k + 1 < c.tiles && dl < in.D) {
             float p = 1.0f, h = 0.0f;
 #pragma unroll
             for (int q = kWaves - 1; q >= 0; --q) {
@@ -286,67 +446,80 @@ __global__ void __launch_bounds__(kThreads) glr_bwd_tiles(GlrBwdArgs a, Cut c) {
     if (w == kWaves - 2)
         start[lane] = group == 0 ? (a.dh_final ? a.dh_final[(size_t)b * in.D + dc] : 0.0f)
                                  : await_state(c.ends + ((size_t)b * c.groups + group - 1) * in.D + dc);
-    float h = rows.live > 0 ? a.states[((size_t)b * c.tiles + tile) * in.D + dc] : 0.0f;
-    for (int q = 0; q < w; ++q) h = __builtin_fmaf(ownP[q][lane], h, ownH[q][lane]);
-    __syncthreads();
-
-    float g = start[lane];
-    for (int q = 0; q * kPer < k - first; ++q) g = __builtin_fmaf(after[q][lane].x, g, after[q][lane].y);
-    for (int q = kWaves - 1; q > w; --q) g = __builtin_fmaf(ownP[q][lane], g, ownC[q][lane]);
-    if (w == 0 && k + 1 < c.tiles && k + 1 == first + kGroup && mine)
-        __hip_atomic_store(c.ends + ((size_t)b * c.groups + group) * in.D + d, present(__builtin_fmaf(P, g, C)),
-                           __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    float dA = 0.0f;
-    if (rows.live > 0) {
-        // cu becomes the state before each step
+    // cu becomes the state before each step; dz needs the state alone
 #pragma unroll
-        for (int t = 0; t < kSteps; ++t) {
-            const float n = __builtin_fmaf(ca[t], h, cu[t]);
-            cu[t] = h;
+    for (int v = 0; v < V; ++v) {
+        float h = at.wave_live > 0 ? a.states[((size_t)b * c.tiles + tile) * in.D + min(me.d + v, in.D - 1)] : 0.0f;
+        for (int q = 0; q < w; ++q) h = __builtin_fmaf(ownP[q][ch + v], h, ownH[q][ch + v]);
+        if constexpr (V == 2) h = me.late ? __builtin_fmaf(Po[v], h, Ho[v]) : h;
+#pragma unroll
+        for (int t = 0; t < T; ++t) {
+            const float n = __builtin_fmaf(ca[t][v], h, cu[t][v]);
+            cu[t][v] = h;
             h = n;
-        }
-#pragma unroll
-        for (int t = kSteps - 1; t >= 0; --t) {
-            float dx, dr, di, dl, dz = 0.0f;
-            float dy = e[t];
-            if constexpr (GATE) {
-                const Sigmoid s(z[t]);
-                dz = dy * h * s.s * __builtin_fmaf(z[t], s.om, 1.0f);  // h: after the step
-                dy *= z[t] * s.s;
-            }
-            g += dy;
-            h = cu[t];
-            glr_gradient<FORM>(g, h, x[t], r[t], FORM == 0 ? i[t] : 0.0f, A, A2, At, &dx, &dr, &di, &dl);
-            g *= ca[t];
-            if (t >= rows.live) dx = dr = di = dl = dz = 0.0f;
-            dA += dl;
-            if (t < rows.stored && mine) {
-                const size_t o = (rows.first + t) * in.D + d;
-                st<BF16>(a.dx, o, dx);
-                st<BF16>(a.dr, o, dr);
-                if constexpr (FORM == 0) st<BF16>(a.di, o, di);
-                if constexpr (GATE) st<BF16>(a.dz, o, dz);
-            }
-        }
-    } else {
-        for (int t = 0; t < rows.stored; ++t) {
-            if (!mine) continue;
-            const size_t o = (rows.first + t) * in.D + d;
-            st<BF16>(a.dx, o, 0.0f);
-            st<BF16>(a.dr, o, 0.0f);
-            if constexpr (FORM == 0) st<BF16>(a.di, o, 0.0f);
-            if constexpr (GATE) st<BF16>(a.dz, o, 0.0f);
+            if constexpr (GATE) f[t][v] = at.wave_live == kSteps || t < at.live ? f[t][v] * h : 0.0f;
         }
     }
-    if (a.dh0 && tile == 0 && w == 0 && mine) a.dh0[(size_t)b * in.D + d] = g;
-    if constexpr (FORM == 0) {  // ownH was last read before the last barrier
-        ownH[w][lane] = dA;
-        __syncthreads();
-        if (w == 0 && mine) {
-            dA = 0.0f;
+    if constexpr (GATE) {
+        const Rows<BF16, V> oz(a.dz, in.D, in.D, at.first, at.wave_stored, me);
 #pragma unroll
-            for (int q = 0; q < kWaves; ++q) dA += ownH[q][lane];
-            c.part[((size_t)b * c.tiles + tile) * in.D + d] = dA;
+        for (int t = 0; t < T; ++t) oz.store(t, f[t]);
+    }
+    __syncthreads();
+
+    float g[V], dA[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        dA[v] = 0.0f;
+        g[v] = entering(start, after, k - first, ch + v);
+        for (int q = kWaves - 1; q > w; --q) g[v] = __builtin_fmaf(ownP[q][ch + v], g[v], ownC[q][ch + v]);
+        if constexpr (V == 2) g[v] = me.late ? g[v] : __builtin_fmaf(Po[v], g[v], Co[v]);
+        if (w == 0 && k + 1 < c.tiles && k + 1 == first + kGroup && mine && me.first())
+            __hip_atomic_store(c.ends + ((size_t)b * c.groups + group) * in.D + me.d + v,
+                               present(__builtin_fmaf(P[v], g[v], C[v])), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    const Rows<BF16, V> ox(a.dx, in.D, in.D, at.first, at.wave_stored, me), orr(a.dr, in.D, in.D, at.first, at.wave_stored, me);
+    const Rows<BF16, V> oi(FORM == 0 ? a.di : a.dx, in.D, in.D, at.first, at.wave_stored, me);
+    auto sweep = [&](auto whole) {
+#pragma unroll
+        for (int t = T - 1; t >= 0; --t) {
+            float dx[V], dr[V], di[V], dl;
+            x[t].anew();
+            r[t].anew();
+            if constexpr (FORM == 0) i[t].anew();
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const Sigmoid sr(r[t][v]);
+                g[v] += e[t][v];
+                glr_gradient<FORM>(g[v], cu[t][v], ca[t][v], x[t][v], sr, FORM == 0 ? Sigmoid(i[t][v]) : sr, A[v], 2.0f * A[v],
+                                   &dx[v], &dr[v], &di[v], &dl);
+                g[v] *= ca[t][v];
+                if (!decltype(whole)::value && t >= at.live) dx[v] = dr[v] = di[v] = dl = 0.0f;
+                dA[v] += dl;
+            }
+            ox.store(t, dx);
+            orr.store(t, dr);
+            if constexpr (FORM == 0) oi.store(t, di);
+            few_at_once(t);
+        }
+    };
+    if (at.wave_live == kSteps) sweep(std::true_type{});
+    else sweep(std::false_type{});
+    if (a.dh0 && tile == 0 && w == 0 && mine && me.first())
+#pragma unroll
+        for (int v = 0; v < V; ++v) a.dh0[(size_t)b * in.D + me.d + v] = g[v];
+    if constexpr (FORM == 0) {  // ownH was last read before the last barrier
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            if constexpr (V == 2) dA[v] += me.other(dA[v]);
+            if (me.first()) ownH[w][ch + v] = dA[v];
+        }
+        __syncthreads();
+        if (w == 0 && dl < in.D) {
+            float sum = 0.0f;
+#pragma unroll
+            for (int q = 0; q < kWaves; ++q) sum += ownH[q][lane];
+            c.part[((size_t)b * c.tiles + tile) * in.D + dl] = sum;
         }
     }
 }
@@ -403,18 +576,28 @@ hipError_t fill_words(void* ws, size_t bytes, hipStream_t s) {
     return hipGetLastError();
 }
 
-template <bool BF16, int FORM>
-void fwd(const GlrArgs& a, const Cut& c, hipStream_t s) {
-    const dim3 grid = fold((long long)c.chains * c.tiles);
-    if (a.in.z) launch((glr_fwd_tiles<BF16, FORM, true>), grid, dim3(kThreads), 0, s, a, c);
-    else launch((glr_fwd_tiles<BF16, FORM, false>), grid, dim3(kThreads), 0, s, a, c);
+// Whether every row of the tensor starts on a pair of bf16 and holds whole pairs.
+bool pairs(const GlrIn& in) {
+    const void* p[] = {in.x, in.r, in.i, in.z};
+    const int stride[] = {in.ldx, in.ldr, in.ldi, in.ldz};
+    if (!in.bf16 || in.D % 2 != 0) return false;
+    for (int k = 0; k < 4; ++k)
+        if (p[k] && (reinterpret_cast<uintptr_t>(p[k]) % 4 != 0 || stride[k] % 2 != 0)) return false;
+    return true;
 }
 
-template <bool BF16, int FORM>
+template <bool BF16, int V, int FORM>
+void fwd(const GlrArgs& a, const Cut& c, hipStream_t s) {
+    const dim3 grid = fold((long long)c.chains * c.tiles);
+    if (a.in.z) launch((glr_fwd_tiles<BF16, V, FORM, true>), grid, dim3(kThreads), 0, s, a, c);
+    else launch((glr_fwd_tiles<BF16, V, FORM, false>), grid, dim3(kThreads), 0, s, a, c);
+}
+
+template <bool BF16, int V, int FORM>
 void bwd(const GlrBwdArgs& a, const Cut& c, hipStream_t s) {
     const dim3 grid = fold((long long)c.chains * c.tiles);
-    if (a.in.z) launch((glr_bwd_tiles<BF16, FORM, true>), grid, dim3(kThreads), 0, s, a, c);
-    else launch((glr_bwd_tiles<BF16, FORM, false>), grid, dim3(kThreads), 0, s, a, c);
+    if (a.in.z) launch((glr_bwd_tiles<BF16, V, FORM, true>), grid, dim3(kThreads), 0, s, a, c);
+    else launch((glr_bwd_tiles<BF16, V, FORM, false>), grid, dim3(kThreads), 0, s, a, c);
 }
 
 }  // namespace
@@ -436,8 +619,9 @@ hipError_t launch_glr_fwd(const GlrArgs& a, hipStream_t s) {
     const Cut c = cut_of(a.in.B, a.in.L, a.in.D, static_cast<char*>(a.ws), &fill);
     const hipError_t e = fill_words(a.ws, fill, s);
     if (e != hipSuccess) return e;
-    if (a.in.bf16) a.in.form == 0 ? fwd<true, 0>(a, c, s) : fwd<true, 1>(a, c, s);
-    else a.in.form == 0 ? fwd<false, 0>(a, c, s) : fwd<false, 1>(a, c, s);
+    if (pairs(a.in)) a.in.form == 0 ? fwd<true, 2, 0>(a, c, s) : fwd<true, 2, 1>(a, c, s);
+    else if (a.in.bf16) a.in.form == 0 ? fwd<true, 1, 0>(a, c, s) : fwd<true, 1, 1>(a, c, s);
+    else a.in.form == 0 ? fwd<false, 1, 0>(a, c, s) : fwd<false, 1, 1>(a, c, s);
     return hipGetLastError();
 }
 
@@ -446,8 +630,9 @@ hipError_t launch_glr_bwd(const GlrBwdArgs& a, hipStream_t s) {
     const Cut c = cut_of(a.in.B, a.in.L, a.in.D, static_cast<char*>(a.ws), &fill);
     hipError_t e = fill_words(a.ws, fill, s);
     if (e != hipSuccess) return e;
-    if (a.in.bf16) a.in.form == 0 ? bwd<true, 0>(a, c, s) : bwd<true, 1>(a, c, s);
-    else a.in.form == 0 ? bwd<false, 0>(a, c, s) : bwd<false, 1>(a, c, s);
+    if (pairs(a.in)) a.in.form == 0 ? bwd<true, 2, 0>(a, c, s) : bwd<true, 2, 1>(a, c, s);
+    else if (a.in.bf16) a.in.form == 0 ? bwd<true, 1, 0>(a, c, s) : bwd<true, 1, 1>(a, c, s);
+    else a.in.form == 0 ? bwd<false, 1, 0>(a, c, s) : bwd<false, 1, 1>(a, c, s);
     if ((e = hipGetLastError()) != hipSuccess || a.in.form != 0) return e;
     launch(glr_sum_parts, dim3((unsigned)((a.in.D + 15) / 16)), dim3(256), 0, s, c.part, (long long)a.in.B * c.tiles,
            a.in.D, a.dA);
