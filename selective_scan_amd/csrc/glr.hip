@@ -32,10 +32,20 @@ constexpr int kPer = 4, kGroup = kWaves * kPer;  // maps a wave fetches; tiles o
 constexpr int kThreads = kWaves * 64;
 static_assert(kTile == kGlrStateSteps, "a tile starts where a state is kept");
 
+// Accesses that leave no lines behind in the L2. Stores of pairs: B4 L4096 D1536 gradient 130 -> 125 us,
+// B1 L4096 D1536 19.3 -> 18.4, and a pass over y behind it no slower. Loads of pairs where the call's
+// tensors outgrow the memory-side cache of 256 MiB: 125 -> 121 us, B8 L32768 D512 244 -> 235; within
+// it they cost (19.3 -> 21.2), and so they do where neighbouring strips share lines (B4 L16384 D1001
+// fp32 537 -> 688), which single channels therefore never use.
+constexpr int kNonTemporal = 2;
+constexpr long long kCached = 256LL << 20;
+
 constexpr uint32_t kAbsent = 0xffffffffu;
 constexpr int kPolls = 1 << 22;
 
 typedef unsigned long long u64;
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 // How the work is cut, and the workspace. chain = (batch, strip of 64 channels).
 struct Cut {
@@ -143,8 +153,8 @@ struct Raw {
 
 // A wave's rows of an io tensor through a buffer that ends behind the last of n rows: rows
 // further on read as 0 and are not written, and so does a lane whose channels do not exist (its
-// offset lies behind every buffer). One scalar addition a row.
-template <bool BF16, int V>
+// offset lies behind every buffer). One scalar addition a row. ONCE: loads leave no lines behind.
+template <bool BF16, int V, bool ONCE>
 struct Rows {
     static constexpr int T = Share<V>::T;
     __amdgpu_buffer_rsrc_t buf;
@@ -163,13 +173,13 @@ struct Rows {
 #pragma unroll
         for (int t = 0; t < T; ++t) {
             if constexpr (BF16 && V == 1) v[t].w = __builtin_amdgcn_raw_buffer_load_b16(buf, (int)off, (int)(t * pitch), 0);
-            else v[t].w = __builtin_amdgcn_raw_buffer_load_b32(buf, (int)off, (int)(t * pitch), 0);
+            else v[t].w = __builtin_amdgcn_raw_buffer_load_b32(buf, (int)off, (int)(t * pitch), ONCE ? kNonTemporal : 0);
         }
     }
     __device__ __forceinline__ void store(int t, const float (&v)[V]) const {
         if constexpr (V == 2) {
-            const uint32_t w = f32_to_bf16(v[0]) | (uint32_t)f32_to_bf16(v[1]) << 16;
-            __builtin_amdgcn_raw_buffer_store_b32(w, buf, (int)off, (int)(t * pitch), 0);
+            const uint32_t w = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{v[0], v[1]}, bf16x2));
+            __builtin_amdgcn_raw_buffer_store_b32(w, buf, (int)off, (int)(t * pitch), kNonTemporal);
         } else {
             store_io<BF16>(buf, off, t * pitch, v[0]);
         }
@@ -191,11 +201,8 @@ struct Steps {
     }
 };
 
-// Keeps the compiler from computing more than a few steps side by side, whose intermediate
-// values would cost the registers of a workgroup a CU: computed() values exist at that place.
-__device__ __forceinline__ void few_at_once(int t) {
-    if (t % 2 == 1) __builtin_amdgcn_sched_barrier(0);
-}
+// Values that exist from here on: left alone, the compiler puts off the gates' arithmetic to where
+// its results are needed and spills what it is made of.
 template <int V>
 __device__ __forceinline__ void computed(float (&v)[V]) {
 #pragma unroll
@@ -211,7 +218,7 @@ __device__ __forceinline__ float entering(const float (&start)[64], const float2
 }
 
 // ------------------------------------------------------------------ forward
-template <bool BF16, int V, int FORM, bool GATE>
+template <bool BF16, int V, bool ONCE, int FORM, bool GATE>
 __global__ void __launch_bounds__(kThreads, 4) glr_fwd_tiles(GlrArgs a, Cut c) {
     constexpr int T = Share<V>::T;
     __shared__ float2 own[kWaves][64], before[kWaves][64];
@@ -231,10 +238,10 @@ __global__ void __launch_bounds__(kThreads, 4) glr_fwd_tiles(GlrArgs a, Cut c) {
     Raw<BF16, V> z[T];
     {
         Raw<BF16, V> x[T], r[T], i[T];
-        Rows<BF16, V>(in.x, in.ldx, in.D, at.first, at.wave_live, me).load(x);
-        Rows<BF16, V>(in.r, in.ldr, in.D, at.first, at.wave_live, me).load(r);
-        if constexpr (FORM == 0) Rows<BF16, V>(in.i, in.ldi, in.D, at.first, at.wave_live, me).load(i);
-        if constexpr (GATE) Rows<BF16, V>(in.z, in.ldz, in.D, at.first, at.wave_live, me).load(z);
+        Rows<BF16, V, ONCE>(in.x, in.ldx, in.D, at.first, at.wave_live, me).load(x);
+        Rows<BF16, V, ONCE>(in.r, in.ldr, in.D, at.first, at.wave_live, me).load(r);
+        if constexpr (FORM == 0) Rows<BF16, V, ONCE>(in.i, in.ldi, in.D, at.first, at.wave_live, me).load(i);
+        if constexpr (GATE) Rows<BF16, V, ONCE>(in.z, in.ldz, in.D, at.first, at.wave_live, me).load(z);
         float A[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) A[v] = FORM == 0 ? in.A[min(me.d + v, in.D - 1)] : 0.0f;
@@ -246,7 +253,6 @@ __global__ void __launch_bounds__(kThreads, 4) glr_fwd_tiles(GlrArgs a, Cut c) {
                                        &cu[t][v]);
             computed(ca[t]);
             computed(cu[t]);
-            few_at_once(t);
         }
     }
     if (at.wave_live < kSteps)  // padding has u = 0 (x = 0); its state stays
@@ -311,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 4) glr_fwd_tiles(GlrArgs a, Cut c) {
             __hip_atomic_store(c.ends + ((size_t)b * c.groups + group) * in.D + me.d + v,
                                present(__builtin_fmaf(P[v], h[v], H[v])), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
-    const Rows<BF16, V> out(a.y, in.D, in.D, at.first, at.wave_stored, me);
+    const Rows<BF16, V, ONCE> out(a.y, in.D, in.D, at.first, at.wave_stored, me);
     auto sweep = [&](auto whole) {
 #pragma unroll
         for (int t = 0; t < T; ++t) {
@@ -323,7 +329,6 @@ __global__ void __launch_bounds__(kThreads, 4) glr_fwd_tiles(GlrArgs a, Cut c) {
                 if (!decltype(whole)::value) y[v] = t < at.live ? y[v] : 0.0f;
             }
             out.store(t, y);
-            few_at_once(t);
         }
     };
     if (at.wave_live == kSteps) sweep(std::true_type{});
@@ -337,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 4) glr_fwd_tiles(GlrArgs a, Cut c) {
 // Tiles are taken from the last to the first. The map of a piece on the gradient leaving it at
 // its end to that at its start is g -> P g + C. The gates are computed twice: what a step needs
 // of them across the wait, held in registers, would cost the second workgroup of a CU.
-template <bool BF16, int V, int FORM, bool GATE>
+template <bool BF16, int V, bool ONCE, int FORM, bool GATE>
 __global__ void __launch_bounds__(kThreads, 4) glr_bwd_tiles(GlrBwdArgs a, Cut c) {
     constexpr int T = Share<V>::T;
     __shared__ float ownP[kWaves][64], ownH[kWaves][64], ownC[kWaves][64];
@@ -359,11 +364,11 @@ __global__ void __launch_bounds__(kThreads, 4) glr_bwd_tiles(GlrBwdArgs a, Cut c
     float e[T][V], f[T][V], ca[T][V], cu[T][V], A[V], P[V], H[V], C[V];  // dz of a step is f h
     {
         Raw<BF16, V> dy[T], z[T];
-        Rows<BF16, V>(in.x, in.ldx, in.D, at.first, at.wave_live, me).load(x);
-        Rows<BF16, V>(in.r, in.ldr, in.D, at.first, at.wave_live, me).load(r);
-        if constexpr (FORM == 0) Rows<BF16, V>(in.i, in.ldi, in.D, at.first, at.wave_live, me).load(i);
-        Rows<BF16, V>(a.dy, in.D, in.D, at.first, at.wave_live, me).load(dy);
-        if constexpr (GATE) Rows<BF16, V>(in.z, in.ldz, in.D, at.first, at.wave_live, me).load(z);
+        Rows<BF16, V, ONCE>(in.x, in.ldx, in.D, at.first, at.wave_live, me).load(x);
+        Rows<BF16, V, ONCE>(in.r, in.ldr, in.D, at.first, at.wave_live, me).load(r);
+        if constexpr (FORM == 0) Rows<BF16, V, ONCE>(in.i, in.ldi, in.D, at.first, at.wave_live, me).load(i);
+        Rows<BF16, V, ONCE>(a.dy, in.D, in.D, at.first, at.wave_live, me).load(dy);
+        if constexpr (GATE) Rows<BF16, V, ONCE>(in.z, in.ldz, in.D, at.first, at.wave_live, me).load(z);
 #pragma unroll
         for (int v = 0; v < V; ++v) A[v] = FORM == 0 ? in.A[min(me.d + v, in.D - 1)] : 0.0f;
 #pragma unroll
@@ -386,7 +391,6 @@ __global__ void __launch_bounds__(kThreads, 4) glr_bwd_tiles(GlrBwdArgs a, Cut c
                 computed(e[t]);
                 computed(f[t]);
             }
-            few_at_once(t);
         }
     }
     if (at.wave_live < kSteps)  // padding has u = 0 and dy = 0; state and gradient stay
@@ -461,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, 4) glr_bwd_tiles(GlrBwdArgs a, Cut c
         }
     }
     if constexpr (GATE) {
-        const Rows<BF16, V> oz(a.dz, in.D, in.D, at.first, at.wave_stored, me);
+        const Rows<BF16, V, ONCE> oz(a.dz, in.D, in.D, at.first, at.wave_stored, me);
 #pragma unroll
         for (int t = 0; t < T; ++t) oz.store(t, f[t]);
     }
@@ -478,15 +482,18 @@ __global__ void __launch_bounds__(kThreads, 4) glr_bwd_tiles(GlrBwdArgs a, Cut c
             __hip_atomic_store(c.ends + ((size_t)b * c.groups + group) * in.D + me.d + v,
                                present(__builtin_fmaf(P[v], g[v], C[v])), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
-    const Rows<BF16, V> ox(a.dx, in.D, in.D, at.first, at.wave_stored, me), orr(a.dr, in.D, in.D, at.first, at.wave_stored, me);
-    const Rows<BF16, V> oi(FORM == 0 ? a.di : a.dx, in.D, in.D, at.first, at.wave_stored, me);
+    const Rows<BF16, V, ONCE> ox(a.dx, in.D, in.D, at.first, at.wave_stored, me), orr(a.dr, in.D, in.D, at.first, at.wave_stored, me);
+    const Rows<BF16, V, ONCE> oi(FORM == 0 ? a.di : a.dx, in.D, in.D, at.first, at.wave_stored, me);
+#pragma unroll
+    for (int t = 0; t < T; ++t) {
+        x[t].anew();
+        r[t].anew();
+        if constexpr (FORM == 0) i[t].anew();
+    }
     auto sweep = [&](auto whole) {
 #pragma unroll
         for (int t = T - 1; t >= 0; --t) {
             float dx[V], dr[V], di[V], dl;
-            x[t].anew();
-            r[t].anew();
-            if constexpr (FORM == 0) i[t].anew();
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 const Sigmoid sr(r[t][v]);
@@ -500,7 +507,6 @@ __global__ void __launch_bounds__(kThreads, 4) glr_bwd_tiles(GlrBwdArgs a, Cut c
             ox.store(t, dx);
             orr.store(t, dr);
             if constexpr (FORM == 0) oi.store(t, di);
-            few_at_once(t);
         }
     };
     if (at.wave_live == kSteps) sweep(std::true_type{});
@@ -576,6 +582,9 @@ hipError_t fill_words(void* ws, size_t bytes, hipStream_t s) {
     return hipGetLastError();
 }
 
+// Bytes of n tensors' elements.
+long long bytes(const GlrIn& in, int n) { return (long long)in.B * in.L * in.D * (in.bf16 ? 2 : 4) * n; }
+
 // Whether every row of the tensor starts on a pair of bf16 and holds whole pairs.
 bool pairs(const GlrIn& in) {
     const void* p[] = {in.x, in.r, in.i, in.z};
@@ -586,18 +595,28 @@ bool pairs(const GlrIn& in) {
     return true;
 }
 
-template <bool BF16, int V, int FORM>
+template <bool BF16, int V, bool ONCE>
 void fwd(const GlrArgs& a, const Cut& c, hipStream_t s) {
-    const dim3 grid = fold((long long)c.chains * c.tiles);
-    if (a.in.z) launch((glr_fwd_tiles<BF16, V, FORM, true>), grid, dim3(kThreads), 0, s, a, c);
-    else launch((glr_fwd_tiles<BF16, V, FORM, false>), grid, dim3(kThreads), 0, s, a, c);
+    const dim3 grid = fold((long long)c.chains * c.tiles), block(kThreads);
+    if (a.in.form == 0) {
+        if (a.in.z) launch((glr_fwd_tiles<BF16, V, ONCE, 0, true>), grid, block, 0, s, a, c);
+        else launch((glr_fwd_tiles<BF16, V, ONCE, 0, false>), grid, block, 0, s, a, c);
+    } else {
+        if (a.in.z) launch((glr_fwd_tiles<BF16, V, ONCE, 1, true>), grid, block, 0, s, a, c);
+        else launch((glr_fwd_tiles<BF16, V, ONCE, 1, false>), grid, block, 0, s, a, c);
+    }
 }
 
-template <bool BF16, int V, int FORM>
+template <bool BF16, int V, bool ONCE>
 void bwd(const GlrBwdArgs& a, const Cut& c, hipStream_t s) {
-    const dim3 grid = fold((long long)c.chains * c.tiles);
-    if (a.in.z) launch((glr_bwd_tiles<BF16, V, FORM, true>), grid, dim3(kThreads), 0, s, a, c);
-    else launch((glr_bwd_tiles<BF16, V, FORM, false>), grid, dim3(kThreads), 0, s, a, c);
+    const dim3 grid = fold((long long)c.chains * c.tiles), block(kThreads);
+    if (a.in.form == 0) {
+        if (a.in.z) launch((glr_bwd_tiles<BF16, V, ONCE, 0, true>), grid, block, 0, s, a, c);
+        else launch((glr_bwd_tiles<BF16, V, ONCE, 0, false>), grid, block, 0, s, a, c);
+    } else {
+        if (a.in.z) launch((glr_bwd_tiles<BF16, V, ONCE, 1, true>), grid, block, 0, s, a, c);
+        else launch((glr_bwd_tiles<BF16, V, ONCE, 1, false>), grid, block, 0, s, a, c);
+    }
 }
 
 }  // namespace
@@ -619,9 +638,10 @@ hipError_t launch_glr_fwd(const GlrArgs& a, hipStream_t s) {
     const Cut c = cut_of(a.in.B, a.in.L, a.in.D, static_cast<char*>(a.ws), &fill);
     const hipError_t e = fill_words(a.ws, fill, s);
     if (e != hipSuccess) return e;
-    if (pairs(a.in)) a.in.form == 0 ? fwd<true, 2, 0>(a, c, s) : fwd<true, 2, 1>(a, c, s);
-    else if (a.in.bf16) a.in.form == 0 ? fwd<true, 1, 0>(a, c, s) : fwd<true, 1, 1>(a, c, s);
-    else a.in.form == 0 ? fwd<false, 1, 0>(a, c, s) : fwd<false, 1, 1>(a, c, s);
+    if (!a.in.bf16) fwd<false, 1, false>(a, c, s);
+    else if (!pairs(a.in)) fwd<true, 1, false>(a, c, s);
+    else if (bytes(a.in, 3 + (a.in.i != nullptr) + (a.in.z != nullptr)) <= kCached) fwd<true, 2, false>(a, c, s);
+    else fwd<true, 2, true>(a, c, s);
     return hipGetLastError();
 }
 
@@ -630,9 +650,10 @@ hipError_t launch_glr_bwd(const GlrBwdArgs& a, hipStream_t s) {
     const Cut c = cut_of(a.in.B, a.in.L, a.in.D, static_cast<char*>(a.ws), &fill);
     hipError_t e = fill_words(a.ws, fill, s);
     if (e != hipSuccess) return e;
-    if (pairs(a.in)) a.in.form == 0 ? bwd<true, 2, 0>(a, c, s) : bwd<true, 2, 1>(a, c, s);
-    else if (a.in.bf16) a.in.form == 0 ? bwd<true, 1, 0>(a, c, s) : bwd<true, 1, 1>(a, c, s);
-    else a.in.form == 0 ? bwd<false, 1, 0>(a, c, s) : bwd<false, 1, 1>(a, c, s);
+    if (!a.in.bf16) bwd<false, 1, false>(a, c, s);
+    else if (!pairs(a.in)) bwd<true, 1, false>(a, c, s);
+    else if (bytes(a.in, 5 + 2 * (a.in.i != nullptr) + 2 * (a.in.z != nullptr)) <= kCached) bwd<true, 2, false>(a, c, s);
+    else bwd<true, 2, true>(a, c, s);
     if ((e = hipGetLastError()) != hipSuccess || a.in.form != 0) return e;
     launch(glr_sum_parts, dim3((unsigned)((a.in.D + 15) / 16)), dim3(256), 0, s, c.part, (long long)a.in.B * c.tiles,
            a.in.D, a.dA);

@@ -166,6 +166,25 @@ def test_an_empty_sequence():
     assert torch.equal(out["dh0"], d["dh_final"]) and (out["dA"] == 0).all()
 
 
+@pytest.mark.parametrize("form,gate", [("decay", True), ("convex", False)])
+def test_tensors_that_outgrow_the_caches(form, gate):
+    """More than 256 MiB in a call; a few channels of every kind of lane against 64 bits."""
+    B, L, D = 2, 16500, 1502
+    t = ref.glr_inputs(B, L, D, BF16, form, seed=14, gate=gate)
+    s = [L, L - 777]
+    d = to(t)
+    y, h, states = fwd(d, form, s)
+    out = bwd(d, states, form, s)
+    torch.cuda.synchronize()
+    pick = torch.tensor([0, 1, 62, 63, 64, 700, 1471, 1472, 1500, 1501])
+    few = {n: None if v is None else v[..., pick].contiguous() for n, v in t.items()}
+    g = ref.Glr(few, form, s, few["dy"], few["dh_final"])
+    ref.close(y[..., pick.to(DEV)], g.y, g.ey, 1.0, "y", store=BF16)
+    ref.close(h[..., pick.to(DEV)], g.h_final, g.eh_final, 1.0, "h_final", store=F32)
+    for n, (v, e) in g.out.items():
+        ref.close(out[n][..., pick.to(DEV)], v, e, 1.0, n, store=F32 if n in ("dA", "dh0") else BF16)
+
+
 @pytest.mark.parametrize("D", [24, 27])
 @pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
 def test_slices_of_one_projection(D, dtype):
