@@ -2,7 +2,17 @@
 //   s = residual + dropout(x),  y = (s - mean) rstd w + b   (rms: s rstd w + b)
 //   ds = rstd (dn - mean(dn) - xhat mean(dn xhat)) + dsum,  dn = dy w   (rms: no mean(dn))
 //   dresidual = ds,  dx = dropout(ds),  dw = sum dy xhat,  db = sum dy
-// First form: a wave per row, the row passed over as often as its sums ask.
+//
+// Bandwidth-bound: every row is read and written once, in registers in between. A lane has eight
+// neighbouring channels (an octet: the generator's block, and one or two 16-byte accesses); a row
+// takes 16 lanes (C <= 128), a wave (C <= 512) or a workgroup of as many waves as its octets
+// fill, one octet a lane, two beyond 8192 channels. Workgroups walk rows, so that a lane reads
+// its weights once and, in the gradient, sums dw and db of its channels in registers, and the
+// next row's loads are under way while the present one is reduced and written. Sums of a row that
+// spans waves go through LDS, two sets of slots in turn, one barrier a sum. Octets that start off
+// a 16-byte border (odd widths) are loaded as they lie; the last one of a row is taken value by
+// value where it is not whole.
+// Statistics and sums are fp32, the variance from squared distances to the mean.
 #include "add_norm.h"
 #include "common.h"
 #include "launch.h"
@@ -12,148 +22,421 @@
 namespace ssm {
 namespace {
 
-constexpr int kT = 64;
-constexpr int kParts = 256;
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+// 16 bytes at any element's address
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4), aligned(2)));
 
-__device__ __forceinline__ float ld(const void* p, size_t i, bool bf16) {
-    return bf16 ? bf16_to_f32(static_cast<const uint16_t*>(p)[i]) : static_cast<const float*>(p)[i];
-}
-
-__device__ __forceinline__ void st(void* p, size_t i, float v, bool bf16) {
-    if (bf16) static_cast<uint16_t*>(p)[i] = f32_to_bf16(v);
-    else static_cast<float*>(p)[i] = v;
-}
-
-__device__ __forceinline__ float sum_wave(float v) {
+// An octet as it is stored: values beyond the row's end read as 0.
+template <bool BF16>
+struct Octet {
+    static constexpr int N = BF16 ? 4 : 8;
+    uint32_t w[N];
+    // n: channels of the row from here on
+    __device__ __forceinline__ void load(const void* p, size_t i, int n) {
+        if (n >= 8) {
+            const char* at = static_cast<const char*>(p) + i * (BF16 ? 2 : 4);
 #pragma unroll
-    for (int f = 1; f < 64; f <<= 1) v += __shfl_xor(v, f);
-    return v;
+            for (int k = 0; k < N / 4; ++k) {
+                const u32x4 q = *reinterpret_cast<const u32x4*>(at + 16 * k);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) w[4 * k + j] = q[j];
+            }
+            return;
+        }
+#pragma unroll
+        for (int k = 0; k < N; ++k) w[k] = 0;
+#pragma unroll
+        for (int j = 0; j < 7; ++j) {
+            if (j >= n) continue;
+            if constexpr (BF16) w[j / 2] |= (uint32_t)static_cast<const uint16_t*>(p)[i + j] << (16 * (j & 1));
+            else w[j] = static_cast<const uint32_t*>(p)[i + j];
+        }
+    }
+    __device__ __forceinline__ float operator[](int j) const {
+        if constexpr (BF16) return j & 1 ? bf16_hi(w[j / 2]) : bf16_lo(w[j / 2]);
+        else return __uint_as_float(w[j]);
+    }
+};
+
+template <bool BF16>
+__device__ __forceinline__ void store(void* p, size_t i, int n, const float (&v)[8]) {
+    if (n >= 8) {
+        char* at = static_cast<char*>(p) + i * (BF16 ? 2 : 4);
+        if constexpr (BF16) {
+            u32x4 q;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                q[k] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{v[2 * k], v[2 * k + 1]}, bf16x2));
+            *reinterpret_cast<u32x4*>(at) = q;
+        } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                u32x4 q;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) q[k] = __float_as_uint(v[4 * h + k]);
+                *reinterpret_cast<u32x4*>(at + 16 * h) = q;
+            }
+        }
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 7; ++j) {
+        if (j >= n) continue;
+        if constexpr (BF16) static_cast<uint16_t*>(p)[i + j] = f32_to_bf16(v[j]);
+        else static_cast<float*>(p)[i + j] = v[j];
+    }
 }
 
-__device__ __forceinline__ float dropped(float v, const Dropout& d, int m, int c, int C) {
-    if (d.least == 0) return v;
-    const Philox p(d.rng[0], d.rng[1] + (unsigned long long)m * ((C + 7) / 8) + c / 8);
-    return p.bits(c % 8) >= d.least ? v * d.scale : 0.0f;
+// Eight of a vector's values (missing: the vector is NULL; 0 behind its end).
+__device__ __forceinline__ void params(const float* p, int c, int n, float missing, float (&v)[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = j < n ? (p ? p[c + j] : missing) : 0.0f;
 }
 
-__global__ void __launch_bounds__(kT) add_norm_fwd_simple(AddNormArgs a) {
-    const int m = blockIdx.x, l = threadIdx.x;
-    const size_t base = (size_t)m * a.C;
-    auto value = [&](int c) {
-        float v = dropped(ld(a.x, base + c, a.bf16), a.drop, m, c, a.C);
-        return a.residual ? v + ld(a.residual, base + c, a.res_bf16) : v;
+// v where the octet's block keeps it, scaled; else 0.
+__device__ __forceinline__ void drop(float (&v)[8], const Dropout& d, unsigned long long seed, unsigned long long block) {
+    const Philox p(seed, block);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = p.bits(j) >= d.least ? v[j] * d.scale : 0.0f;
+}
+
+// The lanes of a row: L of a wave, or (L = 0) the whole workgroup.
+template <int L>
+struct Row {
+    static constexpr int kRows = L == 0 ? 1 : 256 / L;  // rows of a workgroup
+    __device__ __forceinline__ static int lane() { return L == 0 ? threadIdx.x : threadIdx.x % L; }
+    __device__ __forceinline__ static int lanes() { return L == 0 ? blockDim.x : L; }
+    __device__ __forceinline__ static int row() { return L == 0 ? 0 : threadIdx.x / L; }
+
+    // Sums over the row's lanes, in every lane and in a fixed order. slots: 16 a value, another set
+    // than the last call's, whose values waves that are behind may still read; that they have read
+    // those of the call before it, they say at the last call's barrier.
+    template <int N>
+    __device__ __forceinline__ static void sum(float (&v)[N], float (*slots)[16]) {
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+#pragma unroll
+            for (int f = 1; f < (L == 0 ? 64 : L); f <<= 1) v[k] += __shfl_xor(v[k], f);
+        if constexpr (L == 0) {
+            const int waves = blockDim.x >> 6;
+            if (waves == 1) return;
+            if ((threadIdx.x & 63) == 0)
+#pragma unroll
+                for (int k = 0; k < N; ++k) slots[k][threadIdx.x >> 6] = v[k];
+            __syncthreads();
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                v[k] = slots[k][0];
+                for (int w = 1; w < waves; ++w) v[k] += slots[k][w];
+            }
+        }
+    }
+};
+
+// ------------------------------------------------------------------ forward
+template <bool BF16, bool RES16, int L, int R>
+__global__ void __launch_bounds__(L == 0 ? 1024 : 256) add_norm_fwd(AddNormArgs a) {
+    typedef Row<L> Rw;
+    __shared__ float slots[2][1][16];
+    const int l = Rw::lane(), octets = (a.C + 7) / 8;
+    const long long step = (long long)gridDim.x * Rw::kRows;
+    float w[R][8], b[R][8];
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+        const int c = (l + k * Rw::lanes()) * 8;
+        params(a.weight, c, a.C - c, 1.0f, w[k]);
+        params(a.bias, c, a.C - c, 0.0f, b[k]);
+    }
+    const bool dropping = a.drop.least != 0;
+    const unsigned long long seed = dropping ? a.drop.rng[0] : 0, offset = dropping ? a.drop.rng[1] : 0;
+    const float inv = 1.0f / (float)a.C;
+    Octet<BF16> x[R];
+    Octet<RES16> res[R];
+    auto fetch = [&](long long m) {
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            const int c = (l + k * Rw::lanes()) * 8;
+            x[k].load(a.x, m * a.C + c, a.C - c);
+            if (a.residual) res[k].load(a.residual, m * a.C + c, a.C - c);
+        }
     };
+    // with workgroups as rows m is the same in every lane: no wave leaves the barriers early
+    long long m = (long long)blockIdx.x * Rw::kRows + Rw::row();
+    int turn = 0;
+    if (m < a.M) fetch(m);
+    for (; m < a.M; m += step) {
+        float s[R][8], t[1] = {0.0f};
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s[k][j] = x[k][j];
+            if (dropping) drop(s[k], a.drop, seed, offset + (unsigned long long)m * octets + l + k * Rw::lanes());
+            if (a.residual)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) s[k][j] += res[k][j];
+        }
+        if (m + step < a.M) fetch(m + step);
+        float mean = 0.0f;
+        if (!a.rms) {
+#pragma unroll
+            for (int k = 0; k < R; ++k)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) t[0] += s[k][j];
+            Rw::sum(t, slots[turn]);
+            turn ^= 1;
+            mean = t[0] * inv;
+            t[0] = 0.0f;
+        }
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            const int n = a.C - (l + k * Rw::lanes()) * 8;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float d = j < n ? s[k][j] - mean : 0.0f;
+                t[0] = __builtin_fmaf(d, d, t[0]);
+            }
+        }
+        Rw::sum(t, slots[turn]);
+        turn ^= 1;
+        const float rstd = 1.0f / sqrtf(t[0] * inv + a.eps);
+        if (l == 0) {
+            if (a.mean) a.mean[m] = mean;
+            if (a.rstd) a.rstd[m] = rstd;
+        }
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            const int c = (l + k * Rw::lanes()) * 8;
+            if (c >= a.C) continue;
+            if (a.sum) store<RES16>(a.sum, m * a.C + c, a.C - c, s[k]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s[k][j] = __builtin_fmaf((s[k][j] - mean) * rstd, w[k][j], b[k][j]);
+            store<BF16>(a.y, m * a.C + c, a.C - c, s[k]);
+        }
+    }
+}
+
+// ------------------------------------------------------------------ gradient
+// Workgroup g leaves its sums of dw and db in part[g][2][C] (NULL: not wanted).
+template <bool BF16, bool RES16, int L, int R>
+__global__ void __launch_bounds__(L == 0 ? 1024 : 256) add_norm_bwd(AddNormBwdArgs a, float* part) {
+    typedef Row<L> Rw;
+    __shared__ float slots[2][2][16];
+    __shared__ float joined[L == 0 ? 1 : 256 * 16];
+    const int l = Rw::lane(), octets = (a.C + 7) / 8;
+    const long long step = (long long)gridDim.x * Rw::kRows;
+    float w[R][8], dw[R][8], db[R][8];
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+        const int c = (l + k * Rw::lanes()) * 8;
+        params(a.weight, c, a.C - c, 1.0f, w[k]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) dw[k][j] = db[k][j] = 0.0f;
+    }
+    const bool dropping = a.drop.least != 0;
+    const unsigned long long seed = dropping ? a.drop.rng[0] : 0, offset = dropping ? a.drop.rng[1] : 0;
+    const float inv = 1.0f / (float)a.C;
+    Octet<RES16> sum[R], add[R];
+    Octet<BF16> dy[R];
+    float mean = 0.0f, rstd = 0.0f;
+    auto fetch = [&](long long m) {
+        if (!a.rms) mean = a.mean[m];
+        rstd = a.rstd[m];
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            const int c = (l + k * Rw::lanes()) * 8;
+            sum[k].load(a.sum, m * a.C + c, a.C - c);
+            dy[k].load(a.dy, m * a.C + c, a.C - c);
+            if (a.dsum) add[k].load(a.dsum, m * a.C + c, a.C - c);
+        }
+    };
+    long long m = (long long)blockIdx.x * Rw::kRows + Rw::row();
+    int turn = 0;
+    if (m < a.M) fetch(m);
+    for (; m < a.M; m += step) {
+        float xhat[R][8], d[R][8], t[2] = {0.0f, 0.0f};
+        const float r = rstd;
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            const int n = a.C - (l + k * Rw::lanes()) * 8;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                xhat[k][j] = j < n ? (sum[k][j] - mean) * r : 0.0f;
+                const float g = dy[k][j];
+                db[k][j] += g;
+                dw[k][j] = __builtin_fmaf(g, xhat[k][j], dw[k][j]);
+                d[k][j] = g * w[k][j];
+                t[0] += d[k][j];
+                t[1] = __builtin_fmaf(d[k][j], xhat[k][j], t[1]);
+            }
+        }
+        Octet<RES16> more[R];
+#pragma unroll
+        for (int k = 0; k < R; ++k) more[k] = add[k];
+        if (m + step < a.M) fetch(m + step);
+        Rw::sum(t, slots[turn]);
+        turn ^= 1;
+        const float s0 = a.rms ? 0.0f : t[0] * inv, s1 = t[1] * inv;
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            const int c = (l + k * Rw::lanes()) * 8;
+            if (c >= a.C) continue;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                d[k][j] = r * (d[k][j] - s0 - xhat[k][j] * s1);
+                if (a.dsum) d[k][j] += more[k][j];
+            }
+            if (a.dresidual) store<RES16>(a.dresidual, m * a.C + c, a.C - c, d[k]);
+            if (!a.dx) continue;
+            if (dropping) drop(d[k], a.drop, seed, offset + (unsigned long long)m * octets + l + k * Rw::lanes());
+            store<BF16>(a.dx, m * a.C + c, a.C - c, d[k]);
+        }
+    }
+    if (!part) return;
+    float* p = part + (size_t)blockIdx.x * 2 * a.C;
+    if constexpr (L == 0) {
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            const int c = (l + k * Rw::lanes()) * 8;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (c + j < a.C) {
+                    p[c + j] = dw[k][j];
+                    p[a.C + c + j] = db[k][j];
+                }
+        }
+    } else {
+        // the workgroup's rows added in order; R = 1
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            joined[threadIdx.x * 16 + j] = dw[0][j];
+            joined[threadIdx.x * 16 + 8 + j] = db[0][j];
+        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < L * 16; i += 256) {
+            const int c = i / 16 * 8 + i % 8;
+            float s = 0.0f;
+            for (int q = 0; q < Rw::kRows; ++q) s += joined[q * L * 16 + i];
+            if (c < a.C) p[(i % 16 < 8 ? 0 : a.C) + c] = s;
+        }
+    }
+}
+
+// dw and db from n parts: 16 columns a workgroup, 16 lanes on each, in a fixed order.
+__global__ void __launch_bounds__(256) add_norm_sum(const float* __restrict__ part, int n, int C, float* dweight,
+                                                    float* dbias) {
+    __shared__ float sums[16][17];
+    const int cl = threadIdx.x & 15, q = threadIdx.x >> 4, c = blockIdx.x * 16 + cl;
     float s = 0.0f;
-    for (int c = l; c < a.C; c += kT) s += value(c);
-    const float mean = a.rms ? 0.0f : sum_wave(s) / (float)a.C;
-    s = 0.0f;
-    for (int c = l; c < a.C; c += kT) {
-        const float d = value(c) - mean;
-        s = __builtin_fmaf(d, d, s);
-    }
-    const float rstd = 1.0f / sqrtf(sum_wave(s) / (float)a.C + a.eps);
-    if (l == 0) {
-        if (a.mean) a.mean[m] = mean;
-        if (a.rstd) a.rstd[m] = rstd;
-    }
-    for (int c = l; c < a.C; c += kT) {
-        const float v = value(c);
-        if (a.sum) st(a.sum, base + c, v, a.res_bf16);
-        st(a.y, base + c, __builtin_fmaf((v - mean) * rstd, a.weight ? a.weight[c] : 1.0f, a.bias ? a.bias[c] : 0.0f),
-           a.bf16);
+    if (c < 2 * C)
+#pragma unroll 8
+        for (int k = q; k < n; k += 16) s += part[(size_t)k * 2 * C + c];
+    sums[q][cl] = s;
+    __syncthreads();
+    if (q != 0 || c >= 2 * C) return;
+#pragma unroll
+    for (int k = 1; k < 16; ++k) s += sums[k][cl];
+    if (c < C && dweight) dweight[c] = s;
+    if (c >= C && dbias) dbias[c - C] = s;
+}
+
+// ------------------------------------------------------------------ dropout alone
+// An octet a lane at a time; the octets of all rows one after the other.
+template <bool BF16>
+__global__ void __launch_bounds__(256) dropout_octets(DropoutArgs a, long long total, unsigned octets) {
+    const bool dropping = a.drop.least != 0;
+    const unsigned long long seed = dropping ? a.drop.rng[0] : 0, offset = dropping ? a.drop.rng[1] : 0;
+    for (long long q = (long long)blockIdx.x * 256 + threadIdx.x; q < total; q += (long long)gridDim.x * 256) {
+        const long long m = q / octets;
+        const int c = (int)(q - m * octets) * 8, n = a.C - c;
+        Octet<BF16> x;
+        x.load(a.x, m * a.C + c, n);
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = x[j];
+        if (dropping) drop(v, a.drop, seed, offset + (unsigned long long)q);
+        store<BF16>(a.y, m * a.C + c, n, v);
     }
 }
 
-__global__ void __launch_bounds__(kT) add_norm_bwd_simple(AddNormBwdArgs a) {
-    const int m = blockIdx.x, l = threadIdx.x;
-    const size_t base = (size_t)m * a.C;
-    const float mean = a.rms ? 0.0f : a.mean[m], rstd = a.rstd[m];
-    float s0 = 0.0f, s1 = 0.0f;
-    for (int c = l; c < a.C; c += kT) {
-        const float xhat = (ld(a.sum, base + c, a.res_bf16) - mean) * rstd;
-        const float dn = ld(a.dy, base + c, a.bf16) * (a.weight ? a.weight[c] : 1.0f);
-        s0 += dn;
-        s1 = __builtin_fmaf(dn, xhat, s1);
+// ------------------------------------------------------------------ choices
+constexpr int kMostLanes = 2048 * 256;  // the GPU's
+
+// Lanes of a workgroup, and rows it takes at once.
+struct Cut {
+    int lanes, rows;
+    Cut(int C) {
+        const int octets = (C + 7) / 8;
+        if (octets <= 16) lanes = 256, rows = 16;
+        else if (octets <= 64) lanes = 256, rows = 4;
+        else lanes = std::min((octets + 63) / 64 * 64, 1024), rows = 1;
     }
-    s0 = a.rms ? 0.0f : sum_wave(s0) / (float)a.C;
-    s1 = sum_wave(s1) / (float)a.C;
-    for (int c = l; c < a.C; c += kT) {
-        const float xhat = (ld(a.sum, base + c, a.res_bf16) - mean) * rstd;
-        const float dn = ld(a.dy, base + c, a.bf16) * (a.weight ? a.weight[c] : 1.0f);
-        float ds = rstd * (dn - s0 - xhat * s1);
-        if (a.dsum) ds += ld(a.dsum, base + c, a.res_bf16);
-        if (a.dresidual) st(a.dresidual, base + c, ds, a.res_bf16);
-        if (a.dx) st(a.dx, base + c, dropped(ds, a.drop, m, c, a.C), a.bf16);
+    // workgroups for M rows: at most fill times what the GPU holds at once
+    int groups(int M, int fill) const {
+        return (int)std::max<long long>(1, std::min<long long>(((long long)M + rows - 1) / rows, (long long)fill * kMostLanes / lanes));
     }
+};
+
+// Parts of dw and db: at least eight rows each, and no more than half of what the GPU holds.
+int parts(int M, int C) {
+    const Cut c(C);
+    const long long most = std::max<long long>(1, ((long long)M + 8LL * c.rows - 1) / (8LL * c.rows));
+    return (int)std::min<long long>(most, kMostLanes / 2 / c.lanes);
 }
 
-__global__ void __launch_bounds__(kT) add_norm_affine(AddNormBwdArgs a, float* part) {
-    const int c = blockIdx.x * kT + threadIdx.x;
-    if (c >= a.C) return;
-    float dw = 0.0f, db = 0.0f;
-    for (int m = blockIdx.y; m < a.M; m += gridDim.y) {
-        const size_t at = (size_t)m * a.C + c;
-        const float dy = ld(a.dy, at, a.bf16), mean = a.rms ? 0.0f : a.mean[m];
-        dw = __builtin_fmaf(dy, (ld(a.sum, at, a.res_bf16) - mean) * a.rstd[m], dw);
-        db += dy;
-    }
-    part[(size_t)blockIdx.y * 2 * a.C + c] = dw;
-    part[(size_t)blockIdx.y * 2 * a.C + a.C + c] = db;
-}
-
-__global__ void __launch_bounds__(kT) add_norm_sum(const float* part, int n, int C, float* dweight, float* dbias) {
-    const int c = blockIdx.x * kT + threadIdx.x;
-    if (c >= C) return;
-    float dw = 0.0f, db = 0.0f;
-    for (int k = 0; k < n; ++k) {
-        dw += part[(size_t)k * 2 * C + c];
-        db += part[(size_t)k * 2 * C + C + c];
-    }
-    if (dweight) dweight[c] = dw;
-    if (dbias) dbias[c] = db;
-}
-
-__global__ void __launch_bounds__(kT) dropout_simple(DropoutArgs a) {
-    const int m = blockIdx.x;
-    for (int c = threadIdx.x; c < a.C; c += kT) {
-        const size_t at = (size_t)m * a.C + c;
-        st(a.y, at, dropped(ld(a.x, at, a.bf16), a.drop, m, c, a.C), a.bf16);
-    }
-}
-
-int parts(int M) { return std::min(kParts, M); }
-
-}  // namespace
-
-size_t add_norm_bwd_workspace_bytes(int M, int C, bool, bool) { return (size_t)parts(M) * 2 * C * 4; }
-
-hipError_t launch_add_norm_fwd(const AddNormArgs& a, hipStream_t s) {
-    if (a.M == 0) return hipSuccess;
-    launch(add_norm_fwd_simple, dim3((unsigned)a.M), dim3(kT), 0, s, a);
+template <bool BF16, bool RES16>
+hipError_t fwd(const AddNormArgs& a, hipStream_t s) {
+    const Cut c(a.C);
+    const dim3 grid((unsigned)c.groups(a.M, 1)), block((unsigned)c.lanes);
+    if (c.rows == 16) launch((add_norm_fwd<BF16, RES16, 16, 1>), grid, block, 0, s, a);
+    else if (c.rows == 4) launch((add_norm_fwd<BF16, RES16, 64, 1>), grid, block, 0, s, a);
+    else if (a.C <= 8192) launch((add_norm_fwd<BF16, RES16, 0, 1>), grid, block, 0, s, a);
+    else launch((add_norm_fwd<BF16, RES16, 0, 2>), grid, block, 0, s, a);
     return hipGetLastError();
 }
 
+template <bool BF16, bool RES16>
+hipError_t bwd(const AddNormBwdArgs& a, float* part, int n, hipStream_t s) {
+    const Cut c(a.C);
+    const dim3 grid((unsigned)n), block((unsigned)c.lanes);
+    if (c.rows == 16) launch((add_norm_bwd<BF16, RES16, 16, 1>), grid, block, 0, s, a, part);
+    else if (c.rows == 4) launch((add_norm_bwd<BF16, RES16, 64, 1>), grid, block, 0, s, a, part);
+    else if (a.C <= 8192) launch((add_norm_bwd<BF16, RES16, 0, 1>), grid, block, 0, s, a, part);
+    else launch((add_norm_bwd<BF16, RES16, 0, 2>), grid, block, 0, s, a, part);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+size_t add_norm_bwd_workspace_bytes(int M, int C, bool, bool) { return M == 0 ? 0 : (size_t)parts(M, C) * 2 * C * 4; }
+
+hipError_t launch_add_norm_fwd(const AddNormArgs& a, hipStream_t s) {
+    if (a.M == 0) return hipSuccess;
+    if (!a.bf16) return fwd<false, false>(a, s);
+    return a.res_bf16 ? fwd<true, true>(a, s) : fwd<true, false>(a, s);
+}
+
 hipError_t launch_add_norm_bwd(const AddNormBwdArgs& a, hipStream_t s) {
-    const int n = parts(a.M);
-    float* part = static_cast<float*>(a.ws);
-    const unsigned cols = (unsigned)((a.C + kT - 1) / kT);
+    const bool affine = a.dweight || a.dbias;
+    float* part = affine ? static_cast<float*>(a.ws) : nullptr;
+    const int n = a.M == 0 ? 0 : parts(a.M, a.C);
     hipError_t e = hipSuccess;
     if (a.M > 0) {
-        launch(add_norm_bwd_simple, dim3((unsigned)a.M), dim3(kT), 0, s, a);
-        if ((e = hipGetLastError()) != hipSuccess) return e;
+        if (!a.bf16) e = bwd<false, false>(a, part, n, s);
+        else e = a.res_bf16 ? bwd<true, true>(a, part, n, s) : bwd<true, false>(a, part, n, s);
     }
-    if (!a.dweight && !a.dbias) return e;
-    if (a.M > 0) {
-        launch(add_norm_affine, dim3(cols, (unsigned)n), dim3(kT), 0, s, a, part);
-        if ((e = hipGetLastError()) != hipSuccess) return e;
-    }
-    launch(add_norm_sum, dim3(cols), dim3(kT), 0, s, part, n, a.C, a.dweight, a.dbias);
+    if (e != hipSuccess || !affine) return e;
+    launch(add_norm_sum, dim3((unsigned)((2 * a.C + 15) / 16)), dim3(256), 0, s, part, n, a.C, a.dweight, a.dbias);
     return hipGetLastError();
 }
 
 hipError_t launch_dropout(const DropoutArgs& a, hipStream_t s) {
-    if (a.M == 0) return hipSuccess;
-    launch(dropout_simple, dim3((unsigned)a.M), dim3(kT), 0, s, a);
+    const unsigned octets = ((unsigned)a.C + 7) / 8;
+    const long long total = (long long)a.M * octets;
+    if (total == 0) return hipSuccess;
+    const dim3 grid((unsigned)std::min<long long>((total + 255) / 256, kMostLanes / 256));
+    if (a.bf16) launch((dropout_octets<true>), grid, dim3(256), 0, s, a, total, octets);
+    else launch((dropout_octets<false>), grid, dim3(256), 0, s, a, total, octets);
     return hipGetLastError();
 }
 
