@@ -27,6 +27,8 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 // 16 bytes at any element's address
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4), aligned(2)));
 
+constexpr int kBwdLanes = 768;  // of a workgroup in the gradient, but where one row takes more
+
 // An octet as it is stored: values beyond the row's end read as 0.
 template <bool BF16>
 struct Octet {
@@ -101,34 +103,41 @@ __device__ __forceinline__ void drop(float (&v)[8], const Dropout& d, unsigned l
     for (int j = 0; j < 8; ++j) v[j] = p.bits(j) >= d.least ? v[j] * d.scale : 0.0f;
 }
 
-// The lanes of a row: L of a wave, or (L = 0) the whole workgroup.
+// The lanes of a row: L of a wave, or (L = 0) `waves` whole waves of the workgroup, of which it
+// has one or several rows.
 template <int L>
 struct Row {
-    static constexpr int kRows = L == 0 ? 1 : 256 / L;  // rows of a workgroup
-    __device__ __forceinline__ static int lane() { return L == 0 ? threadIdx.x : threadIdx.x % L; }
-    __device__ __forceinline__ static int lanes() { return L == 0 ? blockDim.x : L; }
-    __device__ __forceinline__ static int row() { return L == 0 ? 0 : threadIdx.x / L; }
+    int waves;
+    __device__ __forceinline__ int lanes() const { return L == 0 ? waves * 64 : L; }
+    __device__ __forceinline__ int rows() const { return blockDim.x / lanes(); }
+    // the same in every lane of a wave but with rows of 16 lanes
+    __device__ __forceinline__ int row() const {
+        if constexpr (L == 16) return threadIdx.x / 16;
+        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        return L == 0 ? wave / waves : wave;
+    }
+    __device__ __forceinline__ int lane() const { return threadIdx.x - row() * lanes(); }
 
     // Sums over the row's lanes, in every lane and in a fixed order. slots: 16 a value, another set
     // than the last call's, whose values waves that are behind may still read; that they have read
-    // those of the call before it, they say at the last call's barrier.
+    // those of the call before it, they say at the last call's barrier. Every wave of the workgroup
+    // takes part.
     template <int N>
-    __device__ __forceinline__ static void sum(float (&v)[N], float (*slots)[16]) {
+    __device__ __forceinline__ void sum(float (&v)[N], float (*slots)[16]) const {
 #pragma unroll
         for (int k = 0; k < N; ++k)
 #pragma unroll
             for (int f = 1; f < (L == 0 ? 64 : L); f <<= 1) v[k] += __shfl_xor(v[k], f);
         if constexpr (L == 0) {
-            const int waves = blockDim.x >> 6;
-            if (waves == 1) return;
+            const int wave = threadIdx.x >> 6, first = row() * waves;
             if ((threadIdx.x & 63) == 0)
 #pragma unroll
-                for (int k = 0; k < N; ++k) slots[k][threadIdx.x >> 6] = v[k];
+                for (int k = 0; k < N; ++k) slots[k][wave] = v[k];
             __syncthreads();
 #pragma unroll
             for (int k = 0; k < N; ++k) {
-                v[k] = slots[k][0];
-                for (int w = 1; w < waves; ++w) v[k] += slots[k][w];
+                v[k] = slots[k][first];
+                for (int w = 1; w < waves; ++w) v[k] += slots[k][first + w];
             }
         }
     }
@@ -137,14 +146,14 @@ struct Row {
 // ------------------------------------------------------------------ forward
 template <bool BF16, bool RES16, int L, int R>
 __global__ void __launch_bounds__(L == 0 ? 1024 : 256) add_norm_fwd(AddNormArgs a) {
-    typedef Row<L> Rw;
     __shared__ float slots[2][1][16];
-    const int l = Rw::lane(), octets = (a.C + 7) / 8;
-    const long long step = (long long)gridDim.x * Rw::kRows;
+    const Row<L> me{(int)blockDim.x >> 6};  // with whole waves, one row a workgroup
+    const int l = me.lane(), lanes = me.lanes(), octets = (a.C + 7) / 8;
+    const long long step = (long long)gridDim.x * me.rows();
     float w[R][8], b[R][8];
 #pragma unroll
     for (int k = 0; k < R; ++k) {
-        const int c = (l + k * Rw::lanes()) * 8;
+        const int c = (l + k * lanes) * 8;
         params(a.weight, c, a.C - c, 1.0f, w[k]);
         params(a.bias, c, a.C - c, 0.0f, b[k]);
     }
@@ -156,13 +165,13 @@ __global__ void __launch_bounds__(L == 0 ? 1024 : 256) add_norm_fwd(AddNormArgs 
     auto fetch = [&](long long m) {
 #pragma unroll
         for (int k = 0; k < R; ++k) {
-            const int c = (l + k * Rw::lanes()) * 8;
+            const int c = (l + k * lanes) * 8;
             x[k].load(a.x, m * a.C + c, a.C - c);
             if (a.residual) res[k].load(a.residual, m * a.C + c, a.C - c);
         }
     };
-    // with workgroups as rows m is the same in every lane: no wave leaves the barriers early
-    long long m = (long long)blockIdx.x * Rw::kRows + Rw::row();
+    // one row a workgroup: m is the same in every lane, no wave leaves the barriers early
+    long long m = (long long)blockIdx.x * me.rows() + me.row();
     int turn = 0;
     if (m < a.M) fetch(m);
     for (; m < a.M; m += step) {
@@ -171,7 +180,7 @@ __global__ void __launch_bounds__(L == 0 ? 1024 : 256) add_norm_fwd(AddNormArgs 
         for (int k = 0; k < R; ++k) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) s[k][j] = x[k][j];
-            if (dropping) drop(s[k], a.drop, seed, offset + (unsigned long long)m * octets + l + k * Rw::lanes());
+            if (dropping) drop(s[k], a.drop, seed, offset + (unsigned long long)m * octets + l + k * lanes);
             if (a.residual)
 #pragma unroll
                 for (int j = 0; j < 8; ++j) s[k][j] += res[k][j];
@@ -183,21 +192,21 @@ __global__ void __launch_bounds__(L == 0 ? 1024 : 256) add_norm_fwd(AddNormArgs 
             for (int k = 0; k < R; ++k)
 #pragma unroll
                 for (int j = 0; j < 8; ++j) t[0] += s[k][j];
-            Rw::sum(t, slots[turn]);
+            me.sum(t, slots[turn]);
             turn ^= 1;
             mean = t[0] * inv;
             t[0] = 0.0f;
         }
 #pragma unroll
         for (int k = 0; k < R; ++k) {
-            const int n = a.C - (l + k * Rw::lanes()) * 8;
+            const int n = a.C - (l + k * lanes) * 8;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const float d = j < n ? s[k][j] - mean : 0.0f;
                 t[0] = __builtin_fmaf(d, d, t[0]);
             }
         }
-        Rw::sum(t, slots[turn]);
+        me.sum(t, slots[turn]);
         turn ^= 1;
         const float rstd = 1.0f / sqrtf(t[0] * inv + a.eps);
         if (l == 0) {
@@ -206,7 +215,7 @@ __global__ void __launch_bounds__(L == 0 ? 1024 : 256) add_norm_fwd(AddNormArgs 
         }
 #pragma unroll
         for (int k = 0; k < R; ++k) {
-            const int c = (l + k * Rw::lanes()) * 8;
+            const int c = (l + k * lanes) * 8;
             if (c >= a.C) continue;
             if (a.sum) store<RES16>(a.sum, m * a.C + c, a.C - c, s[k]);
 #pragma unroll
@@ -217,18 +226,19 @@ __global__ void __launch_bounds__(L == 0 ? 1024 : 256) add_norm_fwd(AddNormArgs 
 }
 
 // ------------------------------------------------------------------ gradient
-// Workgroup g leaves its sums of dw and db in part[g][2][C] (NULL: not wanted).
-template <bool BF16, bool RES16, int L, int R>
-__global__ void __launch_bounds__(L == 0 ? 1024 : 256) add_norm_bwd(AddNormBwdArgs a, float* part) {
-    typedef Row<L> Rw;
+// Workgroup g leaves its sums of dw and db, those of its rows added in order, in part[g][2][C]
+// (NULL: not wanted). joined: 16 values a lane, where a workgroup has several rows.
+template <bool BF16, bool RES16, int L, int R, int MOST>
+__global__ void __launch_bounds__(MOST) add_norm_bwd(AddNormBwdArgs a, int waves, float* part) {
     __shared__ float slots[2][2][16];
-    __shared__ float joined[L == 0 ? 1 : 256 * 16];
-    const int l = Rw::lane(), octets = (a.C + 7) / 8;
-    const long long step = (long long)gridDim.x * Rw::kRows;
+    extern __shared__ float joined[];
+    const Row<L> me{waves};
+    const int l = me.lane(), lanes = me.lanes(), rows = me.rows(), octets = (a.C + 7) / 8;
+    const long long step = (long long)gridDim.x * rows;
     float w[R][8], dw[R][8], db[R][8];
 #pragma unroll
     for (int k = 0; k < R; ++k) {
-        const int c = (l + k * Rw::lanes()) * 8;
+        const int c = (l + k * lanes) * 8;
         params(a.weight, c, a.C - c, 1.0f, w[k]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) dw[k][j] = db[k][j] = 0.0f;
@@ -239,26 +249,30 @@ __global__ void __launch_bounds__(L == 0 ? 1024 : 256) add_norm_bwd(AddNormBwdAr
     Octet<RES16> sum[R], add[R];
     Octet<BF16> dy[R];
     float mean = 0.0f, rstd = 0.0f;
+    // a row behind the last reads as zeros
     auto fetch = [&](long long m) {
-        if (!a.rms) mean = a.mean[m];
-        rstd = a.rstd[m];
+        const bool in = m < a.M;
+        if (in && !a.rms) mean = a.mean[m];
+        rstd = in ? a.rstd[m] : 0.0f;
 #pragma unroll
         for (int k = 0; k < R; ++k) {
-            const int c = (l + k * Rw::lanes()) * 8;
-            sum[k].load(a.sum, m * a.C + c, a.C - c);
-            dy[k].load(a.dy, m * a.C + c, a.C - c);
-            if (a.dsum) add[k].load(a.dsum, m * a.C + c, a.C - c);
+            const int c = (l + k * lanes) * 8, n = in ? a.C - c : 0;
+            sum[k].load(a.sum, m * a.C + c, n);
+            dy[k].load(a.dy, m * a.C + c, n);
+            if (a.dsum) add[k].load(a.dsum, m * a.C + c, n);
         }
     };
-    long long m = (long long)blockIdx.x * Rw::kRows + Rw::row();
+    // base: the workgroup's first row, the same in every lane: no wave leaves the barriers early
+    long long base = (long long)blockIdx.x * rows;
     int turn = 0;
-    if (m < a.M) fetch(m);
-    for (; m < a.M; m += step) {
+    if (base < a.M) fetch(base + me.row());
+    for (; base < a.M; base += step) {
+        const long long m = base + me.row();
         float xhat[R][8], d[R][8], t[2] = {0.0f, 0.0f};
         const float r = rstd;
 #pragma unroll
         for (int k = 0; k < R; ++k) {
-            const int n = a.C - (l + k * Rw::lanes()) * 8;
+            const int n = m < a.M ? a.C - (l + k * lanes) * 8 : 0;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 xhat[k][j] = j < n ? (sum[k][j] - mean) * r : 0.0f;
@@ -273,13 +287,14 @@ __global__ void __launch_bounds__(L == 0 ? 1024 : 256) add_norm_bwd(AddNormBwdAr
         Octet<RES16> more[R];
 #pragma unroll
         for (int k = 0; k < R; ++k) more[k] = add[k];
-        if (m + step < a.M) fetch(m + step);
-        Rw::sum(t, slots[turn]);
+        if (base + step < a.M) fetch(m + step);
+        me.sum(t, slots[turn]);
         turn ^= 1;
+        if (m >= a.M) continue;
         const float s0 = a.rms ? 0.0f : t[0] * inv, s1 = t[1] * inv;
 #pragma unroll
         for (int k = 0; k < R; ++k) {
-            const int c = (l + k * Rw::lanes()) * 8;
+            const int c = (l + k * lanes) * 8;
             if (c >= a.C) continue;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -288,37 +303,36 @@ __global__ void __launch_bounds__(L == 0 ? 1024 : 256) add_norm_bwd(AddNormBwdAr
             }
             if (a.dresidual) store<RES16>(a.dresidual, m * a.C + c, a.C - c, d[k]);
             if (!a.dx) continue;
-            if (dropping) drop(d[k], a.drop, seed, offset + (unsigned long long)m * octets + l + k * Rw::lanes());
+            if (dropping) drop(d[k], a.drop, seed, offset + (unsigned long long)m * octets + l + k * lanes);
             store<BF16>(a.dx, m * a.C + c, a.C - c, d[k]);
         }
     }
     if (!part) return;
     float* p = part + (size_t)blockIdx.x * 2 * a.C;
-    if constexpr (L == 0) {
-#pragma unroll
-        for (int k = 0; k < R; ++k) {
-            const int c = (l + k * Rw::lanes()) * 8;
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (c + j < a.C) {
-                    p[c + j] = dw[k][j];
-                    p[a.C + c + j] = db[k][j];
-                }
-        }
-    } else {
-        // the workgroup's rows added in order; R = 1
+    if (rows > 1) {  // R = 1 there
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            joined[threadIdx.x * 16 + j] = dw[0][j];
-            joined[threadIdx.x * 16 + 8 + j] = db[0][j];
+            joined[(me.row() * 16 + j) * lanes + l] = dw[0][j];
+            joined[(me.row() * 16 + 8 + j) * lanes + l] = db[0][j];
         }
         __syncthreads();
-        for (int i = threadIdx.x; i < L * 16; i += 256) {
-            const int c = i / 16 * 8 + i % 8;
-            float s = 0.0f;
-            for (int q = 0; q < Rw::kRows; ++q) s += joined[q * L * 16 + i];
-            if (c < a.C) p[(i % 16 < 8 ? 0 : a.C) + c] = s;
+        for (int i = threadIdx.x; i < 16 * lanes; i += blockDim.x) {
+            float v = 0.0f;
+            for (int q = 0; q < rows; ++q) v += joined[q * 16 * lanes + i];
+            const int j = i / lanes, c = (i - j * lanes) * 8 + j % 8;
+            if (c < a.C) p[(j < 8 ? 0 : a.C) + c] = v;
         }
+        return;
+    }
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+        const int c = (l + k * lanes) * 8;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (c + j < a.C) {
+                p[c + j] = dw[k][j];
+                p[a.C + c + j] = db[k][j];
+            }
     }
 }
 
@@ -360,36 +374,40 @@ __global__ void __launch_bounds__(256) dropout_octets(DropoutArgs a, long long t
 }
 
 // ------------------------------------------------------------------ choices
-constexpr int kMostLanes = 2048 * 256;  // the GPU's
+constexpr int kCus = 256;
+constexpr int kFwdWaves = 12;                  // of a CU
+constexpr int kBwdWaves = 12, kBwdRounds = 2;  // of a CU; rows a lane at least
+// Lanes of a row: 16, or whole waves, up to 16 of them; two octets each beyond 1024 octets.
+int row_lanes(int C) {
+    const int octets = (C + 7) / 8, each = octets > 1024 ? 2 : 1;
+    return octets <= 16 ? 16 : ((octets + each - 1) / each + 63) / 64 * 64;
+}
 
-// Lanes of a workgroup, and rows it takes at once.
-struct Cut {
-    int lanes, rows;
-    Cut(int C) {
-        const int octets = (C + 7) / 8;
-        if (octets <= 16) lanes = 256, rows = 16;
-        else if (octets <= 64) lanes = 256, rows = 4;
-        else lanes = std::min((octets + 63) / 64 * 64, 1024), rows = 1;
-    }
-    // workgroups for M rows: at most fill times what the GPU holds at once
-    int groups(int M, int fill) const {
-        return (int)std::max<long long>(1, std::min<long long>(((long long)M + rows - 1) / rows, (long long)fill * kMostLanes / lanes));
-    }
-};
+// Workgroups of `rows` rows at once for M rows: at least `least` rounds each, and a whole number a
+// CU (all of them resident together: one that has to wait for another's end walks its rows alone).
+int groups(int M, int rows, int least, int a_cu) {
+    const long long most = std::max<long long>(1, ((long long)M + (long long)least * rows - 1) / ((long long)least * rows));
+    return (int)std::min<long long>(most, (long long)kCus * std::max(1, a_cu));
+}
 
-// Parts of dw and db: at least eight rows each, and no more than half of what the GPU holds.
+// Forward: one row of whole waves a workgroup, else 256 lanes.
+int fwd_lanes(int C) { return row_lanes(C) < 128 ? 256 : row_lanes(C); }
+int fwd_groups(int M, int C) { return groups(M, fwd_lanes(C) / row_lanes(C), 1, kFwdWaves * 64 / fwd_lanes(C)); }
+
+// Gradient: as many rows a workgroup as kBwdLanes hold; a part of dw and db each.
+int bwd_rows(int C) { return std::max(1, kBwdLanes / row_lanes(C)); }
 int parts(int M, int C) {
-    const Cut c(C);
-    const long long most = std::max<long long>(1, ((long long)M + 8LL * c.rows - 1) / (8LL * c.rows));
-    return (int)std::min<long long>(most, kMostLanes / 2 / c.lanes);
+    const int rows = bwd_rows(C);
+    const int lanes = rows * row_lanes(C);
+    return groups(M, rows, kBwdRounds, (kBwdWaves * 64 + lanes / 2) / lanes);
 }
 
 template <bool BF16, bool RES16>
 hipError_t fwd(const AddNormArgs& a, hipStream_t s) {
-    const Cut c(a.C);
-    const dim3 grid((unsigned)c.groups(a.M, 1)), block((unsigned)c.lanes);
-    if (c.rows == 16) launch((add_norm_fwd<BF16, RES16, 16, 1>), grid, block, 0, s, a);
-    else if (c.rows == 4) launch((add_norm_fwd<BF16, RES16, 64, 1>), grid, block, 0, s, a);
+    const dim3 grid((unsigned)fwd_groups(a.M, a.C)), block((unsigned)fwd_lanes(a.C));
+    const int lanes = row_lanes(a.C);
+    if (lanes == 16) launch((add_norm_fwd<BF16, RES16, 16, 1>), grid, block, 0, s, a);
+    else if (lanes == 64) launch((add_norm_fwd<BF16, RES16, 64, 1>), grid, block, 0, s, a);
     else if (a.C <= 8192) launch((add_norm_fwd<BF16, RES16, 0, 1>), grid, block, 0, s, a);
     else launch((add_norm_fwd<BF16, RES16, 0, 2>), grid, block, 0, s, a);
     return hipGetLastError();
@@ -397,12 +415,16 @@ hipError_t fwd(const AddNormArgs& a, hipStream_t s) {
 
 template <bool BF16, bool RES16>
 hipError_t bwd(const AddNormBwdArgs& a, float* part, int n, hipStream_t s) {
-    const Cut c(a.C);
-    const dim3 grid((unsigned)n), block((unsigned)c.lanes);
-    if (c.rows == 16) launch((add_norm_bwd<BF16, RES16, 16, 1>), grid, block, 0, s, a, part);
-    else if (c.rows == 4) launch((add_norm_bwd<BF16, RES16, 64, 1>), grid, block, 0, s, a, part);
-    else if (a.C <= 8192) launch((add_norm_bwd<BF16, RES16, 0, 1>), grid, block, 0, s, a, part);
-    else launch((add_norm_bwd<BF16, RES16, 0, 2>), grid, block, 0, s, a, part);
+    const int lanes = row_lanes(a.C), rows = bwd_rows(a.C), waves = lanes / 64;
+    const dim3 grid((unsigned)n), block((unsigned)(lanes * rows));
+    const uint32_t lds = rows > 1 ? 16 * lanes * rows * 4 : 0;
+    const bool two = a.C > 8192, large = lanes > kBwdLanes;
+    if (lanes == 16) launch((add_norm_bwd<BF16, RES16, 16, 1, kBwdLanes>), grid, block, lds, s, a, waves, part);
+    else if (lanes == 64) launch((add_norm_bwd<BF16, RES16, 64, 1, kBwdLanes>), grid, block, lds, s, a, waves, part);
+    else if (!two && !large) launch((add_norm_bwd<BF16, RES16, 0, 1, kBwdLanes>), grid, block, lds, s, a, waves, part);
+    else if (!two) launch((add_norm_bwd<BF16, RES16, 0, 1, 1024>), grid, block, lds, s, a, waves, part);
+    else if (!large) launch((add_norm_bwd<BF16, RES16, 0, 2, kBwdLanes>), grid, block, lds, s, a, waves, part);
+    else launch((add_norm_bwd<BF16, RES16, 0, 2, 1024>), grid, block, lds, s, a, waves, part);
     return hipGetLastError();
 }
 
@@ -434,7 +456,7 @@ hipError_t launch_dropout(const DropoutArgs& a, hipStream_t s) {
     const unsigned octets = ((unsigned)a.C + 7) / 8;
     const long long total = (long long)a.M * octets;
     if (total == 0) return hipSuccess;
-    const dim3 grid((unsigned)std::min<long long>((total + 255) / 256, kMostLanes / 256));
+    const dim3 grid((unsigned)std::min<long long>((total + 255) / 256, kCus * 32));
     if (a.bf16) launch((dropout_octets<true>), grid, dim3(256), 0, s, a, total, octets);
     else launch((dropout_octets<false>), grid, dim3(256), 0, s, a, total, octets);
     return hipGetLastError();
