@@ -706,17 +706,32 @@ def ssm_group_norm_bwd(x, groups, mean, rstd, dy, weight=None, bias=None, z=None
 
 
 # ------------------------------------------------------------------ gated linear recurrence
+def _run(fn, dev, stream, *args):
+    """fn(*args, stream handle) with the tensors' device current; its status."""
+    if dev.type == "cuda" and torch.cuda.current_device() == dev.index:
+        return fn(*args, _raw_stream(dev.index) if stream is None else stream.cuda_stream)
+    with _Launch(dev, stream) as s:
+        return fn(*args, s)
+
+
+def _new(like, shape, dtype, stream):
+    """An output tensor: ``like``'s kind where that is given (a contiguous tensor of the shape and
+    type wanted: the cheapest to make), on the launch stream."""
+    if stream is None:
+        return torch.empty_like(like) if shape is None else torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return _new(like, shape, dtype, None)
+
+
 SSM_GLR_FORM = {"decay": 0, "convex": 1}
 SSM_GLR_STATE_STEPS = 128
 
 
-def _strided(t, name, shape, dtype, device, required=True):
+def _strided(t, name, shape, dtype, device):
     """(address, row stride) of a tensor whose rows may be further apart than they are long (a
     slice of a projection's output): [B, L, D] or [B, D] with neighbouring channels neighbours in
     memory and every row as far from the next."""
     D = shape[-1]
-    if t is None and not required:
-        return None, D
     if type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and t.device == device:
         if t.is_contiguous():
             return t.data_ptr(), D
@@ -730,20 +745,21 @@ def _strided(t, name, shape, dtype, device, required=True):
             return t.data_ptr(), ld
         if t.numel():
             raise ValueError(f"{name} must have adjacent channels and evenly spaced rows, got strides {t.stride()}")
-    _check(t, name, shape, dtype, device, required)
+    _check(t, name, shape, dtype, device)
     return t.data_ptr(), D
 
 
 def _glr_inputs(x, r, i, A, z, form):
     """(form code, io code, addresses of x, r, i, A, z and the row strides) after checks."""
     form, code, dev, io, shape = SSM_GLR_FORM[form], _io_code(x), x.device, x.dtype, x.shape
-    if (form == 0) != (A is not None) or (form == 0) != (i is not None):
+    decay, D = form == 0, shape[-1]
+    if decay != (A is not None) or decay != (i is not None):
         raise ValueError("i and A are given exactly with form 'decay'")
-    rows = [_strided(t, n, shape, io, dev, need) for t, n, need in
-            ((x, "x", True), (r, "r", True), (i, "i", form == 0), (z, "z", False))]
-    Ap = _fits(A, "A", shape[-1:], torch.float32, dev, form == 0)
-    (xp, lx), (rp, lr), (ip, li), (zp, lz) = rows
-    D = shape[-1]
+    xp, lx = _strided(x, "x", shape, io, dev)
+    rp, lr = _strided(r, "r", shape, io, dev)
+    ip, li = _strided(i, "i", shape, io, dev) if decay else (None, D)
+    zp, lz = (None, D) if z is None else _strided(z, "z", shape, io, dev)
+    Ap = _fits(A, "A", (D,), torch.float32, dev) if decay else None
     ld = None if lx == lr == li == lz == D else (ctypes.c_int * 4)(lx, lr, li, lz)
     return form, code, (xp, rp, ip, Ap, zp, ld)
 
@@ -768,18 +784,18 @@ def ssm_glr_fwd(x, r, i=None, A=None, z=None, *, form="decay", seqlens=None, h0=
     lens, h0p = _fits(seqlens, "seqlens", (B,), torch.int32, dev, False), _fits(h0, "h0", (B, D), f32, dev, False)
     n = -(-L // SSM_GLR_STATE_STEPS)
     need = lib().ssm_glr_workspace_size(B, L, D)
-    with _on(stream):
-        if y is None:
-            y = torch.empty((B, L, D), dtype=io, device=dev)
-        if want_final_state and h_final is None:
-            h_final = torch.empty((B, D), dtype=f32, device=dev)
-        if want_states and states is None:
-            states = torch.empty((B, n, D), dtype=f32, device=dev)
-        workspace, wp, wbytes = _space(need, workspace, dev)
+    if y is None:
+        y = _new(x, (B, L, D), io, stream)
+    if want_final_state and h_final is None:
+        h_final = _new(x, (B, D), f32, stream)
+    if want_states and states is None:
+        states = _new(x, (B, n, D), f32, stream)
+    if workspace is None and need > 0:
+        workspace = _new(x, (need,), torch.uint8, stream)
+    workspace, wp, wbytes = _space(0, workspace, dev)
     out = (_fits(y, "y", (B, L, D), io, dev), _fits(h_final, "h_final", (B, D), f32, dev, False),
            _fits(states, "states", (B, n, D), f32, dev, False))
-    with _Launch(dev, stream) as s:
-        rc = lib().ssm_glr_fwd(B, L, D, code, form, *p, lens, h0p, *out, wp, wbytes, s)
+    rc = _run(lib().ssm_glr_fwd, dev, stream, B, L, D, code, form, *p, lens, h0p, *out, wp, wbytes)
     if rc != SSM_OK:
         _raise("ssm_glr_fwd", rc)
     return y, h_final, states
@@ -815,8 +831,7 @@ def ssm_glr_bwd(x, r, states, dy, i=None, A=None, z=None, *, form="decay", seqle
                 g[n] = torch.empty(sh, dtype=dt, device=dev)
             gp.append(_fits(g[n], n, sh, dt, dev, wanted))
         workspace, wp, wbytes = _space(need, workspace, dev)
-    with _Launch(dev, stream) as s:
-        rc = lib().ssm_glr_bwd(B, L, D, code, form, *p, lens, *ins, *gp, wp, wbytes, s)
+    rc = _run(lib().ssm_glr_bwd, dev, stream, B, L, D, code, form, *p, lens, *ins, *gp, wp, wbytes)
     if rc != SSM_OK:
         _raise("ssm_glr_bwd", rc)
     return g
@@ -832,11 +847,11 @@ def ssm_glr_step(state, x, r, i=None, A=None, z=None, *, form="decay", y=None, s
     form, code, p = _glr_inputs(x, r, i, A, z, form)
     sp = _fits(state, "state", (B, D), torch.float32, dev)
     if y is None:
-        with _on(stream):
-            y = torch.empty((B, D), dtype=io, device=dev)
-    yp = _fits(y, "y", (B, D), io, dev)
-    with _Launch(dev, stream) as s:
-        rc = lib().ssm_glr_step(B, D, code, form, sp, *p, yp, s)
+        y = _new(x, None if x.is_contiguous() else (B, D), io, stream)
+        yp = y.data_ptr()
+    else:
+        yp = _fits(y, "y", (B, D), io, dev)
+    rc = _run(lib().ssm_glr_step, dev, stream, B, D, code, form, sp, *p, yp)
     if rc != SSM_OK:
         _raise("ssm_glr_step", rc)
     return y
@@ -860,30 +875,31 @@ def ssm_add_norm_fwd(x, residual=None, weight=None, bias=None, *, eps=1e-5, norm
     "layer" ((s - mean) rstd) or "rms" (s rstd). x: [..., C] bf16 or fp32; residual: the same shape,
     fp32 or x's type; weight, bias: [C] fp32; p, rng: as for ``ssm_dropout``. y may be x, sum may be
     residual. Returns (y, sum, mean, rstd): sum in the residual's type (x itself where nothing is
-    added or dropped; None unless want_sum), mean (None for "rms") and rstd [...] fp32."""
+    added or dropped and y is not written over it; None unless want_sum), mean (None for "rms") and rstd [...] fp32."""
     M, C = _rows_dims(x, "x")
     dev, io, f32, shape = x.device, x.dtype, torch.float32, x.shape
     code, kind = _io_code(x), SSM_NORM[norm]
     given = residual if residual is not None else sum
     res = io if given is None else given.dtype
     rcode = code if given is None else _io_code(given)
-    ins = (_fits(x, "x", shape, io, dev), _fits(residual, "residual", shape, res, dev, False),
-           _fits(weight, "weight", (C,), f32, dev, False), _fits(bias, "bias", (C,), f32, dev, False))
-    rp = _fits(rng, "rng", (2,), torch.int64, dev, p != 0.0)
-    same = sum is None and residual is None and p == 0.0
-    with _on(stream):
-        if y is None:
-            y = torch.empty(shape, dtype=io, device=dev)
-        if sum is None and want_sum and not same:
-            sum = torch.empty(shape, dtype=res, device=dev)
-        if mean is None and kind == 0:
-            mean = torch.empty(shape[:-1], dtype=f32, device=dev)
-        if rstd is None:
-            rstd = torch.empty(shape[:-1], dtype=f32, device=dev)
-    out = (_fits(y, "y", shape, io, dev), _fits(sum, "sum", shape, res, dev, False),
-           _fits(mean, "mean", shape[:-1], f32, dev, False), _fits(rstd, "rstd", shape[:-1], f32, dev))
-    with _Launch(dev, stream) as s:
-        rc = lib().ssm_add_norm_fwd(M, C, code, rcode, kind, *ins, eps, p, rp, *out, s)
+    xp = _fits(x, "x", shape, io, dev)
+    ep = None if residual is None else _fits(residual, "residual", shape, res, dev)
+    wp = None if weight is None else _fits(weight, "weight", (C,), f32, dev)
+    bp = None if bias is None else _fits(bias, "bias", (C,), f32, dev)
+    rp = _fits(rng, "rng", (2,), torch.int64, dev) if p != 0.0 else None
+    # the sum is x, unless y is written over it
+    same = sum is None and residual is None and p == 0.0 and (y is None or y.data_ptr() != xp)
+    if y is None:
+        y = _new(x, None, io, stream)
+    if sum is None and want_sum and not same:
+        sum = _new(x, shape, res, stream) if residual is None else _new(residual, None, res, stream)
+    if mean is None and kind == 0:
+        mean = _new(x, shape[:-1], f32, stream)
+    if rstd is None:
+        rstd = _new(x, shape[:-1], f32, stream)
+    rc = _run(lib().ssm_add_norm_fwd, dev, stream, M, C, code, rcode, kind, xp, ep, wp, bp, eps, p, rp,
+              _fits(y, "y", shape, io, dev), None if sum is None else _fits(sum, "sum", shape, res, dev),
+              None if mean is None else _fits(mean, "mean", shape[:-1], f32, dev), _fits(rstd, "rstd", shape[:-1], f32, dev))
     if rc != SSM_OK:
         _raise("ssm_add_norm_fwd", rc)
     return y, (x if same and want_sum else sum), mean, rstd
@@ -905,7 +921,7 @@ def ssm_add_norm_bwd(sum, mean, rstd, dy, weight=None, dsum=None, *, norm="layer
     ins = (_fits(sum, "sum", shape, res, dev), _fits(weight, "weight", (C,), f32, dev, False),
            _fits(mean, "mean", shape[:-1], f32, dev, kind == 0), _fits(rstd, "rstd", shape[:-1], f32, dev),
            _fits(dy, "dy", shape, io, dev), _fits(dsum, "dsum", shape, res, dev, False))
-    rp = _fits(rng, "rng", (2,), torch.int64, dev, p != 0.0)
+    rp = _fits(rng, "rng", (2,), torch.int64, dev) if p != 0.0 else None
     g, gp = dict(out or {}), []
     need = lib().ssm_add_norm_bwd_workspace_size(M, C, code, rcode)
     with _on(stream):
@@ -917,8 +933,7 @@ def ssm_add_norm_bwd(sum, mean, rstd, dy, weight=None, dsum=None, *, norm="layer
                 g[n] = torch.empty(sh, dtype=dt, device=dev)
             gp.append(_fits(g[n], n, sh, dt, dev, wanted))
         workspace, wp, wbytes = _space(need, workspace, dev)
-    with _Launch(dev, stream) as s:
-        rc = lib().ssm_add_norm_bwd(M, C, code, rcode, kind, *ins, p, rp, *gp, wp, wbytes, s)
+    rc = _run(lib().ssm_add_norm_bwd, dev, stream, M, C, code, rcode, kind, *ins, p, rp, *gp, wp, wbytes)
     if rc != SSM_OK:
         _raise("ssm_add_norm_bwd", rc)
     return g
@@ -935,13 +950,11 @@ def ssm_dropout(x, p, rng=None, *, y=None, stream=None):
     (seed, offset), read when the kernel runs. On dy with the same rng it is the gradient. y may be x."""
     M, C = _rows_dims(x, "x")
     dev, io, shape, code = x.device, x.dtype, x.shape, _io_code(x)
-    xp, rp = _fits(x, "x", shape, io, dev), _fits(rng, "rng", (2,), torch.int64, dev, p != 0.0)
+    xp, rp = _fits(x, "x", shape, io, dev), _fits(rng, "rng", (2,), torch.int64, dev) if p != 0.0 else None
     if y is None:
-        with _on(stream):
-            y = torch.empty(shape, dtype=io, device=dev)
+        y = _new(x, None, io, stream)
     yp = _fits(y, "y", shape, io, dev)
-    with _Launch(dev, stream) as s:
-        rc = lib().ssm_dropout(M, C, code, xp, p, rp, yp, s)
+    rc = _run(lib().ssm_dropout, dev, stream, M, C, code, xp, p, rp, yp)
     if rc != SSM_OK:
         _raise("ssm_dropout", rc)
     return y

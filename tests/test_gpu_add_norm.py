@@ -188,6 +188,9 @@ def test_shapes_and_what_is_not_wanted():
     only = ssa.ssm_add_norm_bwd(s, mean, rstd, x3, d["w"], want_dx=False, want_dweight=False)
     assert only["dx"] is None and only["dweight"] is None and torch.equal(only["dresidual"], g["dx"])
     assert ssa.ssm_add_norm_fwd(x3, d["residual"].reshape(3, 4, 40), want_sum=False)[1] is None
+    over = x3.clone()
+    y4, s4, *_ = ssa.ssm_add_norm_fwd(over, weight=d["w"], y=over)
+    assert y4 is over and torch.equal(s4, x3) and torch.equal(y4, y)
     e = torch.empty((0, 40), dtype=BF16, device=DEV)
     y, s, mean, rstd = ssa.ssm_add_norm_fwd(e, weight=d["w"])
     g = ssa.ssm_add_norm_bwd(e, mean, rstd, e, d["w"])
