@@ -360,38 +360,23 @@ __global__ void __launch_bounds__(kThreads, 4) glr_bwd_tiles(GlrBwdArgs a, Cut c
     const Steps<V> at(in, b, tile * kTile + w * kSteps, me);
     const int ch = me.d - strip * 64;
     const bool mine = me.d < in.D;
-    Raw<BF16, V> x[T], r[T], i[T];
-    float e[T][V], f[T][V], ca[T][V], cu[T][V], A[V], P[V], H[V], C[V];  // dz of a step is f h
-    {
-        Raw<BF16, V> dy[T], z[T];
-        Rows<BF16, V, ONCE>(in.x, in.ldx, in.D, at.first, at.wave_live, me).load(x);
-        Rows<BF16, V, ONCE>(in.r, in.ldr, in.D, at.first, at.wave_live, me).load(r);
-        if constexpr (FORM == 0) Rows<BF16, V, ONCE>(in.i, in.ldi, in.D, at.first, at.wave_live, me).load(i);
-        Rows<BF16, V, ONCE>(a.dy, in.D, in.D, at.first, at.wave_live, me).load(dy);
-        if constexpr (GATE) Rows<BF16, V, ONCE>(in.z, in.ldz, in.D, at.first, at.wave_live, me).load(z);
+    Raw<BF16, V> x[T], r[T], i[T], dy[T], z[T];
+    float ca[T][V], cu[T][V], A[V], P[V], H[V], C[V];
+    Rows<BF16, V, ONCE>(in.x, in.ldx, in.D, at.first, at.wave_live, me).load(x);
+    Rows<BF16, V, ONCE>(in.r, in.ldr, in.D, at.first, at.wave_live, me).load(r);
+    if constexpr (FORM == 0) Rows<BF16, V, ONCE>(in.i, in.ldi, in.D, at.first, at.wave_live, me).load(i);
+    Rows<BF16, V, ONCE>(a.dy, in.D, in.D, at.first, at.wave_live, me).load(dy);
+    if constexpr (GATE) Rows<BF16, V, ONCE>(in.z, in.ldz, in.D, at.first, at.wave_live, me).load(z);
 #pragma unroll
-        for (int v = 0; v < V; ++v) A[v] = FORM == 0 ? in.A[min(me.d + v, in.D - 1)] : 0.0f;
+    for (int v = 0; v < V; ++v) A[v] = FORM == 0 ? in.A[min(me.d + v, in.D - 1)] : 0.0f;
 #pragma unroll
-        for (int t = 0; t < T; ++t) {
+    for (int t = 0; t < T; ++t) {
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                glr_coefficients<FORM>(x[t][v], r[t][v], FORM == 0 ? i[t][v] : 0.0f, A[v] * kLog2e, 2.0f * A[v], &ca[t][v],
-                                       &cu[t][v]);
-                e[t][v] = dy[t][v];
-                if constexpr (GATE) {
-                    const Sigmoid s(z[t][v]);
-                    const float es = e[t][v] * s.s;
-                    e[t][v] = z[t][v] * es;
-                    f[t][v] = __builtin_fmaf(e[t][v], s.om, es);
-                }
-            }
-            computed(ca[t]);
-            computed(cu[t]);
-            if constexpr (GATE) {
-                computed(e[t]);
-                computed(f[t]);
-            }
-        }
+        for (int v = 0; v < V; ++v)
+            glr_coefficients<FORM>(x[t][v], r[t][v], FORM == 0 ? i[t][v] : 0.0f, A[v] * kLog2e, 2.0f * A[v], &ca[t][v],
+                                   &cu[t][v]);
+        computed(ca[t]);
+        computed(cu[t]);
     }
     if (at.wave_live < kSteps)  // padding has u = 0 and dy = 0; state and gradient stay
 #pragma unroll
@@ -409,8 +394,9 @@ __global__ void __launch_bounds__(kThreads, 4) glr_bwd_tiles(GlrBwdArgs a, Cut c
         }
         C[v] = 0.0f;
 #pragma unroll
-        for (int t = T - 1; t >= 0; --t) C[v] = ca[t][v] * (C[v] + e[t][v]);
+        for (int t = T - 1; t >= 0; --t) C[v] = ca[t][v] * (C[v] + (GATE ? dy[t][v] * silu(z[t][v]) : dy[t][v]));
     }
+    computed(C);
     float Po[V], Ho[V], Co[V];  // of the lane with the other steps
     if constexpr (V == 1) {
         ownP[w][lane] = P[0];
@@ -451,23 +437,35 @@ __global__ void __launch_bounds__(kThreads, 4) glr_bwd_tiles(GlrBwdArgs a, Cut c
         start[lane] = group == 0 ? (a.dh_final ? a.dh_final[(size_t)b * in.D + dc] : 0.0f)
                                  : await_state(c.ends + ((size_t)b * c.groups + group - 1) * in.D + dc);
     // cu becomes the state before each step; dz needs the state alone
+    float h[V], e[T][V];  // e: dy [silu(z)]
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        float h = at.wave_live > 0 ? a.states[((size_t)b * c.tiles + tile) * in.D + min(me.d + v, in.D - 1)] : 0.0f;
-        for (int q = 0; q < w; ++q) h = __builtin_fmaf(ownP[q][ch + v], h, ownH[q][ch + v]);
-        if constexpr (V == 2) h = me.late ? __builtin_fmaf(Po[v], h, Ho[v]) : h;
-#pragma unroll
-        for (int t = 0; t < T; ++t) {
-            const float n = __builtin_fmaf(ca[t][v], h, cu[t][v]);
-            cu[t][v] = h;
-            h = n;
-            if constexpr (GATE) f[t][v] = at.wave_live == kSteps || t < at.live ? f[t][v] * h : 0.0f;
-        }
+        h[v] = at.wave_live > 0 ? a.states[((size_t)b * c.tiles + tile) * in.D + min(me.d + v, in.D - 1)] : 0.0f;
+        for (int q = 0; q < w; ++q) h[v] = __builtin_fmaf(ownP[q][ch + v], h[v], ownH[q][ch + v]);
+        if constexpr (V == 2) h[v] = me.late ? __builtin_fmaf(Po[v], h[v], Ho[v]) : h[v];
     }
-    if constexpr (GATE) {
-        const Rows<BF16, V, ONCE> oz(a.dz, in.D, in.D, at.first, at.wave_stored, me);
+    const Rows<BF16, V, ONCE> oz(GATE ? a.dz : a.dx, in.D, in.D, at.first, at.wave_stored, me);
 #pragma unroll
-        for (int t = 0; t < T; ++t) oz.store(t, f[t]);
+    for (int t = 0; t < T; ++t) {
+        float dz[V];
+        dy[t].anew();
+        if constexpr (GATE) z[t].anew();
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const float n = __builtin_fmaf(ca[t][v], h[v], cu[t][v]);
+            cu[t][v] = h[v];
+            h[v] = n;
+            if constexpr (GATE) {
+                const Sigmoid s(z[t][v]);
+                const float es = dy[t][v] * s.s;
+                e[t][v] = z[t][v] * es;
+                dz[v] = at.wave_live == kSteps || t < at.live ? __builtin_fmaf(e[t][v], s.om, es) * h[v] : 0.0f;
+            }
+        }
+        if constexpr (GATE) {
+            computed(e[t]);
+            oz.store(t, dz);
+        }
     }
     __syncthreads();
 
@@ -497,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 4) glr_bwd_tiles(GlrBwdArgs a, Cut c
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 const Sigmoid sr(r[t][v]);
-                g[v] += e[t][v];
+                g[v] += GATE ? e[t][v] : dy[t][v];
                 glr_gradient<FORM>(g[v], cu[t][v], ca[t][v], x[t][v], sr, FORM == 0 ? Sigmoid(i[t][v]) : sr, A[v], 2.0f * A[v],
                                    &dx[v], &dr[v], &di[v], &dl);
                 g[v] *= ca[t][v];
