@@ -241,7 +241,6 @@ __global__ void __launch_bounds__(kThreads, 4) glr_fwd_tiles(GlrArgs a, Cut c) {
         Rows<BF16, V, ONCE>(in.x, in.ldx, in.D, at.first, at.wave_live, me).load(x);
         Rows<BF16, V, ONCE>(in.r, in.ldr, in.D, at.first, at.wave_live, me).load(r);
         if constexpr (FORM == 0) Rows<BF16, V, ONCE>(in.i, in.ldi, in.D, at.first, at.wave_live, me).load(i);
-        if constexpr (GATE) Rows<BF16, V, ONCE>(in.z, in.ldz, in.D, at.first, at.wave_live, me).load(z);
         float A[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) A[v] = FORM == 0 ? in.A[min(me.d + v, in.D - 1)] : 0.0f;
@@ -281,6 +280,7 @@ __global__ void __launch_bounds__(kThreads, 4) glr_fwd_tiles(GlrArgs a, Cut c) {
             if (me.first()) own[w][ch + v] = make_float2(P[v] * Po[v], __builtin_fmaf(Po[v], H[v], Ho[v]));
         }
     }
+    if constexpr (GATE) Rows<BF16, V, ONCE>(in.z, in.ldz, in.D, at.first, at.wave_live, me).load(z);
     __syncthreads();
 
     const int group = tile / kGroup, first = group * kGroup;
