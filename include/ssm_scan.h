@@ -576,8 +576,8 @@ int ssm_group_norm_bwd(int M, int S, int C, int G, ssm_dtype_t io, ssm_act_t act
  * is gated by the input of every token. Per (b, d), from h = h0[b, d] (or 0), for
  * t = 0 .. len_b - 1, with sigma the logistic function:
  *   SSM_GLR_DECAY    a = exp(A[d] sigma(r[b,t,d])),  u = sqrt(1 - a^2) sigma(i[b,t,d]) x[b,t,d]
- *                    (the real-gated linear recurrent unit of De et al., "Griffin", 2024;
- *                    the factor keeps the state's variance that of the gated input)
+ *                    (the real-gated linear recurrent unit of De et al., arXiv
+ *                    2402.19427, 2024; the factor keeps the state's variance that of the gated input)
  *   SSM_GLR_CONVEX   a = 1 - sigma(r[b,t,d]),        u = sigma(r[b,t,d]) x[b,t,d]
  *                    (the minimal gated unit of Feng et al., "Were RNNs all we needed?", 2024)
  *   h = a h + u

@@ -1,16 +1,26 @@
 // Gated linear recurrence over whole sequences on gfx950, and its gradient:
 //   h_t = a_t h_{t-1} + u_t,   y = h [silu(z)],   g_t = dy_t [silu(z_t)] + a_{t+1} g_{t+1}
 //
-// Every element is read and written once; its gates cost 45 (forward) to 120 (gradient with
-// gate) vector instruction slots, about what the memory takes for its bytes, so neither can be
-// done twice. A workgroup has a tile of 64 channels (a lane each) by 128 steps (16 a wave); a
-// and u stay in registers from the load to the end. A piece of the sequence maps the state
-// entering it to h -> P h + H, and the maps of consecutive pieces compose: of a wave's steps in
-// registers, of the waves through LDS, of the tiles of a sequence through memory, from workgroup
-// to workgroup of the same launch. A tile leaves its map, then needs the maps of the tiles before
-// it: those of its group of 32 tiles, fetched by the eight waves in parallel, and the state at the
-// group's start, which the group before leaves. The order of all operations is fixed by the
-// shape, so results repeat bit for bit.
+// Bandwidth-bound: every element is read and written once, 8 bytes of bf16 forward (10 with the
+// gate), 14 (18) in the gradient, beside some 50 (65) and 125 (160) vector instruction slots, a
+// third to two thirds of the memory's time: a second pass over the data, or over its arithmetic,
+// would show. A workgroup has a tile of 64 channels by 128 steps, 16 a wave; a and u stay in
+// registers from the load to the end. A piece of the sequence maps the state entering it to
+// h -> P h + H, and the maps of consecutive pieces compose: of a lane's steps in registers, of the
+// waves through LDS, of the tiles of a sequence through memory, from workgroup to workgroup of
+// the same launch. A tile leaves its map, then needs the maps of the tiles before it: those of its
+// group of 32 tiles, fetched by the eight waves in parallel, and the state at the group's start,
+// which the group before leaves. The order of all operations is fixed by the shape, so results
+// repeat bit for bit.
+// Measured (with the launch that fills the words, and for the gradient the one that sums dA):
+// B8 L32768 D512 bf16 235 us (1.07 GB that have to move, 4.6 TB/s; a copy of that size reaches 4.9
+// to 5.1), B1 L4096 D1536 with gate 18 us (3 of them the fill), gradient of B4 L4096 D1536 with
+// gate 120 us (453 MB, 3.8 TB/s: two workgroups a CU, whose loads, waits and stores take turns;
+// counters show no byte moved twice), of B3 L2047 D1001 fp32 convex 30 us. Waiting costs nothing
+// that shows (a copy that does not wait takes as long); with one XCD of eight slower by 12 % the
+// others end that much earlier. Half as many or twice as many steps, wider strips, workgroups that
+// take tile after tile and maps looked at ahead of time were all slower, for the registers they
+// take or the lanes that wait.
 //
 // Waiting on other workgroups: a workgroup takes the next tile of its sequence from a counter, so
 // that the tiles it waits for belong to workgroups that run already, and the first unfinished
@@ -41,7 +51,7 @@ constexpr int kNonTemporal = 2;
 constexpr long long kCached = 256LL << 20;
 
 constexpr uint32_t kAbsent = 0xffffffffu;
-constexpr int kPolls = 1 << 22;
+constexpr int kPolls = 1 << 22;  // some seconds; a wait of this kernel's ends after microseconds
 
 typedef unsigned long long u64;
 typedef float f32x2 __attribute__((ext_vector_type(2)));

@@ -2,7 +2,8 @@
 //   h = a h + u,  y = h [silu(z)]
 // A handful of bytes an element (19 in bf16 with gate, 8 of them the state's) and no sums:
 // latency for one user's token, the bytes for a batch's. A lane takes four neighbouring channels
-// where rows hold whole fours, one otherwise.
+// where rows hold whole fours, one otherwise. Measured: B256 D2560 bf16 with gate 3.9 us, B1 D1536
+// 2.2 us (latency; the call's host side takes 8).
 #include "glr.h"
 #include "launch.h"
 

@@ -322,3 +322,26 @@ def test_a_residual_block(norm):
     torch.cuda.synchronize()
     for a, b, n in zip(got, want, ["x"] + ["w", "b", "inp", "A", "out"] * 2 + ["wf", "bf"]):
         assert float((a.double().cpu() - b).norm() / b.norm()) < 2e-4, n
+
+
+@pytest.mark.parametrize("C", [1, 7, 100, 129, 1001, 9001])
+@pytest.mark.parametrize("types", [(BF16, F32), (F32, F32), (BF16, BF16)], ids=str)
+def test_nothing_is_written_around_the_outputs(C, types):
+    M = 37
+    t = make(M, C, *types, seed=60)
+    d = {k: v.to(DEV) for k, v in t.items()}
+    r = rng_tensor()
+    y, s, mean, rstd = ssa.ssm_add_norm_fwd(d["x"], d["residual"], d["w"], d["b"], p=0.2, rng=r)
+    g = ssa.ssm_add_norm_bwd(s, mean, rstd, d["dy"], d["w"], d["dsum"], p=0.2, rng=r)
+    want = dict(y=y, sum=s, mean=mean, rstd=rstd, **g, drop=ssa.ssm_dropout(d["x"], 0.2, r))
+    bufs = {n: torch.full((v.numel() + 128,), 7.0, dtype=v.dtype, device=DEV) for n, v in want.items()}
+    out = {n: b[64:64 + want[n].numel()].view(want[n].shape) for n, b in bufs.items()}
+    ssa.ssm_add_norm_fwd(d["x"], d["residual"], d["w"], d["b"], p=0.2, rng=r,
+                         **{n: out[n] for n in ("y", "sum", "mean", "rstd")})
+    ssa.ssm_add_norm_bwd(s, mean, rstd, d["dy"], d["w"], d["dsum"], p=0.2, rng=r,
+                         out={n: out[n] for n in ("dx", "dresidual", "dweight", "dbias")})
+    ssa.ssm_dropout(d["x"], 0.2, r, y=out["drop"])
+    torch.cuda.synchronize()
+    for n, b in bufs.items():
+        assert (b[:64] == 7).all() and (b[64 + want[n].numel():] == 7).all(), n
+        assert torch.equal(out[n], want[n]), n

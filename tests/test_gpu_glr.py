@@ -347,3 +347,49 @@ def test_outputs_of_the_caller_and_what_is_not_wanted():
     g2 = bwd(d, states, "decay", out=out, want_dh0=False)
     torch.cuda.synchronize()
     assert torch.equal(y, buf) and g2["dx"] is out["dx"] and torch.equal(g["dx"], g2["dx"]) and g2["dh0"] is None
+
+
+@pytest.mark.parametrize("D", [36, 65, 130])
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+def test_nothing_is_written_around_the_outputs_and_nothing_read_between_the_rows(D, dtype):
+    """Every output lies between guards; every input is a slice of rows whose rest is NaN, at an
+    odd and at an even place."""
+    B, L = 2, 333
+    t = ref.glr_inputs(B, L, D, dtype, "decay", seed=50)
+    d = to(t)
+    s = [L, 200]
+    y, h, states = fwd(d, "decay", s)
+    want = dict(y=y, h_final=h, states=states, **bwd(d, states, "decay", s))
+    for at in (3, 8):
+        wide = {n: torch.full((B, L, D + 16), float("nan"), dtype=dtype, device=DEV) for n in ("x", "r", "i", "z")}
+        e = dict(d)
+        for n, v in wide.items():
+            v[..., at:at + D] = d[n]
+            e[n] = v[..., at:at + D]
+        bufs = {n: torch.full((v.numel() + 128,), 7.0, dtype=v.dtype, device=DEV) for n, v in want.items()}
+        out = {n: b[64:64 + want[n].numel()].view(want[n].shape) for n, b in bufs.items()}
+        fwd(e, "decay", s, y=out["y"], h_final=out["h_final"], states=out["states"])
+        bwd(e, out["states"], "decay", s, out={n: out[n] for n in ("dx", "dr", "di", "dA", "dz", "dh0")})
+        torch.cuda.synchronize()
+        for n, b in bufs.items():
+            assert (b[:64] == 7).all() and (b[64 + want[n].numel():] == 7).all(), n
+            # strided rows that are no pairs take the single-channel kernels, whose sums run in
+            # another order: equal to a rounding of the fp32 values behind them, in storage to a step
+            a, c = out[n].double(), want[n].double()
+            tol = torch.finfo(want[n].dtype).eps * c.abs() + 2.0 ** -17 * c.abs().mean()
+            assert ((a - c).abs() <= tol).all(), n
+
+
+@pytest.mark.parametrize("form", FORMS)
+def test_a_sequence_in_two_parts(form):
+    t = ref.glr_inputs(2, 900, 50, F32, form, seed=51)
+    g = ref.Glr(t, form)
+    d = to(t)
+    for cut in (1, 128, 517, 899):
+        a, b = ({n: v[:, sl].contiguous() if n in ("x", "r", "i", "z", "dy") and v is not None else v for n, v in d.items()}
+                for sl in (slice(0, cut), slice(cut, None)))
+        y1, h1, _ = fwd(a, form)
+        y2, h2, _ = fwd(dict(b, h0=h1), form)
+        torch.cuda.synchronize()
+        ref.close(torch.cat([y1, y2], 1), g.y, 2 * g.ey, 1.0, f"y cut at {cut}", store=F32)
+        ref.close(h2, g.h_final, 2 * g.eh_final, 1.0, f"h_final cut at {cut}", store=F32)
