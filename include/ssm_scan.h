@@ -601,7 +601,7 @@ int ssm_group_norm_bwd(int M, int S, int C, int G, ssm_dtype_t io, ssm_act_t act
  *   workspace  : at least ssm_glr_workspace_size(B, L, D) bytes, for one call at a time
  * Arithmetic: fp32; 1 - a^2 by a series where a is close to 1.
  * A value that is not finite stays in its channel and sequence, from its own step on.
- * Supported: B <= 65535; L <= 2^30; D <= 2^18; ld in [D, 2^20]; B ceil(L / 128) ceil(D / 64)
+ * Supported: B <= 65535; L <= 2^30; D <= 2^18; ld in [D, 2^24]; B ceil(L / 128) ceil(D / 64)
  * <= 2^30. x, r, i and z must be aligned to their element, every other pointer to 16 bytes.
  * Outputs must not alias inputs or each other (the same address is refused). Errors as for
  * ssm_scan_fwd.
@@ -656,8 +656,8 @@ int ssm_glr_bwd(int B, int L, int D, ssm_dtype_t io, ssm_glr_form_t form,
  *   state      : [B, D]  fp32, updated in place
  *   x, r, i, z : [B, D]  io dtype, rows ld[0..3] elements apart (ld NULL: D each)
  *   y          : [B, D]  io dtype out
- * Supported: B * D <= 2^30. Sizes, alignment and errors otherwise as for ssm_glr_fwd; y and
- * state must not alias each other or another argument.
+ * Supported: B * D <= 2^30; any ld >= D. Sizes, alignment and errors otherwise as for
+ * ssm_glr_fwd; y and state must not alias each other or another argument.
  * ------------------------------------------------------------------------- */
 int ssm_glr_step(int B, int D, ssm_dtype_t io, ssm_glr_form_t form,
                  float* state, const void* x, const void* r, const void* i, const float* A,

@@ -485,14 +485,15 @@ bool group_norm_dims_ok(int M, int S, int C, int G, int io) {
            product_ok({M, S}, 1LL << 30) && product_ok({M, G}, 1LL << 30) && product_ok({M, S, C}, 1LL << 38);
 }
 
-// Sizes and inputs of the gated linear recurrence; SSM_OK with *in filled, or the failure.
 bool glr_dims_ok(int B, int L, int D) {
     return B >= 1 && B <= 65535 && L >= 0 && L <= (1 << 30) && D >= 1 && D <= (1 << 18) &&
            product_ok({B, ((long long)L + 127) / 128, (D + 63) / 64}, 1LL << 30);
 }
 
+// Sizes and inputs of the gated linear recurrence, rows at most `most` elements apart; SSM_OK with
+// *in filled, or the failure.
 int glr_inputs(const char* fn, int B, int L, int D, int io, int form, const void* x, const void* r, const void* i,
-               const float* A, const void* z, const int* ld, const int* seqlens, ssm::GlrIn* in) {
+               const float* A, const void* z, const int* ld, int most, const int* seqlens, ssm::GlrIn* in) {
     if (B < 1 || L < 0 || D < 1) return fail(SSM_ERR_INVALID_ARG, fn, "B, D must be >= 1 and L >= 0");
     if (io != SSM_F32 && io != SSM_BF16) return fail(SSM_ERR_INVALID_ARG, fn, "io must be SSM_F32 or SSM_BF16");
     if (form != SSM_GLR_DECAY && form != SSM_GLR_CONVEX)
@@ -515,7 +516,7 @@ int glr_inputs(const char* fn, int B, int L, int D, int io, int form, const void
             return fail(SSM_ERR_INVALID_ARG, fn, "x, r, i and z must be aligned to their element");
         if (!ld) continue;
         if (ld[k] < D) return fail(SSM_ERR_INVALID_ARG, fn, "a row stride must be >= D");
-        if (ld[k] > (1 << 20)) return fail(SSM_ERR_UNSUPPORTED, fn, "a row stride must be <= 2^20");
+        if (ld[k] > most) return fail(SSM_ERR_UNSUPPORTED, fn, "a row stride must be <= 2^24");
         strides[k] = ld[k];
     }
     if (!aligned16(A) || !aligned16(seqlens))
@@ -713,7 +714,7 @@ int ssm_glr_fwd(int B, int L, int D, ssm_dtype_t io, ssm_glr_form_t form,
                 void* workspace, size_t workspace_bytes, void* stream) {
     const char* fn = "ssm_glr_fwd";
     ssm::GlrArgs a{};
-    const int s = glr_inputs(fn, B, L, D, io, form, x, r, i, A, z, ld, seqlens, &a.in);
+    const int s = glr_inputs(fn, B, L, D, io, form, x, r, i, A, z, ld, 1 << 24, seqlens, &a.in);
     if (s != SSM_OK) return s;
     if (L > 0 && !y) return fail(SSM_ERR_INVALID_ARG, fn, "y is required");
     const void* ptrs[] = {h0, y, h_final, states, workspace};
@@ -745,7 +746,7 @@ int ssm_glr_bwd(int B, int L, int D, ssm_dtype_t io, ssm_glr_form_t form,
                 void* workspace, size_t workspace_bytes, void* stream) {
     const char* fn = "ssm_glr_bwd";
     ssm::GlrBwdArgs a{};
-    const int s = glr_inputs(fn, B, L, D, io, form, x, r, i, A, z, ld, seqlens, &a.in);
+    const int s = glr_inputs(fn, B, L, D, io, form, x, r, i, A, z, ld, 1 << 24, seqlens, &a.in);
     if (s != SSM_OK) return s;
     if (L > 0 && (!states || !dy || !dx || !dr))
         return fail(SSM_ERR_INVALID_ARG, fn, "states, dy, dx and dr are required");
@@ -779,7 +780,7 @@ int ssm_glr_step(int B, int D, ssm_dtype_t io, ssm_glr_form_t form,
                  const void* z, const int* ld, void* y, void* stream) {
     const char* fn = "ssm_glr_step";
     ssm::GlrStepArgs a{};
-    const int s = glr_inputs(fn, B, 1, D, io, form, x, r, i, A, z, ld, nullptr, &a.in);
+    const int s = glr_inputs(fn, B, 1, D, io, form, x, r, i, A, z, ld, std::numeric_limits<int>::max(), nullptr, &a.in);
     if (s != SSM_OK) return s;
     if (!state || !y) return fail(SSM_ERR_INVALID_ARG, fn, "state and y are required");
     if (!product_ok({B, D}, 1LL << 30)) return fail(SSM_ERR_UNSUPPORTED, fn, "B * D must be <= 2^30");

@@ -715,12 +715,20 @@ def _run(fn, dev, stream, *args):
 
 
 def _new(like, shape, dtype, stream):
-    """An output tensor: ``like``'s kind where that is given (a contiguous tensor of the shape and
-    type wanted: the cheapest to make), on the launch stream."""
+    """An output tensor: ``like``'s kind where no shape is given (a contiguous tensor of the shape
+    and type wanted: the cheapest to make), on the launch stream."""
     if stream is None:
         return torch.empty_like(like) if shape is None else torch.empty(shape, dtype=dtype, device=like.device)
     with torch.cuda.stream(stream):
         return _new(like, shape, dtype, None)
+
+
+def _output(t, name, like, shape, dtype, stream, whole=False):
+    """(tensor, address): the caller's output after checks, or a new one (``whole``: as ``like``)."""
+    if t is None:
+        t = _new(like, None if whole else shape, dtype, stream)
+        return t, t.data_ptr()
+    return t, _fits(t, name, shape, dtype, like.device)
 
 
 SSM_GLR_FORM = {"decay": 0, "convex": 1}
@@ -741,7 +749,7 @@ def _strided(t, name, shape, dtype, device):
                 if rows == 1:
                     ld = s
                 even, rows = even and s == ld * rows, rows * n
-        if even and ld >= D:
+        if even and D <= ld < 2 ** 31:
             return t.data_ptr(), ld
         if t.numel():
             raise ValueError(f"{name} must have adjacent channels and evenly spaced rows, got strides {t.stride()}")
@@ -784,18 +792,16 @@ def ssm_glr_fwd(x, r, i=None, A=None, z=None, *, form="decay", seqlens=None, h0=
     lens, h0p = _fits(seqlens, "seqlens", (B,), torch.int32, dev, False), _fits(h0, "h0", (B, D), f32, dev, False)
     n = -(-L // SSM_GLR_STATE_STEPS)
     need = lib().ssm_glr_workspace_size(B, L, D)
-    if y is None:
-        y = _new(x, (B, L, D), io, stream)
-    if want_final_state and h_final is None:
-        h_final = _new(x, (B, D), f32, stream)
-    if want_states and states is None:
-        states = _new(x, (B, n, D), f32, stream)
+    hp = sp = None
+    y, yp = _output(y, "y", x, (B, L, D), io, stream, x.is_contiguous())
+    if want_final_state or h_final is not None:
+        h_final, hp = _output(h_final, "h_final", x, (B, D), f32, stream)
+    if want_states or states is not None:
+        states, sp = _output(states, "states", x, (B, n, D), f32, stream)
     if workspace is None and need > 0:
         workspace = _new(x, (need,), torch.uint8, stream)
     workspace, wp, wbytes = _space(0, workspace, dev)
-    out = (_fits(y, "y", (B, L, D), io, dev), _fits(h_final, "h_final", (B, D), f32, dev, False),
-           _fits(states, "states", (B, n, D), f32, dev, False))
-    rc = _run(lib().ssm_glr_fwd, dev, stream, B, L, D, code, form, *p, lens, h0p, *out, wp, wbytes)
+    rc = _run(lib().ssm_glr_fwd, dev, stream, B, L, D, code, form, *p, lens, h0p, yp, hp, sp, wp, wbytes)
     if rc != SSM_OK:
         _raise("ssm_glr_fwd", rc)
     return y, h_final, states
@@ -846,11 +852,7 @@ def ssm_glr_step(state, x, r, i=None, A=None, z=None, *, form="decay", y=None, s
     dev, io = x.device, x.dtype
     form, code, p = _glr_inputs(x, r, i, A, z, form)
     sp = _fits(state, "state", (B, D), torch.float32, dev)
-    if y is None:
-        y = _new(x, None if x.is_contiguous() else (B, D), io, stream)
-        yp = y.data_ptr()
-    else:
-        yp = _fits(y, "y", (B, D), io, dev)
+    y, yp = _output(y, "y", x, (B, D), io, stream, x.is_contiguous())
     rc = _run(lib().ssm_glr_step, dev, stream, B, D, code, form, sp, *p, yp)
     if rc != SSM_OK:
         _raise("ssm_glr_step", rc)
@@ -889,17 +891,14 @@ def ssm_add_norm_fwd(x, residual=None, weight=None, bias=None, *, eps=1e-5, norm
     rp = _fits(rng, "rng", (2,), torch.int64, dev) if p != 0.0 else None
     # the sum is x, unless y is written over it
     same = sum is None and residual is None and p == 0.0 and (y is None or y.data_ptr() != xp)
-    if y is None:
-        y = _new(x, None, io, stream)
-    if sum is None and want_sum and not same:
-        sum = _new(x, shape, res, stream) if residual is None else _new(residual, None, res, stream)
-    if mean is None and kind == 0:
-        mean = _new(x, shape[:-1], f32, stream)
-    if rstd is None:
-        rstd = _new(x, shape[:-1], f32, stream)
-    rc = _run(lib().ssm_add_norm_fwd, dev, stream, M, C, code, rcode, kind, xp, ep, wp, bp, eps, p, rp,
-              _fits(y, "y", shape, io, dev), None if sum is None else _fits(sum, "sum", shape, res, dev),
-              None if mean is None else _fits(mean, "mean", shape[:-1], f32, dev), _fits(rstd, "rstd", shape[:-1], f32, dev))
+    sp = mp = None
+    y, yp = _output(y, "y", x, shape, io, stream, True)
+    if sum is not None or (want_sum and not same):
+        sum, sp = _output(sum, "sum", x if residual is None else residual, shape, res, stream, residual is not None)
+    if mean is not None or kind == 0:
+        mean, mp = _output(mean, "mean", x, shape[:-1], f32, stream)
+    rstd, dp = _output(rstd, "rstd", x, shape[:-1], f32, stream)
+    rc = _run(lib().ssm_add_norm_fwd, dev, stream, M, C, code, rcode, kind, xp, ep, wp, bp, eps, p, rp, yp, sp, mp, dp)
     if rc != SSM_OK:
         _raise("ssm_add_norm_fwd", rc)
     return y, (x if same and want_sum else sum), mean, rstd
@@ -951,9 +950,7 @@ def ssm_dropout(x, p, rng=None, *, y=None, stream=None):
     M, C = _rows_dims(x, "x")
     dev, io, shape, code = x.device, x.dtype, x.shape, _io_code(x)
     xp, rp = _fits(x, "x", shape, io, dev), _fits(rng, "rng", (2,), torch.int64, dev) if p != 0.0 else None
-    if y is None:
-        y = _new(x, None, io, stream)
-    yp = _fits(y, "y", shape, io, dev)
+    y, yp = _output(y, "y", x, shape, io, stream, True)
     rc = _run(lib().ssm_dropout, dev, stream, M, C, code, xp, p, rp, yp)
     if rc != SSM_OK:
         _raise("ssm_dropout", rc)

@@ -224,6 +224,18 @@ def test_steps_continue_a_sequence(B, D, gate, form, dtype):
     ref.close(state, g.h_final, g.eh_final, 1.0, "state", store=F32)
 
 
+def test_a_step_on_tokens_of_a_long_sequence():
+    """Rows 5 million elements apart."""
+    B, L, D = 2, 5000, 1024
+    g = torch.Generator(device=DEV).manual_seed(4)
+    x, r = (torch.randn((B, L, D), generator=g, device=DEV, dtype=BF16) for _ in range(2))
+    a, b = (torch.zeros((B, D), device=DEV) for _ in range(2))
+    y = ssa.ssm_glr_step(a, x[:, 77], r[:, 4321], form="convex")
+    y2 = ssa.ssm_glr_step(b, x[:, 77].contiguous(), r[:, 4321].contiguous(), form="convex")
+    torch.cuda.synchronize()
+    assert torch.equal(y, y2) and torch.equal(a, b)
+
+
 def test_the_gradient_is_the_difference_of_the_loss():
     """Along random directions, in fp32: (l(v + e d) - l(v - e d)) / 2 e against <gradient, d>. The
     loss is a sum of n products that are off by 2^-20 of their size at most, and its third
