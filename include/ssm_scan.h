@@ -707,7 +707,7 @@ int ssm_add_norm_fwd(int M, int C, ssm_dtype_t io, ssm_dtype_t res, ssm_norm_t n
  *   dweight, dbias  : [C]     fp32 out, each may be NULL (not written); given or not whether
  *                     weight and bias were
  *   workspace       : at least ssm_add_norm_bwd_workspace_size(M, C, io, res) bytes, for one
- *                     call at a time
+ *                     call at a time; not used (NULL) without dweight and dbias
  * Sums over rows run in a fixed order. But for dresidual and dsum, outputs must not alias
  * inputs or each other. M = 0 writes dweight = dbias = 0. Sizes and errors as for
  * ssm_add_norm_fwd.

@@ -841,7 +841,8 @@ int ssm_add_norm_bwd(int M, int C, ssm_dtype_t io, ssm_dtype_t res, ssm_norm_t n
     const void* ptrs[] = {sum, weight, mean, rstd, dy, dsum, dx, dresidual, dweight, dbias, workspace};
     for (const void* q : ptrs)
         if (!aligned16(q)) return fail(SSM_ERR_INVALID_ARG, fn, "every pointer must be 16-byte aligned");
-    const size_t need = ssm::add_norm_bwd_workspace_bytes(M, C, io == SSM_BF16, res == SSM_BF16);
+    const bool affine = dweight || dbias;
+    const size_t need = affine ? ssm::add_norm_bwd_workspace_bytes(M, C, io == SSM_BF16, res == SSM_BF16) : 0;
     if (need > 0 && (workspace == nullptr || workspace_bytes < need))
         return fail(SSM_ERR_WORKSPACE, fn, "workspace missing or smaller than ssm_add_norm_bwd_workspace_size()");
     if (shared_buffer({dx, dresidual, dweight, dbias}, {sum, weight, mean, rstd, dy, rng}) ||

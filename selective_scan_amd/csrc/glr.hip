@@ -637,8 +637,8 @@ size_t glr_workspace_bytes(int B, int L, int D) {
 
 size_t glr_bwd_workspace_bytes(int B, int L, int D) {
     size_t fill;
-    const Cut c = cut_of(B, L, D, nullptr, &fill);
-    return fill + (size_t)B * c.tiles * D * 4;
+    const size_t parts = (size_t)B * cut_of(B, L, D, nullptr, &fill).tiles;
+    return parts == 1 ? 0 : fill + parts * D * 4;
 }
 
 hipError_t launch_glr_fwd(const GlrArgs& a, hipStream_t s) {
@@ -655,16 +655,17 @@ hipError_t launch_glr_fwd(const GlrArgs& a, hipStream_t s) {
 
 hipError_t launch_glr_bwd(const GlrBwdArgs& a, hipStream_t s) {
     size_t fill;
-    const Cut c = cut_of(a.in.B, a.in.L, a.in.D, static_cast<char*>(a.ws), &fill);
+    Cut c = cut_of(a.in.B, a.in.L, a.in.D, static_cast<char*>(a.ws), &fill);
+    const long long parts = (long long)a.in.B * c.tiles;
+    if (parts == 1) c.part = a.dA;  // the whole sum
     hipError_t e = fill_words(a.ws, fill, s);
     if (e != hipSuccess) return e;
     if (!a.in.bf16) bwd<false, 1, false>(a, c, s);
     else if (!pairs(a.in)) bwd<true, 1, false>(a, c, s);
     else if (bytes(a.in, 5 + 2 * (a.in.i != nullptr) + 2 * (a.in.z != nullptr)) <= kCached) bwd<true, 2, false>(a, c, s);
     else bwd<true, 2, true>(a, c, s);
-    if ((e = hipGetLastError()) != hipSuccess || a.in.form != 0) return e;
-    launch(glr_sum_parts, dim3((unsigned)((a.in.D + 15) / 16)), dim3(256), 0, s, c.part, (long long)a.in.B * c.tiles,
-           a.in.D, a.dA);
+    if ((e = hipGetLastError()) != hipSuccess || a.in.form != 0 || parts == 1) return e;
+    launch(glr_sum_parts, dim3((unsigned)((a.in.D + 15) / 16)), dim3(256), 0, s, c.part, parts, a.in.D, a.dA);
     return hipGetLastError();
 }
 

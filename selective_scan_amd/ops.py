@@ -731,6 +731,22 @@ def _output(t, name, like, shape, dtype, stream, whole=False):
     return t, _fits(t, name, shape, dtype, like.device)
 
 
+def _outputs(given, like, stream, wanted):
+    """(dict, addresses) of a gradient's outputs (name, shape, dtype, whether wanted): the caller's
+    or new ones, None where not wanted."""
+    g, at = dict(given or {}), []
+    plain, own = like.is_contiguous(), like.shape
+    for name, shape, dtype, want in wanted:
+        if want:
+            g[name], p = _output(g.get(name), name, like, shape, dtype, stream,
+                                 plain and dtype is like.dtype and shape == own)
+            at.append(p)
+        else:
+            g[name] = None
+            at.append(None)
+    return g, at
+
+
 SSM_GLR_FORM = {"decay": 0, "convex": 1}
 SSM_GLR_STATE_STEPS = 128
 
@@ -825,18 +841,13 @@ def ssm_glr_bwd(x, r, states, dy, i=None, A=None, z=None, *, form="decay", seqle
     lens = _fits(seqlens, "seqlens", (B,), torch.int32, dev, False)
     ins = (_fits(states, "states", (B, -(-L // SSM_GLR_STATE_STEPS), D), f32, dev), _fits(dy, "dy", shape, io, dev),
            _fits(dh_final, "dh_final", (B, D), f32, dev, False))
-    g, gp = dict(out or {}), []
     need = lib().ssm_glr_bwd_workspace_size(B, L, D)
-    with _on(stream):
-        for n, sh, dt, wanted in (("dx", shape, io, True), ("dr", shape, io, True), ("di", shape, io, i is not None),
-                                  ("dA", (D,), f32, A is not None), ("dz", shape, io, z is not None),
-                                  ("dh0", (B, D), f32, want_dh0)):
-            if not wanted:
-                g[n] = None
-            elif g.get(n) is None:
-                g[n] = torch.empty(sh, dtype=dt, device=dev)
-            gp.append(_fits(g[n], n, sh, dt, dev, wanted))
-        workspace, wp, wbytes = _space(need, workspace, dev)
+    g, gp = _outputs(out, x, stream, (("dx", shape, io, True), ("dr", shape, io, True), ("di", shape, io, i is not None),
+                                      ("dA", (D,), f32, A is not None), ("dz", shape, io, z is not None),
+                                      ("dh0", (B, D), f32, want_dh0)))
+    if workspace is None and need > 0:
+        workspace = _new(x, (need,), torch.uint8, stream)
+    workspace, wp, wbytes = _space(0, workspace, dev)
     rc = _run(lib().ssm_glr_bwd, dev, stream, B, L, D, code, form, *p, lens, *ins, *gp, wp, wbytes)
     if rc != SSM_OK:
         _raise("ssm_glr_bwd", rc)
@@ -921,17 +932,12 @@ def ssm_add_norm_bwd(sum, mean, rstd, dy, weight=None, dsum=None, *, norm="layer
            _fits(mean, "mean", shape[:-1], f32, dev, kind == 0), _fits(rstd, "rstd", shape[:-1], f32, dev),
            _fits(dy, "dy", shape, io, dev), _fits(dsum, "dsum", shape, res, dev, False))
     rp = _fits(rng, "rng", (2,), torch.int64, dev) if p != 0.0 else None
-    g, gp = dict(out or {}), []
-    need = lib().ssm_add_norm_bwd_workspace_size(M, C, code, rcode)
-    with _on(stream):
-        for n, sh, dt, wanted in (("dx", shape, io, want_dx), ("dresidual", shape, res, want_dresidual),
-                                  ("dweight", (C,), f32, want_dweight), ("dbias", (C,), f32, want_dbias)):
-            if not wanted:
-                g[n] = None
-            elif g.get(n) is None:
-                g[n] = torch.empty(sh, dtype=dt, device=dev)
-            gp.append(_fits(g[n], n, sh, dt, dev, wanted))
-        workspace, wp, wbytes = _space(need, workspace, dev)
+    need = lib().ssm_add_norm_bwd_workspace_size(M, C, code, rcode) if want_dweight or want_dbias else 0
+    g, gp = _outputs(out, dy, stream, (("dx", shape, io, want_dx), ("dresidual", shape, res, want_dresidual),
+                                       ("dweight", (C,), f32, want_dweight), ("dbias", (C,), f32, want_dbias)))
+    if workspace is None and need > 0:
+        workspace = _new(dy, (need,), torch.uint8, stream)
+    workspace, wp, wbytes = _space(0, workspace, dev)
     rc = _run(lib().ssm_add_norm_bwd, dev, stream, M, C, code, rcode, kind, *ins, p, rp, *gp, wp, wbytes)
     if rc != SSM_OK:
         _raise("ssm_add_norm_bwd", rc)

@@ -11,6 +11,7 @@ import selective_scan_amd as ssa
 from selective_scan_amd import ops
 
 P = ctypes.c_void_p(0x10000)
+P2 = ctypes.c_void_p(0x40000)
 ODD = ctypes.c_void_p(0x10004)
 ODDER = ctypes.c_void_p(0x10001)
 
@@ -176,7 +177,7 @@ def add_norm_bwd(**kw):
     (dict(sum=None), 1), (dict(rstd=None), 1), (dict(dy=None), 1), (dict(dx=None), 1), (dict(mean=None), 1),
     (dict(norm=1), 1), (dict(dsum=ODD), 1), (dict(dres=ODD), 1), (dict(dx=P), 1), (dict(dres=P), 1),
     (dict(dx=ctypes.c_void_p(0x30000), dsum=ctypes.c_void_p(0x30000)), 1), (dict(dw=ctypes.c_void_p(0x20000)), 1),
-    (dict(ws=None, M=1000), 3), (dict(wsb=8, M=1000), 3)])
+    (dict(ws=None, M=1000, dw=P2), 3), (dict(wsb=8, M=1000, db=P2), 3)])
 def test_add_norm_bwd_rejects(kw, status):
     assert add_norm_bwd(**kw) == status
     assert ops.lib().ssm_last_error().startswith(b"ssm_add_norm_bwd: ")
