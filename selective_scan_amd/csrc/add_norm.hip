@@ -13,9 +13,9 @@
 // a 16-byte border (odd widths) are loaded as they lie; the last one of a row is taken value by
 // value where it is not whole.
 // Statistics and sums are fp32, the variance from squared distances to the mean.
-// Measured: 32768 x 1536 bf16 on an fp32 stream with dropout 119 us (604 MB, 5.1 TB/s, a copy's
-// rate), its gradient 151 us (805 MB, 5.3 TB/s), gradient of 4099 x 1001 fp32 24 us (82 MB, partly
-// in the memory-side cache; a second launch that sums the parts takes 4), 64 x 2048 3.6 us (the
+// Measured: 32768 x 1536 bf16 on an fp32 stream with dropout 115 us (604 MB, 5.2 TB/s, a copy's
+// rate), its gradient 152 us (805 MB, 5.3 TB/s), gradient of 4099 x 1001 fp32 23 us (82 MB, partly
+// in the memory-side cache; a second launch that sums the parts takes 4), 64 x 2048 3.2 us (the
 // call's host side 11), dropout alone of 32768 x 1536 bf16 33 us (201 MB; 6.2 TB/s, partly in the
 // cache). 12 waves a CU walk the rows: 18 or 24 of the forward's were slower (122, 124 us), in the
 // gradient 6 (186) and 15 (161); workgroups that do not all fit at once cost a quarter (201).
@@ -98,8 +98,10 @@ __device__ __forceinline__ void store(void* p, size_t i, int n, const float (&v)
 
 // Eight of a vector's values (missing: the vector is NULL; 0 behind its end).
 __device__ __forceinline__ void params(const float* p, int c, int n, float missing, float (&v)[8]) {
+    Octet<false> q;
+    if (p) q.load(p, c, n);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = j < n ? (p ? p[c + j] : missing) : 0.0f;
+    for (int j = 0; j < 8; ++j) v[j] = p ? q[j] : j < n ? missing : 0.0f;
 }
 
 // v where the octet's block keeps it, scaled; else 0.
@@ -124,6 +126,11 @@ struct Row {
     }
     __device__ __forceinline__ int lane() const { return threadIdx.x - row() * lanes(); }
 
+    template <int CTRL>
+    __device__ __forceinline__ static void exchange(float& v) {
+        v += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), CTRL, 0xf, 0xf, false));
+    }
+
     // Sums over the row's lanes, in every lane and in a fixed order. slots: 16 a value, another set
     // than the last call's, whose values waves that are behind may still read; that they have read
     // those of the call before it, they say at the last call's barrier. Every wave of the workgroup
@@ -131,9 +138,16 @@ struct Row {
     template <int N>
     __device__ __forceinline__ void sum(float (&v)[N], float (*slots)[16]) const {
 #pragma unroll
-        for (int k = 0; k < N; ++k)
-#pragma unroll
-            for (int f = 1; f < (L == 0 ? 64 : L); f <<= 1) v[k] += __shfl_xor(v[k], f);
+        for (int k = 0; k < N; ++k) {
+            exchange<0xb1>(v[k]);   // lanes 1, 0, 3, 2
+            exchange<0x4e>(v[k]);   // lanes 2, 3, 0, 1
+            exchange<0x141>(v[k]);  // 8 lanes mirrored
+            exchange<0x140>(v[k]);  // 16 lanes mirrored
+            if constexpr (L != 16) {
+                v[k] += __shfl_xor(v[k], 16);
+                v[k] += __shfl_xor(v[k], 32);
+            }
+        }
         if constexpr (L == 0) {
             const int wave = threadIdx.x >> 6, first = row() * waves;
             if ((threadIdx.x & 63) == 0)
@@ -398,7 +412,10 @@ int groups(int M, int rows, int least, int a_cu) {
 
 // Forward: one row of whole waves a workgroup, else 256 lanes.
 int fwd_lanes(int C) { return row_lanes(C) < 128 ? 256 : row_lanes(C); }
-int fwd_groups(int M, int C) { return groups(M, fwd_lanes(C) / row_lanes(C), 1, kFwdWaves * 64 / fwd_lanes(C)); }
+int fwd_groups(int M, int C) {
+    const int lanes = fwd_lanes(C);
+    return groups(M, lanes / row_lanes(C), 1, (kFwdWaves * 64 + lanes / 2) / lanes);
+}
 
 // Gradient: as many rows a workgroup as kBwdLanes hold; a part of dw and db each.
 int bwd_rows(int C) { return std::max(1, kBwdLanes / row_lanes(C)); }
