@@ -13,9 +13,9 @@
 // which the group before leaves. The order of all operations is fixed by the shape, so results
 // repeat bit for bit.
 // Measured (with the launch that fills the words, and for the gradient the one that sums dA):
-// B8 L32768 D512 bf16 235 us (1.07 GB that have to move, 4.6 TB/s; a copy of that size reaches 4.9
-// to 5.1), B1 L4096 D1536 with gate 18 us (3 of them the fill), gradient of B4 L4096 D1536 with
-// gate 120 us (453 MB, 3.8 TB/s: two workgroups a CU, whose loads, waits and stores take turns;
+// B8 L32768 D512 bf16 233 us (1.07 GB that have to move, 4.6 TB/s; a copy of that size reaches 4.9
+// to 5.1), B1 L4096 D1536 with gate 17.4 us (3 of them the fill), gradient of B4 L4096 D1536 with
+// gate 119 us (453 MB, 3.8 TB/s: two workgroups a CU, whose loads, waits and stores take turns;
 // counters show no byte moved twice), of B3 L2047 D1001 fp32 convex 30 us. Waiting costs nothing
 // that shows (a copy that does not wait takes as long); with one XCD of eight slower by 12 % the
 // others end that much earlier. Half as many or twice as many steps, wider strips, workgroups that
