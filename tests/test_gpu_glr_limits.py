@@ -1,0 +1,117 @@
+"""Gated linear recurrence at the ends of its range: more workgroups than one dimension of the
+grid takes (sequences of one token for 65535 batches; one channel over 2^29 steps, whose tiles
+wait for one another), and rows that are no whole pairs."""
+import pytest
+import torch
+
+import glr_ref as ref
+import selective_scan_amd as ssa
+import test_gpu_glr as base
+from gpu_util import DEV
+
+pytestmark = pytest.mark.gpu
+
+F32, BF16 = torch.float32, torch.bfloat16
+FOLD = 1 << 22  # workgroups in the grid's first dimension
+
+
+def normal(shape, seed):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    return torch.randn(shape, generator=g, device=DEV, dtype=BF16)
+
+
+def test_one_token_for_as_many_batches_as_there_may_be():
+    """Without a state before it a token's y is k x, dx = dy k, dr = dy x k (1 - k) and dh0 = (1 - k) dy,
+    k = sigmoid(r): each a product, off by what glr_ref.py says of the gates and 2^-22. Every element."""
+    B, D = 65535, 4160
+    assert B * (D // 64) > FOLD
+    print("inputs", flush=True)
+    x, r, dy = (normal((B, 1, D), s) for s in range(3))
+    print("forward", flush=True)
+    y, h, states = ssa.ssm_glr_fwd(x, r, form="convex", want_states=True)
+    torch.cuda.synchronize()
+    print("gradient", flush=True)
+    out = ssa.ssm_glr_bwd(x, r, states, dy, form="convex")
+    torch.cuda.synchronize()
+    assert out["di"] is out["dA"] is out["dz"] is None and int(states.count_nonzero()) == 0
+
+    def close(got, want, e, what):
+        tol = torch.finfo(got.dtype).eps / 2 * want.abs() * (1 + e) + e * want.abs() + torch.finfo(F32).tiny
+        worst = float(((got.double() - want).abs() / tol).max())
+        assert worst <= 1.0, (what, at, worst)
+
+    step = 4096
+    for at in range(0, B, step):
+        s = slice(at, at + step)
+        xs, rs, ds = (t[s, 0].double() for t in (x, r, dy))
+        k, om = torch.sigmoid(rs), torch.sigmoid(-rs)
+        e = ref.esig(rs) + 2.0 ** -22  # of k and of 1 - k
+        close(y[s, 0], k * xs, e, "y")
+        close(h[s], k * xs, e, "h_final")
+        close(out["dx"][s, 0], ds * k, e, "dx")
+        close(out["dr"][s, 0], ds * xs * k * om, 2 * e, "dr")
+        close(out["dh0"][s], om * ds, e, "dh0")
+
+
+def test_one_channel_over_more_tiles_than_one_dimension_of_the_grid_takes():
+    """2^22 + 6 tiles in one chain. The gates are half open (five deviations and more of r leave a
+    decay below 0.999, the mean of log a is -0.8), so that 3200 steps leave nothing of what a
+    window of the sequence does not know of the steps before and behind it."""
+    L, n, near = (1 << 29) + 700, 9600, 3200
+    assert -(-L // 128) > FOLD
+    print("inputs", flush=True)
+    x, r, dy = (normal((1, L, 1), 10 + s) for s in range(3))
+    print("forward", flush=True)
+    y, h, states = ssa.ssm_glr_fwd(x, r, form="convex", want_states=True)
+    torch.cuda.synchronize()
+    print("gradient", flush=True)
+    out = ssa.ssm_glr_bwd(x, r, states, dy, form="convex")
+    torch.cuda.synchronize()
+    assert all(torch.isfinite(v).all() for v in (y, h, states, out["dx"], out["dr"], out["dh0"]))
+    # tile 2^22 starts at step 2^29; the gradient takes its tiles from the end
+    for at in (0, (1 << 29) - n // 256 * 128, (L - n) // 128 * 128, 700 // 128 * 128, L // 2 // 128 * 128):
+        print(at, flush=True)
+        cut = lambda t: t[:, at:at + n].cpu()  # noqa: B023, E731
+        m = min(n, L - at)
+        t = dict(x=cut(x), r=cut(r), dy=cut(dy))
+        g = ref.Glr(t, "convex", None, t["dy"])
+        lo, hi = 0 if at == 0 else near, m if at + m == L else m - near
+        ref.close(cut(y)[:, lo:], g.y[:, lo:], g.ey[:, lo:], 1.0, f"y at {at}", store=BF16)
+        sl, got = slice(lo // 128, None), states[:, at // 128:(at + m + 127) // 128].cpu()
+        ref.close(got[:, sl], g.states[:, sl], g.estates[:, sl], 1.0, f"states at {at}", store=F32)
+        if at + m == L:
+            ref.close(h, g.h_final, g.eh_final, 1.0, "h_final", store=F32)
+        if at == 0:
+            ref.close(out["dh0"], *g.out["dh0"], 1.0, "dh0", store=F32)
+        for k in ("dx", "dr"):
+            v, e = g.out[k]
+            ref.close(cut(out[k])[:, lo:hi], v[:, lo:hi], e[:, lo:hi], 1.0, f"{k} at {at}", store=BF16)
+
+
+@pytest.mark.parametrize("form", ["decay", "convex"])
+def test_slices_at_odd_channels_are_the_same_to_the_bounds(form):
+    """bf16 rows that are no whole pairs take other lanes, which compose a wave's steps in another
+    order: other bits, to the same bounds as the contiguous call; the same slices, the same bits."""
+    B, L, D = 2, 700, 66
+    t = ref.glr_inputs(B, L, D, BF16, form, seed=73)
+    g = ref.Glr(t, form, None, t["dy"], t["dh_final"])
+    d = base.to(t)
+    e = dict(d)
+    for n in ("x", "r", "i", "z"):
+        if d[n] is not None:
+            wide = torch.zeros((B, L, D + 7), dtype=BF16, device=DEV)
+            wide[..., 3:3 + D] = d[n]
+            e[n] = wide[..., 3:3 + D]
+    first = None
+    for _ in range(2):
+        y, h, states = base.fwd(e, form)
+        out = base.bwd(e, states, form)
+        torch.cuda.synchronize()
+        ref.close(y, g.y, g.ey, 1.0, "y", store=BF16)
+        ref.close(h, g.h_final, g.eh_final, 1.0, "h_final", store=F32)
+        for n, (v, b) in g.out.items():
+            ref.close(out[n], v, b, 1.0, n, store=F32 if n in ("dA", "dh0") else BF16)
+        every = [y, h, states, *(out[n] for n in g.out)]
+        assert first is None or all(torch.equal(a, b) for a, b in zip(first, every))
+        first = every
