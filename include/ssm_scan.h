@@ -587,7 +587,7 @@ int ssm_group_norm_bwd(int M, int S, int C, int G, ssm_dtype_t io, ssm_act_t act
  *
  *   x, r, i, z : [B, L, D]  io dtype, rows ld[0..3] elements apart (i: given exactly with
  *                SSM_GLR_DECAY; z may be NULL: no gate)
- *   A          : [D]        fp32, finite and <= 0 (SSM_GLR_DECAY; else NULL)
+ *   A          : [D]        fp32, in [-2^100, 0] (SSM_GLR_DECAY; else NULL)
  *   ld         : HOST array of the row strides of x, r, i, z in elements (slices of one
  *                projection's rows; row t of batch b at (b L + t) ld), or NULL: D each. The
  *                entry of an absent tensor is not read.

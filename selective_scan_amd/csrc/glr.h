@@ -73,25 +73,25 @@ struct Sigmoid {
     }
 };
 
-// 1 - a^2 for a = exp(t / 2), t <= 0. Close to 0 the difference would cancel: there the
-// series of -expm1(t), whose next term is t^5 / 720 (4e-8 relative at t = -1/8). Beyond,
+// 1 - a^2 for a = exp(t), t <= 0. Close to 0 the difference would cancel: there the series of
+// -expm1(2 t), whose next term is (2 t)^5 / 720 of the first (4e-8 relative at t = -1/16). Beyond,
 // what the roundings of a leave is 1e-6 relative at most, where 1 - a^2 is still small.
 __device__ __forceinline__ float one_minus_square(float t, float a) {
-    float q = __builtin_fmaf(t, 1.0f / 120.0f, 1.0f / 24.0f);
-    q = __builtin_fmaf(t, q, 1.0f / 6.0f);
-    q = __builtin_fmaf(t, q, 0.5f);
-    q = __builtin_fmaf(t, q, 1.0f);
+    float q = __builtin_fmaf(t, 4.0f / 15.0f, 2.0f / 3.0f);
+    q = __builtin_fmaf(t, q, 4.0f / 3.0f);
+    q = __builtin_fmaf(t, q, 2.0f);
+    q = __builtin_fmaf(t, q, 2.0f);
     const float series = -t * q, difference = __builtin_fmaf(-a, a, 1.0f);
-    return t > -0.125f ? series : difference;
+    return t > -0.0625f ? series : difference;
 }
 
-// a and u of one element; FORM 0: A2 = A log2(e), At = 2 A.
+// a and u of one element; FORM 0: A2 = A log2(e).
 template <int FORM>
-__device__ __forceinline__ void glr_coefficients(float x, float r, float i, float A2, float At, float* a, float* u) {
+__device__ __forceinline__ void glr_coefficients(float x, float r, float i, float A2, float A, float* a, float* u) {
     if constexpr (FORM == 0) {
         const float sr = rcp_fast(1.0f + exp2_fast(-r * kLog2e)), si = rcp_fast(1.0f + exp2_fast(-i * kLog2e));
         *a = exp2_fast(A2 * sr);
-        *u = __builtin_amdgcn_sqrtf(one_minus_square(At * sr, *a)) * si * x;
+        *u = __builtin_amdgcn_sqrtf(one_minus_square(A * sr, *a)) * si * x;
     } else {
         // 1 - k cancels where k is close to 1: e k there
         const float e = exp2_fast(-r * kLog2e), k = rcp_fast(1.0f + e);
@@ -104,16 +104,17 @@ __device__ __forceinline__ void glr_coefficients(float x, float r, float i, floa
 // k: sigma(r), q: sigma(i).
 template <int FORM>
 __device__ __forceinline__ void glr_gradient(float g, float before, float a, float x, const Sigmoid& k, const Sigmoid& q,
-                                             float A, float At, float* dx, float* dr, float* di, float* dl) {
+                                             float A, float* dx, float* dr, float* di, float* dl) {
     if constexpr (FORM == 0) {
-        const float m2 = one_minus_square(At * k.s, a);
+        const float t = A * k.s, m2 = one_minus_square(t, a);
         // 1 / m; 0 where m is 0 (the limit of dr as the gate closes)
         const float rs = __builtin_amdgcn_rsqf(m2), rm = m2 > kTiny ? rs : 0.0f, gq = g * q.s, m = m2 * rm;
         *dx = gq * m;
         *di = *dx * x * q.om;
         const float w = a * (g * before - a * rm * gq * x);  // d / d(A s)
         *dl = w * k.s;
-        *dr = *dl * A * k.om;
+        // in this order what is too small for fp32 stays so: where |t| > 104, w is 0
+        *dr = w * k.om * t;
     } else {
         *dx = g * k.s;
         *dr = *dx * (x - before) * k.om;

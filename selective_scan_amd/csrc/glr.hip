@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, 4) glr_fwd_tiles(GlrArgs a, Cut c) {
         for (int t = 0; t < T; ++t) {
 #pragma unroll
             for (int v = 0; v < V; ++v)
-                glr_coefficients<FORM>(x[t][v], r[t][v], FORM == 0 ? i[t][v] : 0.0f, A[v] * kLog2e, 2.0f * A[v], &ca[t][v],
+                glr_coefficients<FORM>(x[t][v], r[t][v], FORM == 0 ? i[t][v] : 0.0f, A[v] * kLog2e, A[v], &ca[t][v],
                                        &cu[t][v]);
             computed(ca[t]);
             computed(cu[t]);
@@ -383,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 4) glr_bwd_tiles(GlrBwdArgs a, Cut c
     for (int t = 0; t < T; ++t) {
 #pragma unroll
         for (int v = 0; v < V; ++v)
-            glr_coefficients<FORM>(x[t][v], r[t][v], FORM == 0 ? i[t][v] : 0.0f, A[v] * kLog2e, 2.0f * A[v], &ca[t][v],
+            glr_coefficients<FORM>(x[t][v], r[t][v], FORM == 0 ? i[t][v] : 0.0f, A[v] * kLog2e, A[v], &ca[t][v],
                                    &cu[t][v]);
         computed(ca[t]);
         computed(cu[t]);
@@ -506,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, 4) glr_bwd_tiles(GlrBwdArgs a, Cut c
             for (int v = 0; v < V; ++v) {
                 const Sigmoid sr(r[t][v]);
                 g[v] += GATE ? e[t][v] : dy[t][v];
-                glr_gradient<FORM>(g[v], cu[t][v], ca[t][v], x[t][v], sr, FORM == 0 ? Sigmoid(i[t][v]) : sr, A[v], 2.0f * A[v],
+                glr_gradient<FORM>(g[v], cu[t][v], ca[t][v], x[t][v], sr, FORM == 0 ? Sigmoid(i[t][v]) : sr, A[v],
                                    &dx[v], &dr[v], &di[v], &dl);
                 g[v] *= ca[t][v];
                 if (!decltype(whole)::value && t >= at.live) dx[v] = dr[v] = di[v] = dl = 0.0f;

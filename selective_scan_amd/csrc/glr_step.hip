@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(kT) glr_step_kernel(GlrStepArgs a, unsigned n,
     for (int v = 0; v < V; ++v) {
         float c, u;
         glr_coefficients<FORM>(x[v], r[v], FORM == 0 ? i[v] : 0.0f, FORM == 0 ? A[v] * kLog2e : 0.0f,
-                               FORM == 0 ? 2.0f * A[v] : 0.0f, &c, &u);
+                               FORM == 0 ? A[v] : 0.0f, &c, &u);
         h[v] = __builtin_fmaf(c, h[v], u);
     }
     st<false>(a.state, at, h);

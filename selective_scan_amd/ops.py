@@ -797,7 +797,7 @@ def ssm_glr_fwd(x, r, i=None, A=None, z=None, *, form="decay", seqlens=None, h0=
     """Gated linear recurrence h_t = a_t h_{t-1} + u_t, y = h [silu(z)]. form "decay": a = exp(A
     sigmoid(r)), u = sqrt(1 - a^2) sigmoid(i) x; "convex" (without i and A): a = 1 - sigmoid(r), u =
     sigmoid(r) x. x, r, i, z: [B, L, D] bf16 or fp32, rows may be strided (slices of a projection);
-    A: [D] fp32, <= 0; seqlens: [B] int32, rows past a length are padding (y is 0 there); h0: [B, D]
+    A: [D] fp32, in [-2^100, 0]; seqlens: [B] int32, rows past a length are padding (y is 0 there); h0: [B, D]
     fp32. Returns (y [B, L, D], h_final [B, D] fp32, states), the last with ``want_states``: the
     state entering every 128th step, [B, ceil(L / 128), D] fp32, for ``ssm_glr_bwd``."""
     if x.dim() != 3:

@@ -1,6 +1,7 @@
 """Gated linear recurrence at the ends of its range: more workgroups than one dimension of the
 grid takes (sequences of one token for 65535 batches; one channel over 2^29 steps, whose tiles
-wait for one another), and rows that are no whole pairs."""
+wait for one another), rows that are no whole pairs, and
+decays from the fastest to none."""
 import pytest
 import torch
 
@@ -115,3 +116,36 @@ def test_slices_at_odd_channels_are_the_same_to_the_bounds(form):
         every = [y, h, states, *(out[n] for n in g.out)]
         assert first is None or all(torch.equal(a, b) for a, b in zip(first, every))
         first = every
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("gate", [True, False])
+@pytest.mark.parametrize("seqlens", [None, [300, 137]])
+def test_decays_from_the_fastest_to_none(dtype, gate, seqlens):
+    """A from -2^100 to 0, the gate around where A sigmoid(r) is -1 on half of the steps, anywhere
+    within 100 on the others. Beside the bounds of glr_ref.py: a below 2^-126 may be 0. Of dr that
+    loses |g| (|h_{t-1}| + |x|) a |A sigmoid(r)|, where the last is at most 104 (beyond, a is below
+    2^-149 and the product smaller still), and its own products as much again: 2^-126 104 (G H + 1)
+    with G the largest |g| that sums of |dy silu(z)| and |dh_final| allow and H the largest |h| + |x|."""
+    A = torch.tensor([-2.0 ** 100, -2.0 ** 64, -1e9, -300.0, -1.0, -1e-4, -1e-12, -1e-30, -1e-38, -1e-42, -0.0, 0.0])
+    D, L = len(A), 300
+    t = ref.glr_inputs(2, L, D, dtype, "decay", seed=71, gate=gate)
+    gen = torch.Generator().manual_seed(72)
+    around = (-A.abs().clamp(1e-20, 2.0 ** 100).log()).clamp(-80, 80) + 3 * torch.randn((2, L, D), generator=gen)
+    anywhere = 200 * torch.rand((2, L, D), generator=gen) - 100
+    t["r"] = torch.where(torch.rand((2, L, D), generator=gen) < 0.5, around, anywhere).to(dtype)
+    t["A"] = A
+    g = ref.Glr(t, "decay", seqlens, t["dy"], t["dh_final"])
+    d = base.to(t)
+    y, h, states = base.fwd(d, "decay", seqlens)
+    out = base.bwd(d, states, "decay", seqlens)
+    torch.cuda.synchronize()
+    ref.close(y, g.y, g.ey, 1.0, "y", store=dtype)
+    ref.close(h, g.h_final, g.eh_final, 1.0, "h_final", store=F32)
+    ref.close(states, g.states, g.estates, 1.0, "states", store=F32)
+    most = 1.0 if t["z"] is None else float(t["z"].abs().max())
+    G = float(t["dy"].double().abs().sum(1).max()) * most + float(t["dh_final"].abs().max())
+    H = float(g.magb.max()) + float(t["x"].abs().max())
+    for n, (v, e) in g.out.items():
+        e = e + 2.0 ** -126 * 104 * (G * H + 1) if n == "dr" else e
+        ref.close(out[n], v, e, 1.0, n, store=F32 if n in ("dA", "dh0") else dtype)
