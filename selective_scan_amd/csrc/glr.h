@@ -63,13 +63,13 @@ hipError_t launch_glr_step(const GlrStepArgs& a, hipStream_t stream);
 constexpr float kTiny = 1.17549435e-38f;  // smallest normal fp32
 
 // sigmoid(v) and 1 - sigmoid(v), the second to its own relative precision (e s, where
-// 1 - s would cancel); e is held below infinity, where s is 0 already.
+// 1 - s would cancel); e is held below infinity, where s is 0 (as it is from e = 2^126 on).
 struct Sigmoid {
     float s, om;
     __device__ __forceinline__ explicit Sigmoid(float v) {
         const float e = exp2_fast(-v * kLog2e);
         s = rcp_fast(1.0f + e);
-        om = __builtin_fminf(e, 8e37f) * s;
+        om = __builtin_fminf(e, __FLT_MAX__) * s;
     }
 };
 

@@ -149,3 +149,27 @@ def test_decays_from_the_fastest_to_none(dtype, gate, seqlens):
     for n, (v, e) in g.out.items():
         e = e + 2.0 ** -126 * 104 * (G * H + 1) if n == "dr" else e
         ref.close(out[n], v, e, 1.0, n, store=F32 if n in ("dA", "dh0") else dtype)
+
+
+def test_gates_whose_sigmoid_is_just_above_the_smallest_number():
+    """sigmoid(v) down to 2^-126 (v > -87.33), where 1 - sigmoid(v) is 1: dr of a decay that brings
+    sigmoid(r) back, and dz. Every value is a product (x and h0 of opposite signs: no difference in
+    dr either), off by the gates' exponents, 96 2^-23 each and twice in dr: 2^-14 holds all."""
+    D = 64
+    v = torch.linspace(-87.33, -87.2, D)
+    one = torch.ones((1, 1, D))
+    d = dict(x=-one, r=v.reshape(1, 1, D), i=0 * one, z=2 * one, dy=one, h0=torch.ones((1, D)), A=torch.full((D,), -2.0 ** 100))
+    d = {n: t.to(DEV) for n, t in d.items()}
+    states = ssa.ssm_glr_fwd(d["x"], d["r"], d["i"], d["A"], d["z"], h0=d["h0"], want_states=True)[2]
+    dr = ssa.ssm_glr_bwd(d["x"], d["r"], states, d["dy"], d["i"], d["A"], d["z"])["dr"]
+    s, g = torch.sigmoid(v.double()), 2 / (1 + torch.exp(torch.tensor(-2.0, dtype=torch.float64)))
+    la = -2.0 ** 100 * s
+    a, m = torch.exp(la), torch.sqrt(-torch.expm1(2 * la))
+    want = g * a * (1 + a * 0.5 / m) * la
+    assert float((dr[0, 0].double().cpu() / want - 1).abs().max()) < 2.0 ** -14
+
+    big = dict(d, r=0 * d["r"], z=v.reshape(1, 1, D).to(DEV), A=torch.full((D,), -1.0, device=DEV))
+    y, h, states = ssa.ssm_glr_fwd(big["x"], big["r"], big["i"], big["A"], big["z"], h0=d["h0"], want_states=True)
+    dz = ssa.ssm_glr_bwd(big["x"], big["r"], states, d["dy"], big["i"], big["A"], big["z"])["dz"]
+    want = h[0].double().cpu() * s * (1 + v.double())
+    assert float((dz[0, 0].double().cpu() / want - 1).abs().max()) < 2.0 ** -14
