@@ -33,6 +33,7 @@
 #include "launch.h"
 
 #include <algorithm>
+#include <initializer_list>
 
 namespace ssm {
 namespace {
@@ -42,12 +43,18 @@ constexpr int kPer = 4, kGroup = kWaves * kPer;  // maps a wave fetches; tiles o
 constexpr int kThreads = kWaves * 64;
 static_assert(kTile == kGlrStateSteps, "a tile starts where a state is kept");
 
-// Accesses that leave no lines behind in the L2. Stores of pairs: B4 L4096 D1536 gradient 130 -> 125 us,
-// B1 L4096 D1536 19.3 -> 18.4, and a pass over y behind it no slower. Loads of pairs where the call's
-// tensors outgrow the memory-side cache of 256 MiB: 125 -> 121 us, B8 L32768 D512 244 -> 235; within
-// it they cost (19.3 -> 21.2), and so they do where neighbouring strips share lines (B4 L16384 D1001
-// fp32 537 -> 688), which single channels therefore never use.
+// Accesses that leave no lines behind in the L2 (PAST 1: stores of pairs, 2: their loads as well).
+// Stores gain where every 64 bytes of a row belong to one strip: gradients of B4 L4096 D1536 130 ->
+// 127 us, B8 L16384 D96 91 -> 81..89, B8 L8192 D160 71 -> 63 (B4 L4096 D1504 133..138 either way); where
+// strips share them, a piece at a time goes to memory: B4 L4096 D1000 110 -> 160, D1502 162 -> 256.
+// Loads gain where the call's tensors outgrow the memory-side cache of 256 MiB and strips share no
+// line of 128 bytes: B8 L32768 D512 309 -> 300, its gradient 617 -> 595. Within the cache they cost
+// (B4 L4096 D1502 78 -> 101), and so do shared lines, fetched twice (B4 L16384 D480 88 -> 98, D1002
+// 202 -> 263, its gradient 563 -> 675). (All bf16 decay with gate.) Single channels use neither:
+// stores of fp32 gain 0 to 17 % on whole lines (B4 L16384 D1024 282 -> 267) and cost 16 % on shared
+// ones (gradient of D1001 728 -> 842).
 constexpr int kNonTemporal = 2;
+constexpr int kPiece = 64, kLine = 128;  // bytes
 constexpr long long kCached = 256LL << 20;
 
 constexpr uint32_t kAbsent = 0xffffffffu;
@@ -163,8 +170,8 @@ struct Raw {
 
 // A wave's rows of an io tensor through a buffer that ends behind the last of n rows: rows
 // further on read as 0 and are not written, and so does a lane whose channels do not exist (its
-// offset lies behind every buffer). One scalar addition a row. ONCE: loads leave no lines behind.
-template <bool BF16, int V, bool ONCE>
+// offset lies behind every buffer). One scalar addition a row.
+template <bool BF16, int V, int PAST>
 struct Rows {
     static constexpr int T = Share<V>::T;
     __amdgpu_buffer_rsrc_t buf;
@@ -183,13 +190,13 @@ struct Rows {
 #pragma unroll
         for (int t = 0; t < T; ++t) {
             if constexpr (BF16 && V == 1) v[t].w = __builtin_amdgcn_raw_buffer_load_b16(buf, (int)off, (int)(t * pitch), 0);
-            else v[t].w = __builtin_amdgcn_raw_buffer_load_b32(buf, (int)off, (int)(t * pitch), ONCE ? kNonTemporal : 0);
+            else v[t].w = __builtin_amdgcn_raw_buffer_load_b32(buf, (int)off, (int)(t * pitch), PAST > 1 ? kNonTemporal : 0);
         }
     }
     __device__ __forceinline__ void store(int t, const float (&v)[V]) const {
         if constexpr (V == 2) {
             const uint32_t w = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{v[0], v[1]}, bf16x2));
-            __builtin_amdgcn_raw_buffer_store_b32(w, buf, (int)off, (int)(t * pitch), kNonTemporal);
+            __builtin_amdgcn_raw_buffer_store_b32(w, buf, (int)off, (int)(t * pitch), PAST > 0 ? kNonTemporal : 0);
         } else {
             store_io<BF16>(buf, off, t * pitch, v[0]);
         }
@@ -228,7 +235,7 @@ __device__ __forceinline__ float entering(const float (&start)[64], const float2
 }
 
 // ------------------------------------------------------------------ forward
-template <bool BF16, int V, bool ONCE, int FORM, bool GATE>
+template <bool BF16, int V, int PAST, int FORM, bool GATE>
 __global__ void __launch_bounds__(kThreads, 4) glr_fwd_tiles(GlrArgs a, Cut c) {
     constexpr int T = Share<V>::T;
     __shared__ float2 own[kWaves][64], before[kWaves][64];
@@ -248,9 +255,9 @@ __global__ void __launch_bounds__(kThreads, 4) glr_fwd_tiles(GlrArgs a, Cut c) {
     Raw<BF16, V> z[T];
     {
         Raw<BF16, V> x[T], r[T], i[T];
-        Rows<BF16, V, ONCE>(in.x, in.ldx, in.D, at.first, at.wave_live, me).load(x);
-        Rows<BF16, V, ONCE>(in.r, in.ldr, in.D, at.first, at.wave_live, me).load(r);
-        if constexpr (FORM == 0) Rows<BF16, V, ONCE>(in.i, in.ldi, in.D, at.first, at.wave_live, me).load(i);
+        Rows<BF16, V, PAST>(in.x, in.ldx, in.D, at.first, at.wave_live, me).load(x);
+        Rows<BF16, V, PAST>(in.r, in.ldr, in.D, at.first, at.wave_live, me).load(r);
+        if constexpr (FORM == 0) Rows<BF16, V, PAST>(in.i, in.ldi, in.D, at.first, at.wave_live, me).load(i);
         float A[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) A[v] = FORM == 0 ? in.A[min(me.d + v, in.D - 1)] : 0.0f;
@@ -290,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 4) glr_fwd_tiles(GlrArgs a, Cut c) {
             if (me.first()) own[w][ch + v] = make_float2(P[v] * Po[v], __builtin_fmaf(Po[v], H[v], Ho[v]));
         }
     }
-    if constexpr (GATE) Rows<BF16, V, ONCE>(in.z, in.ldz, in.D, at.first, at.wave_live, me).load(z);
+    if constexpr (GATE) Rows<BF16, V, PAST>(in.z, in.ldz, in.D, at.first, at.wave_live, me).load(z);
     __syncthreads();
 
     const int group = tile / kGroup, first = group * kGroup;
@@ -327,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 4) glr_fwd_tiles(GlrArgs a, Cut c) {
             __hip_atomic_store(c.ends + ((size_t)b * c.groups + group) * in.D + me.d + v,
                                present(__builtin_fmaf(P[v], h[v], H[v])), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
-    const Rows<BF16, V, ONCE> out(a.y, in.D, in.D, at.first, at.wave_stored, me);
+    const Rows<BF16, V, PAST> out(a.y, in.D, in.D, at.first, at.wave_stored, me);
     auto sweep = [&](auto whole) {
 #pragma unroll
         for (int t = 0; t < T; ++t) {
@@ -352,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 4) glr_fwd_tiles(GlrArgs a, Cut c) {
 // Tiles are taken from the last to the first. The map of a piece on the gradient leaving it at
 // its end to that at its start is g -> P g + C. The gates are computed twice: what a step needs
 // of them across the wait, held in registers, would cost the second workgroup of a CU.
-template <bool BF16, int V, bool ONCE, int FORM, bool GATE>
+template <bool BF16, int V, int PAST, int FORM, bool GATE>
 __global__ void __launch_bounds__(kThreads, 4) glr_bwd_tiles(GlrBwdArgs a, Cut c) {
     constexpr int T = Share<V>::T;
     __shared__ float ownP[kWaves][64], ownH[kWaves][64], ownC[kWaves][64];
@@ -372,11 +379,11 @@ __global__ void __launch_bounds__(kThreads, 4) glr_bwd_tiles(GlrBwdArgs a, Cut c
     const bool mine = me.d < in.D;
     Raw<BF16, V> x[T], r[T], i[T], dy[T], z[T];
     float ca[T][V], cu[T][V], A[V], P[V], H[V], C[V];
-    Rows<BF16, V, ONCE>(in.x, in.ldx, in.D, at.first, at.wave_live, me).load(x);
-    Rows<BF16, V, ONCE>(in.r, in.ldr, in.D, at.first, at.wave_live, me).load(r);
-    if constexpr (FORM == 0) Rows<BF16, V, ONCE>(in.i, in.ldi, in.D, at.first, at.wave_live, me).load(i);
-    Rows<BF16, V, ONCE>(a.dy, in.D, in.D, at.first, at.wave_live, me).load(dy);
-    if constexpr (GATE) Rows<BF16, V, ONCE>(in.z, in.ldz, in.D, at.first, at.wave_live, me).load(z);
+    Rows<BF16, V, PAST>(in.x, in.ldx, in.D, at.first, at.wave_live, me).load(x);
+    Rows<BF16, V, PAST>(in.r, in.ldr, in.D, at.first, at.wave_live, me).load(r);
+    if constexpr (FORM == 0) Rows<BF16, V, PAST>(in.i, in.ldi, in.D, at.first, at.wave_live, me).load(i);
+    Rows<BF16, V, PAST>(a.dy, in.D, in.D, at.first, at.wave_live, me).load(dy);
+    if constexpr (GATE) Rows<BF16, V, PAST>(in.z, in.ldz, in.D, at.first, at.wave_live, me).load(z);
 #pragma unroll
     for (int v = 0; v < V; ++v) A[v] = FORM == 0 ? in.A[min(me.d + v, in.D - 1)] : 0.0f;
 #pragma unroll
@@ -454,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 4) glr_bwd_tiles(GlrBwdArgs a, Cut c
         for (int q = 0; q < w; ++q) h[v] = __builtin_fmaf(ownP[q][ch + v], h[v], ownH[q][ch + v]);
         if constexpr (V == 2) h[v] = me.late ? __builtin_fmaf(Po[v], h[v], Ho[v]) : h[v];
     }
-    const Rows<BF16, V, ONCE> oz(GATE ? a.dz : a.dx, in.D, in.D, at.first, at.wave_stored, me);
+    const Rows<BF16, V, PAST> oz(GATE ? a.dz : a.dx, in.D, in.D, at.first, at.wave_stored, me);
 #pragma unroll
     for (int t = 0; t < T; ++t) {
         float dz[V];
@@ -490,8 +497,8 @@ __global__ void __launch_bounds__(kThreads, 4) glr_bwd_tiles(GlrBwdArgs a, Cut c
             __hip_atomic_store(c.ends + ((size_t)b * c.groups + group) * in.D + me.d + v,
                                present(__builtin_fmaf(P[v], g[v], C[v])), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
-    const Rows<BF16, V, ONCE> ox(a.dx, in.D, in.D, at.first, at.wave_stored, me), orr(a.dr, in.D, in.D, at.first, at.wave_stored, me);
-    const Rows<BF16, V, ONCE> oi(FORM == 0 ? a.di : a.dx, in.D, in.D, at.first, at.wave_stored, me);
+    const Rows<BF16, V, PAST> ox(a.dx, in.D, in.D, at.first, at.wave_stored, me), orr(a.dr, in.D, in.D, at.first, at.wave_stored, me);
+    const Rows<BF16, V, PAST> oi(FORM == 0 ? a.di : a.dx, in.D, in.D, at.first, at.wave_stored, me);
 #pragma unroll
     for (int t = 0; t < T; ++t) {
         x[t].anew();
@@ -603,27 +610,41 @@ bool pairs(const GlrIn& in) {
     return true;
 }
 
-template <bool BF16, int V, bool ONCE>
+// PAST of a call with pairs: tensors, as many as bytes() is to count, and where its outputs start.
+int past(const GlrIn& in, int tensors, std::initializer_list<const void*> outputs) {
+    const auto starts = [](const void* p, int at) { return reinterpret_cast<uintptr_t>(p) % at == 0; };
+    if (in.D * 2 % kPiece != 0) return 0;
+    for (const void* p : outputs)
+        if (!starts(p, kPiece)) return 0;
+    if (bytes(in, tensors) <= kCached || in.D * 2 % kLine != 0) return 1;
+    const void* p[] = {in.x, in.r, in.i, in.z};
+    const int stride[] = {in.ldx, in.ldr, in.ldi, in.ldz};
+    for (int k = 0; k < 4; ++k)
+        if (p[k] && (!starts(p[k], kLine) || stride[k] % (kLine / 2) != 0)) return 1;
+    return 2;
+}
+
+template <bool BF16, int V, int PAST>
 void fwd(const GlrArgs& a, const Cut& c, hipStream_t s) {
     const dim3 grid = fold((long long)c.chains * c.tiles), block(kThreads);
     if (a.in.form == 0) {
-        if (a.in.z) launch((glr_fwd_tiles<BF16, V, ONCE, 0, true>), grid, block, 0, s, a, c);
-        else launch((glr_fwd_tiles<BF16, V, ONCE, 0, false>), grid, block, 0, s, a, c);
+        if (a.in.z) launch((glr_fwd_tiles<BF16, V, PAST, 0, true>), grid, block, 0, s, a, c);
+        else launch((glr_fwd_tiles<BF16, V, PAST, 0, false>), grid, block, 0, s, a, c);
     } else {
-        if (a.in.z) launch((glr_fwd_tiles<BF16, V, ONCE, 1, true>), grid, block, 0, s, a, c);
-        else launch((glr_fwd_tiles<BF16, V, ONCE, 1, false>), grid, block, 0, s, a, c);
+        if (a.in.z) launch((glr_fwd_tiles<BF16, V, PAST, 1, true>), grid, block, 0, s, a, c);
+        else launch((glr_fwd_tiles<BF16, V, PAST, 1, false>), grid, block, 0, s, a, c);
     }
 }
 
-template <bool BF16, int V, bool ONCE>
+template <bool BF16, int V, int PAST>
 void bwd(const GlrBwdArgs& a, const Cut& c, hipStream_t s) {
     const dim3 grid = fold((long long)c.chains * c.tiles), block(kThreads);
     if (a.in.form == 0) {
-        if (a.in.z) launch((glr_bwd_tiles<BF16, V, ONCE, 0, true>), grid, block, 0, s, a, c);
-        else launch((glr_bwd_tiles<BF16, V, ONCE, 0, false>), grid, block, 0, s, a, c);
+        if (a.in.z) launch((glr_bwd_tiles<BF16, V, PAST, 0, true>), grid, block, 0, s, a, c);
+        else launch((glr_bwd_tiles<BF16, V, PAST, 0, false>), grid, block, 0, s, a, c);
     } else {
-        if (a.in.z) launch((glr_bwd_tiles<BF16, V, ONCE, 1, true>), grid, block, 0, s, a, c);
-        else launch((glr_bwd_tiles<BF16, V, ONCE, 1, false>), grid, block, 0, s, a, c);
+        if (a.in.z) launch((glr_bwd_tiles<BF16, V, PAST, 1, true>), grid, block, 0, s, a, c);
+        else launch((glr_bwd_tiles<BF16, V, PAST, 1, false>), grid, block, 0, s, a, c);
     }
 }
 
@@ -646,10 +667,12 @@ hipError_t launch_glr_fwd(const GlrArgs& a, hipStream_t s) {
     const Cut c = cut_of(a.in.B, a.in.L, a.in.D, static_cast<char*>(a.ws), &fill);
     const hipError_t e = fill_words(a.ws, fill, s);
     if (e != hipSuccess) return e;
-    if (!a.in.bf16) fwd<false, 1, false>(a, c, s);
-    else if (!pairs(a.in)) fwd<true, 1, false>(a, c, s);
-    else if (bytes(a.in, 3 + (a.in.i != nullptr) + (a.in.z != nullptr)) <= kCached) fwd<true, 2, false>(a, c, s);
-    else fwd<true, 2, true>(a, c, s);
+    const int far = past(a.in, 3 + (a.in.i != nullptr) + (a.in.z != nullptr), {a.y});
+    if (!a.in.bf16) fwd<false, 1, 0>(a, c, s);
+    else if (!pairs(a.in)) fwd<true, 1, 0>(a, c, s);
+    else if (far == 0) fwd<true, 2, 0>(a, c, s);
+    else if (far == 1) fwd<true, 2, 1>(a, c, s);
+    else fwd<true, 2, 2>(a, c, s);
     return hipGetLastError();
 }
 
@@ -660,10 +683,12 @@ hipError_t launch_glr_bwd(const GlrBwdArgs& a, hipStream_t s) {
     if (parts == 1) c.part = a.dA;  // the whole sum
     hipError_t e = fill_words(a.ws, fill, s);
     if (e != hipSuccess) return e;
-    if (!a.in.bf16) bwd<false, 1, false>(a, c, s);
-    else if (!pairs(a.in)) bwd<true, 1, false>(a, c, s);
-    else if (bytes(a.in, 5 + 2 * (a.in.i != nullptr) + 2 * (a.in.z != nullptr)) <= kCached) bwd<true, 2, false>(a, c, s);
-    else bwd<true, 2, true>(a, c, s);
+    const int far = past(a.in, 5 + 2 * (a.in.i != nullptr) + 2 * (a.in.z != nullptr), {a.dx, a.dr, a.di, a.dz});
+    if (!a.in.bf16) bwd<false, 1, 0>(a, c, s);
+    else if (!pairs(a.in)) bwd<true, 1, 0>(a, c, s);
+    else if (far == 0) bwd<true, 2, 0>(a, c, s);
+    else if (far == 1) bwd<true, 2, 1>(a, c, s);
+    else bwd<true, 2, 2>(a, c, s);
     if ((e = hipGetLastError()) != hipSuccess || a.in.form != 0 || parts == 1) return e;
     launch(glr_sum_parts, dim3((unsigned)((a.in.D + 15) / 16)), dim3(256), 0, s, c.part, parts, a.in.D, a.dA);
     return hipGetLastError();

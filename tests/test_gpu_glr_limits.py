@@ -173,3 +173,37 @@ def test_gates_whose_sigmoid_is_just_above_the_smallest_number():
     dz = ssa.ssm_glr_bwd(big["x"], big["r"], states, d["dy"], big["i"], big["A"], big["z"])["dz"]
     want = h[0].double().cpu() * s * (1 + v.double())
     assert float((dz[0, 0].double().cpu() / want - 1).abs().max()) < 2.0 ** -14
+
+
+@pytest.mark.parametrize("form,gate", [("decay", True), ("convex", False)])
+def test_whole_lines_past_the_caches(form, gate):
+    """More than 256 MiB in a call, strips of whole lines: a few channels against 64 bits. Outputs that
+    start off a piece of 64 bytes, inputs off a line of 128, fewer tokens: other accesses, the same bits."""
+    B, L, D = 2, 16500, 1536
+    t = ref.glr_inputs(B, L, D, BF16, form, seed=15, gate=gate)
+    d = base.to(t)
+    y, h, states = base.fwd(d, form)
+    out = base.bwd(d, states, form)
+    torch.cuda.synchronize()
+    pick = torch.tensor([0, 1, 62, 63, 64, 700, 1471, 1472, 1534, 1535])
+    few = {n: None if v is None else v[..., pick].contiguous() for n, v in t.items()}
+    g = ref.Glr(few, form, None, few["dy"], few["dh_final"])
+    ref.close(y[..., pick.to(DEV)], g.y, g.ey, 1.0, "y", store=BF16)
+    ref.close(h[..., pick.to(DEV)], g.h_final, g.eh_final, 1.0, "h_final", store=F32)
+    for n, (v, e) in g.out.items():
+        ref.close(out[n][..., pick.to(DEV)], v, e, 1.0, n, store=F32 if n in ("dA", "dh0") else BF16)
+
+    def at(v, first):
+        return torch.empty(v.numel() + 64, dtype=v.dtype, device=DEV)[first:first + v.numel()].view(v.shape)
+
+    names = [n for n in ("dx", "dr", "di", "dz") if out[n] is not None]
+    y2 = base.fwd(d, form, y=at(y, 8))[0]
+    out2 = base.bwd(d, states, form, out={n: at(out[n], 8) for n in names})
+    e = dict(d, x=at(d["x"], 32).copy_(d["x"]))
+    y3 = base.fwd(e, form)[0]
+    out3 = base.bwd(e, states, form)
+    torch.cuda.synchronize()
+    assert torch.equal(y, y2) and torch.equal(y, y3)
+    assert all(out[n] is None or (torch.equal(out[n], out2[n]) and torch.equal(out[n], out3[n])) for n in out)
+    short = {n: v[:, :300].contiguous() if v is not None and v.dim() == 3 else v for n, v in d.items()}
+    assert torch.equal(base.fwd(short, form)[0], y[:, :300])
