@@ -599,8 +599,15 @@ int ssm_group_norm_bwd(int M, int S, int C, int G, ssm_dtype_t io, ssm_act_t act
  *   states     : [B, ceil(L / SSM_GLR_STATE_STEPS), D] fp32 out, or NULL: the state entering
  *                every SSM_GLR_STATE_STEPS-th step, which ssm_glr_bwd takes
  *   workspace  : at least ssm_glr_workspace_size(B, L, D) bytes, for one call at a time
- * Arithmetic: fp32; 1 - a^2 by a series where a is close to 1.
+ * Arithmetic: fp32; 1 - a^2 by a series where a is close to 1. Order of the sums: fixed by the
+ * sizes, io and whether x, r, i and z hold whole pairs of bf16 (D, every row stride and every
+ * address in elements even). Calls alike in that give the same bits; a slice at an odd channel
+ * gives those of another order.
  * A value that is not finite stays in its channel and sequence, from its own step on.
+ * A sequence is one: its state is not reset inside (documents packed into one row need a call
+ * each, or rows of a padded batch), and its first step is scaled by sqrt(1 - a^2) as the others.
+ * Tiles of a sequence wait for one another within the launch. A wait that took some seconds would
+ * give up: what depends on it becomes NaN (the call has returned and reports no status).
  * Supported: B <= 65535; L <= 2^30; D <= 2^18; ld in [D, 2^24]; B ceil(L / 128) ceil(D / 64)
  * <= 2^30. x, r, i and z must be aligned to their element, every other pointer to 16 bytes.
  * Outputs must not alias inputs or each other (the same address is refused). Errors as for
@@ -638,8 +645,8 @@ int ssm_glr_fwd(int B, int L, int D, ssm_dtype_t io, ssm_glr_form_t form,
  *   dA         : [D]        fp32 out; given exactly when A is
  *   dh0        : [B, D]     fp32 out, or NULL (not written)
  *   workspace  : at least ssm_glr_bwd_workspace_size(B, L, D) bytes, for one call at a time
- * Sums over b and t run in a fixed order. Sizes, alignment, aliasing and errors as for
- * ssm_glr_fwd. L = 0 writes dh0 = dh_final and dA = 0.
+ * Sums over b and t run in a fixed order; orders and waits as for ssm_glr_fwd, and so are sizes,
+ * alignment, aliasing and errors. L = 0 writes dh0 = dh_final and dA = 0.
  * ------------------------------------------------------------------------- */
 size_t ssm_glr_bwd_workspace_size(int B, int L, int D);
 

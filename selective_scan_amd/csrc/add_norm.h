@@ -63,7 +63,7 @@ hipError_t launch_dropout(const DropoutArgs& a, hipStream_t stream);
 // Philox-4x32-10 (Salmon, Moraes, Dror, Shaw: Parallel random numbers: as easy as 1, 2, 3;
 // 2011): the four words of a block number under a seed. Eight channels of a row share a
 // block, 16 bits each: the keep probability is then a multiple of 2^-16, which the scale
-// takes exactly, and a value costs a quarter of a word-sized draw's multiplications.
+// takes exactly, and a value costs half of a word-sized draw's multiplications.
 struct Philox {
     uint32_t w[4];
     __device__ __forceinline__ Philox(unsigned long long seed, unsigned long long block) {

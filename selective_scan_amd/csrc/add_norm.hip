@@ -3,7 +3,8 @@
 //   ds = rstd (dn - mean(dn) - xhat mean(dn xhat)) + dsum,  dn = dy w   (rms: no mean(dn))
 //   dresidual = ds,  dx = dropout(ds),  dw = sum dy xhat,  db = sum dy
 //
-// Bandwidth-bound: every row is read and written once, in registers in between. A lane has eight
+// Bandwidth-bound: every row is read and written once, in registers in between (but for the
+// gradient beyond 8192 channels, below). A lane has eight
 // neighbouring channels (an octet: the generator's block, and one or two 16-byte accesses); a row
 // takes 16 lanes (C <= 128), a wave (C <= 512) or a workgroup of as many waves as its octets
 // fill, one octet a lane, two beyond 8192 channels. Workgroups walk rows, so that a lane reads
@@ -13,12 +14,20 @@
 // a 16-byte border (odd widths) are loaded as they lie; the last one of a row is taken value by
 // value where it is not whole.
 // Statistics and sums are fp32, the variance from squared distances to the mean.
-// Measured: 32768 x 1536 bf16 on an fp32 stream with dropout 115 us (604 MB, 5.2 TB/s, a copy's
-// rate), its gradient 152 us (805 MB, 5.3 TB/s), gradient of 4099 x 1001 fp32 23 us (82 MB, partly
+// Measured: 32768 x 1536 bf16 on an fp32 stream with dropout 115 us (604 MB, 5.3 TB/s, a copy's
+// rate), its gradient 153 us (805 MB, 5.3 TB/s), gradient of 4099 x 1001 fp32 23 us (82 MB, partly
 // in the memory-side cache; a second launch that sums the parts takes 4), 64 x 2048 3.2 us (the
-// call's host side 11), dropout alone of 32768 x 1536 bf16 33 us (201 MB; 6.2 TB/s, partly in the
-// cache). 12 waves a CU walk the rows: 18 or 24 of the forward's were slower (122, 124 us), in the
-// gradient 6 (186) and 15 (161); workgroups that do not all fit at once cost a quarter (201).
+// call's host side 10), dropout alone of 32768 x 1536 bf16 33 us (201 MB; 6.2 TB/s, partly in the
+// cache). 12 waves a CU walk the rows: 18 or 24 of the forward's were slower at 32768 x 1536 (122,
+// 124 us), in the gradient 6 (186) and 15 (161); workgroups that do not all fit at once cost a
+// quarter (201). Other widths, bf16 on fp32 without dropout: 65536 x 256, 520 and 768 and 8192 x
+// 4096 to 5120 take 42, 94, 121 and 83 to 97 us (4.4 to 5.2 TB/s), their gradients 56, 115, 151 and
+// 119 to 138; rows that leave lanes idle run at that share of it (65536 x 32 10 and 18 us, 65536 x
+// 136 33 and 49: 1.9 to 3.3 TB/s).
+// In the gradient with two octets a lane registers do not hold a row: 22 (fp32) or 19 (bf16 on
+// fp32) of them go to scratch beyond 8192 channels, 43 to 106 beyond 12288, and counters show that
+// traffic in memory: 4096 x 10000 fp32 252 us (3.2 TB/s of what has to move; 1.3 times that moved),
+// 2048 x 16384 318 us (2.1 TB/s; 2.3 times).
 #include "add_norm.h"
 #include "common.h"
 #include "launch.h"

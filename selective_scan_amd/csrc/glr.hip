@@ -10,17 +10,24 @@
 // waves through LDS, of the tiles of a sequence through memory, from workgroup to workgroup of
 // the same launch. A tile leaves its map, then needs the maps of the tiles before it: those of its
 // group of 32 tiles, fetched by the eight waves in parallel, and the state at the group's start,
-// which the group before leaves. The order of all operations is fixed by the shape, so results
-// repeat bit for bit.
+// which the group before leaves (a chained scan with look-back). The order of all operations is
+// fixed by the shape, the type and whether x, r, i and z hold whole pairs of bf16 (two channels a
+// lane, or one), so the same call gives the same bits.
 // Measured (with the launch that fills the words, and for the gradient the one that sums dA):
 // B8 L32768 D512 bf16 233 us (1.07 GB that have to move, 4.6 TB/s; a copy of that size reaches 4.9
 // to 5.1), B1 L4096 D1536 with gate 17.4 us (3 of them the fill), gradient of B4 L4096 D1536 with
 // gate 119 us (453 MB, 3.8 TB/s: two workgroups a CU, whose loads, waits and stores take turns;
-// counters show no byte moved twice), of B3 L2047 D1001 fp32 convex 30 us. Waiting costs nothing
-// that shows (a copy that does not wait takes as long); with one XCD of eight slower by 12 % the
-// others end that much earlier. Half as many or twice as many steps, wider strips, workgroups that
-// take tile after tile and maps looked at ahead of time were all slower, for the registers they
-// take or the lanes that wait.
+// counters show no byte moved twice), of B3 L<=2047 D1001 fp32 convex, padded, 31 to 36 us by the
+// lengths. Waiting costs nothing that shows (a copy that does not wait takes as long); with one XCD
+// of eight slower by 12 % the others end that much earlier. Half as many or twice as many steps,
+// wider strips, workgroups that take tile after tile and maps looked at ahead of time were all
+// slower, for the registers they take or the lanes that wait.
+// Where strips share lines, neighbours run on different XCDs and each fetches the line: B4 L4096
+// D1502 bf16 reads 2.0 times its bytes (gradient 169 us, whole lines at D1536 127), D1001 fp32 1.5
+// (gradient 1.6). The gradient of the decay form with gate takes 114 registers with pairs; with
+// single channels 128 and 6 of them in scratch (B4 L2048 D2048 fp32 144 us, 4.2 TB/s). A sequence
+// shorter than a tile leaves waves without steps: B256 D1536 bf16 with gate takes 67 us at L = 1 and
+// at L = 16 alike (its gradient 159), B64 L64 D2560 33 (81).
 //
 // Waiting on other workgroups: a workgroup takes the next tile of its sequence from a counter, so
 // that the tiles it waits for belong to workgroups that run already, and the first unfinished
